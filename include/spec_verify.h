@@ -358,4 +358,7 @@ int spec_version(void);
 }
 #endif
 
+/* The paged cache, the attention over it and the recurrence of the forward. */
+#include "spec_forward.h"
+
 #endif /* SPEC_VERIFY_H */

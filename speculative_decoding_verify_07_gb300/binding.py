@@ -8,6 +8,7 @@ not been built (see ``speculative_decoding_verify_07_gb300.build``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -17,6 +18,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "lib
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_E4M3 = 2
 
 SPEC_OK = 0
 SPEC_E_NULL = -1
@@ -39,6 +41,14 @@ F_TIMEOUT = 256
 
 SPEC_MAX_V = 524288
 SPEC_MAX_K = 16
+
+
+class CacheView(ctypes.Structure):
+    """spec_cache_t of include/spec_forward.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_exp", "v_exp", "page_table", "cu_tokens",
+                                                "kv_len")]
+                + [(n, ctypes.c_int64) for n in ("page_stride", "exp_stride")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "B", "max_pages", "pages", "heads", "page_size", "head_dim")])
 
 
 class SpecError(RuntimeError):
@@ -72,6 +82,23 @@ def _load():
     lib.spec_draft_workspace_size.restype = sz
     lib.spec_draft_sample.argtypes = [vp, i32, vp, u64, u32, u32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.spec_draft_sample.restype = i32
+    i64, cache = ctypes.c_int64, ctypes.POINTER(CacheView)
+    lib.spec_cache_write.argtypes = [vp, vp, i32, i64, i32, cache, vp, vp]
+    lib.spec_cache_write.restype = i32
+    lib.spec_cache_read.argtypes = [vp, vp, i32, cache, vp, vp]
+    lib.spec_cache_read.restype = i32
+    lib.spec_attend_workspace_size.argtypes = [i32, i32, i32]
+    lib.spec_attend_workspace_size.restype = sz
+    lib.spec_attend.argtypes = [vp, i64, i32, i32, ctypes.c_float, i32, cache, vp, vp, vp, vp, sz, vp]
+    lib.spec_attend.restype = i32
+    lib.spec_recur_workspace_size.argtypes = [i32, i32, i32]
+    lib.spec_recur_workspace_size.restype = sz
+    lib.spec_recur.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, vp, i32, vp, i32, i32, i32, vp, i32, vp, vp, i32,
+                               vp, vp, sz, vp]
+    lib.spec_recur.restype = i32
+    lib.spec_recur_backward.argtypes = [vp, i64, i64, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp,
+                                        vp, vp, sz, vp]
+    lib.spec_recur_backward.restype = i32
     lib.spec_philox4x32_10.argtypes = [vp, u64, vp, ctypes.c_int64, vp]
     lib.spec_philox4x32_10.restype = i32
     lib.spec_status_string.argtypes = [i32]
@@ -452,3 +479,276 @@ def philox4x32_10(ctr: torch.Tensor, seed: int, stream=None) -> torch.Tensor:
     if rc != SPEC_OK:
         raise SpecError(rc, "spec_philox4x32_10")
     return out
+
+
+# The forward's sequence mixers (include/spec_forward.h).
+
+_POOL_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
+_IO_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+
+
+def _io_dtype(t, name):
+    dt = _IO_DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return dt
+
+
+def _page_stride(a, b, names, per_page):
+    """Elements from page to page of two pools whose pages are dense inside."""
+    strides = []
+    for t, name in zip((a, b), names):
+        inner = 1
+        for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            if size != 1 and stride != inner:
+                raise ValueError(f"{name} must be dense within a page")
+            inner *= size
+        strides.append(t.stride(0) if t.shape[0] > 1 else per_page)
+    if a.shape[0] > 1 and strides[0] != strides[1]:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same page stride")
+    if strides[0] < per_page:
+        raise ValueError(f"{names[0]} has overlapping pages")
+    return strides[0]
+
+
+def _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp):
+    """spec_cache_t of a batch's tensors, checked.  The struct holds raw
+    pointers: the tensors outlive the call that it is made for."""
+    dt = _POOL_DTYPES.get(k_pages.dtype)
+    if dt is None:
+        raise TypeError("the cache must be bfloat16 or float8_e4m3fn")
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [pages, heads, page_size, head_dim]")
+    pages, heads, page_size, dim = k_pages.shape
+    dev = k_pages.device
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != dev:
+        raise ValueError("v_pages must be like k_pages")
+    if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1 or page_table.dim() != 2:
+        raise ValueError("cu_tokens must be [B + 1] and page_table [B, max_pages]")
+    B, max_pages = page_table.shape
+    _check(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    _check(kv_len, "kv_len", torch.int32, (B,), dev)
+    _check(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    exp_stride = 0
+    if dt == SPEC_E4M3:
+        for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            if t is None:
+                raise ValueError(f"an e4m3 cache needs {name}")
+            if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != (pages, heads, page_size):
+                raise ValueError(f"{name} must be uint8 [pages, heads, page_size] on {dev}")
+        exp_stride = _page_stride(k_exp, v_exp, ("k_exp", "v_exp"), heads * page_size)
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("a bfloat16 cache has no exponents")
+    return CacheView(k_pages.data_ptr(), v_pages.data_ptr(), None if k_exp is None else k_exp.data_ptr(),
+                     None if v_exp is None else v_exp.data_ptr(), page_table.data_ptr(), cu_tokens.data_ptr(),
+                     kv_len.data_ptr(), _page_stride(k_pages, v_pages, ("k_pages", "v_pages"), heads * page_size * dim),
+                     exp_stride, dt, B, max_pages, pages, heads, page_size, dim)
+
+
+def _token_stride(t, name):
+    """Elements from token to token of [N, heads, dim] with dense tokens."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, heads, head_dim]")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be dense within a token")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _flags_ok(flags, B, dev):
+    if flags is not None:
+        _check(flags, "flags", torch.int32, (B,), dev)
+
+
+def _on(stream):
+    """What a call allocates for itself is allocated (and cleared) on the stream that it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _done(rc, what):
+    if rc != SPEC_OK:
+        raise SpecError(rc, what)
+
+
+def spec_cache_write(k, v, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, flags=None,
+                     stream=None):
+    """Put new tokens' keys and values into the paged cache (see spec_cache_write
+    in spec_forward.h).
+
+    k, v [N, heads, head_dim] float32 or bfloat16 (tokens may be strided);
+    cu_tokens [B + 1], kv_len [B], page_table [B, max_pages] int32; k_pages,
+    v_pages [pages, heads, page_size, head_dim] bfloat16 or float8_e4m3fn, the
+    latter with k_exp, v_exp [pages, heads, page_size] uint8; flags [B] int32.
+    """
+    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
+    dt, stride, shape = _io_dtype(k, "k"), _token_stride(k, "k"), (k.shape[0], view.heads, view.head_dim)
+    if tuple(k.shape) != shape or k.device != k_pages.device:
+        raise ValueError(f"k must be {shape} on {k_pages.device}")
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or _token_stride(v, "v") != stride:
+        raise ValueError("v must be like k")
+    _flags_ok(flags, view.B, k.device)
+    _done(LIB.spec_cache_write(k.data_ptr(), v.data_ptr(), dt, stride, shape[0], view, _ptr(flags), _stream(stream)),
+          "spec_cache_write")
+
+
+def spec_cache_read(tokens, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, k=None, v=None,
+                    flags=None, stream=None):
+    """Read `tokens` = cu_tokens[B] packed tokens back as bfloat16 (see
+    spec_cache_read in spec_forward.h); returns (k, v), each [tokens, heads,
+    head_dim]."""
+    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
+    shape, dev = (int(tokens), view.heads, view.head_dim), k_pages.device
+    with _on(stream):
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _check(k, "k", torch.bfloat16, shape, dev)
+    _check(v, "v", torch.bfloat16, shape, dev)
+    _flags_ok(flags, view.B, dev)
+    _done(LIB.spec_cache_read(k.data_ptr(), v.data_ptr(), shape[0], view, _ptr(flags), _stream(stream)), "spec_cache_read")
+    return k, v
+
+
+def new_attend_workspace(heads: int, group: int, head_dim: int, device) -> torch.Tensor:
+    """A zero-filled workspace for spec_attend: any batch of a cache of `heads`
+    heads of head_dim, each read by `group` query heads; one stream."""
+    n = int(LIB.spec_attend_workspace_size(int(heads), int(group), int(head_dim)))
+    if n == 0:
+        raise ValueError(f"spec_attend takes no {heads} heads of {head_dim} read by {group}")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, *, max_tokens, scale=None,
+                out=None, lse=None, flags=None, workspace=None, stream=None):
+    """Causal attention of each row's new tokens over its paged cache (see
+    spec_attend in spec_forward.h); the cache as for spec_cache_write, which
+    has put the new tokens in.
+
+    q [N, heads * group, head_dim] bfloat16 (tokens may be strided); scale
+    defaults to head_dim ** -0.5; max_tokens is the largest number of new
+    tokens of a row.  Returns (out [N, heads * group, head_dim] bfloat16,
+    lse [N, heads * group] float32).
+    """
+    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
+    stride, dev = _token_stride(q, "q"), k_pages.device
+    N, hq, dim = q.shape
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if dim != view.head_dim or hq % view.heads or q.device != dev:
+        raise ValueError(f"q must be [N, a multiple of {view.heads}, {view.head_dim}] on {dev}")
+    group = hq // view.heads
+    with _on(stream):
+        if out is None:
+            out = torch.empty((N, hq, dim), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((N, hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = new_attend_workspace(view.heads, group, dim, dev)
+    _check(out, "out", torch.bfloat16, (N, hq, dim), dev)
+    _check(lse, "lse", torch.float32, (N, hq), dev)
+    _flags_ok(flags, view.B, dev)
+    _done(LIB.spec_attend(q.data_ptr(), stride, N, group, dim ** -0.5 if scale is None else scale, int(max_tokens), view,
+                          out.data_ptr(), lse.data_ptr(), _ptr(flags), workspace.data_ptr(), workspace.numel(),
+                          _stream(stream)), "spec_attend")
+    return out, lse
+
+
+def recur_workspace_size(B: int, T: int, D: int) -> int:
+    return int(LIB.spec_recur_workspace_size(int(B), int(T), int(D)))
+
+
+def new_recur_workspace(B: int, T: int, D: int, device) -> torch.Tensor:
+    """A zero-filled workspace for spec_recur and spec_recur_backward."""
+    return torch.zeros(max(recur_workspace_size(B, T, D), 256), dtype=torch.uint8, device=device)
+
+
+def _recur_strides(t, name, shape, dtype, dev):
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {shape} on {dev}")
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have dense channels")
+    return t.stride(0), t.stride(1)
+
+
+def _recur_state(state, slot, lens, B, D, dev):
+    slots = 0
+    if state is not None:
+        if state.dim() != 2:
+            raise ValueError("state must be [slots, D]")
+        slots = state.shape[0]
+        _check(state, "state", torch.float32, (slots, D), dev)
+    if slot is not None:
+        _check(slot, "slot", torch.int32, (B,), dev)
+    if lens is not None:
+        _check(lens, "lens", torch.int32, (B,), dev)
+    return slots
+
+
+def spec_recur(g, x, state=None, slot=None, lens=None, *, h=None, h_dtype=torch.float32, last=None, last_slot=None,
+               flags=None, workspace=None, stream=None):
+    """h_t = exp(g_t) h_{t-1} + x_t (see spec_recur in spec_forward.h).
+
+    g, x [B, T, D] float32 or bfloat16 (rows and tokens may be strided); state
+    [slots, D] float32, slot [B], lens [B] int32, each or None.  Returns (h
+    [B, T, D] of h_dtype, last).  last [B, D] float32 is made where None is
+    given; last=state, last_slot=slot updates a cache in place.
+    """
+    if g.dim() != 3:
+        raise ValueError("g must be [B, T, D]")
+    B, T, D = shape = tuple(g.shape)
+    dev, dt = g.device, _io_dtype(g, "g")
+    g_row, g_tok = _recur_strides(g, "g", shape, g.dtype, dev)
+    x_row, x_tok = _recur_strides(x, "x", shape, g.dtype, dev)
+    slots = _recur_state(state, slot, lens, B, D, dev)
+    with _on(stream):
+        if h is None:
+            h = torch.empty(shape, dtype=h_dtype, device=dev)
+        if last is None:
+            last = torch.empty((B, D), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = new_recur_workspace(B, T, D, dev)
+    _check(h, "h", h.dtype, shape, dev)
+    _check(last, "last", torch.float32, (last.shape[0], D), dev)
+    if last_slot is not None:
+        _check(last_slot, "last_slot", torch.int32, (B,), dev)
+    _flags_ok(flags, B, dev)
+    _done(LIB.spec_recur(g.data_ptr(), g_row, g_tok, x.data_ptr(), x_row, x_tok, dt, _ptr(state), _ptr(slot), slots,
+                         _ptr(lens), B, T, D, h.data_ptr(), _io_dtype(h, "h"), last.data_ptr(), _ptr(last_slot),
+                         last.shape[0], _ptr(flags), workspace.data_ptr(), workspace.numel(), _stream(stream)), "spec_recur")
+    return h, last
+
+
+def spec_recur_backward(g, h, dh, state=None, slot=None, lens=None, d_last=None, *, dg=None, dx=None, d_state=None,
+                        flags=None, workspace=None, stream=None):
+    """The gradients of spec_recur (see spec_recur_backward in spec_forward.h):
+    g, state, slot, lens as given to it, h as it wrote it, dh [B, T, D] of g's
+    dtype, d_last [B, D] float32 or None.  Returns (dg, dx, d_state)."""
+    if g.dim() != 3:
+        raise ValueError("g must be [B, T, D]")
+    B, T, D = shape = tuple(g.shape)
+    dev, dt = g.device, _io_dtype(g, "g")
+    g_row, g_tok = _recur_strides(g, "g", shape, g.dtype, dev)
+    _check(dh, "dh", g.dtype, shape, dev)
+    _check(h, "h", h.dtype, shape, dev)
+    slots = _recur_state(state, slot, lens, B, D, dev)
+    if d_last is not None:
+        _check(d_last, "d_last", torch.float32, (B, D), dev)
+    with _on(stream):
+        if dg is None:
+            dg = torch.empty(shape, dtype=g.dtype, device=dev)
+        if dx is None:
+            dx = torch.empty(shape, dtype=g.dtype, device=dev)
+        if d_state is None:
+            d_state = torch.empty((B, D), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = new_recur_workspace(B, T, D, dev)
+    _check(dg, "dg", g.dtype, shape, dev)
+    _check(dx, "dx", g.dtype, shape, dev)
+    _check(d_state, "d_state", torch.float32, (B, D), dev)
+    _flags_ok(flags, B, dev)
+    _done(LIB.spec_recur_backward(g.data_ptr(), g_row, g_tok, h.data_ptr(), _io_dtype(h, "h"), dh.data_ptr(), _ptr(d_last),
+                                  dt, _ptr(state), _ptr(slot), slots, _ptr(lens), B, T, D, dg.data_ptr(), dx.data_ptr(),
+                                  d_state.data_ptr(), _ptr(flags), workspace.data_ptr(), workspace.numel(),
+                                  _stream(stream)), "spec_recur_backward")
+    return dg, dx, d_state

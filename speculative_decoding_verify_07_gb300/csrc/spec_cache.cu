@@ -1,0 +1,275 @@
+// spec_cache_write and spec_cache_read: a token's keys and values into the
+// paged cache, in 16 bits or quantised to 8, and back.
+//
+// A lane holds 8 consecutive elements of one head's vector, so D / 8 lanes
+// hold the vector, a few shuffles find its largest magnitude, and the source
+// is read once in 16-byte loads.  The scale is a power of two, 2^s with
+// max|x| <= 448 * 2^s: x * 2^-s and c * 2^s are then exact, the one rounding
+// is that to e4m3 (relative 2^-4, the same at every magnitude above 2^-6 of
+// the code range, so the finest scale would gain nothing but sub-normal
+// range), and what is read back is exact in bf16.  One exponent byte a
+// vector costs 1/128 of an 8-bit cache.
+//
+// Both kernels are bound by memory (3 bytes an element for bf16 to e4m3).
+// A CTA takes a run of (token, key or value, head, lane) items in the order
+// of the packed array; the tokens' places in the cache are looked up once a
+// CTA, into shared memory, while the loads of the items are in flight.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/spec_verify.h"
+#include "spec_host.h"
+#include "spec_paged.cuh"
+
+namespace specv {
+
+constexpr int kCacheThreads = 256;
+
+struct CacheIO {
+  PagedCache C;
+  unsigned char* kv[2];      // packed keys and values
+  long long token_bytes;     // from one token to the next
+  long long items;           // N * 2 * heads * (D / 8)
+  int N;
+  uint32_t* flags;
+};
+
+// Where the run of items starting at `first` finds its tokens: the byte offset
+// of each token's page and slot, in shared memory; -1 where there is none.
+struct TokenPlace {
+  long long page;   // page index, or -1
+  int slot;
+  int row;
+};
+
+// `bad`: flag the row of a token without a place.
+__device__ __forceinline__ TokenPlace find_place(const CacheIO& A, int token) {
+  TokenPlace t;
+  t.page = -1;
+  t.slot = 0;
+  t.row = paged_row(A.C, token);
+  if (t.row < 0) return t;
+  const int end = __ldg(A.C.cu + t.row + 1);
+  const int pos = __ldg(A.C.kv_len + t.row) - (end - token);
+  if (pos >= 0) t.page = paged_lookup(A.C, t.row, pos, &t.slot);
+  if (t.page < 0 && A.flags) atomicOr(&A.flags[t.row], (uint32_t)SPEC_F_BAD_IDX);
+  return t;
+}
+
+struct Item {
+  int token, head, kv, lane;
+};
+
+template <int LPV>
+__device__ __forceinline__ Item item_of(const CacheIO& A, long long i) {
+  Item t;
+  t.lane = (int)(i % LPV);
+  const unsigned vec = (unsigned)(i / LPV);
+  const unsigned per = 2u * (unsigned)A.C.heads;
+  t.token = (int)(vec / per);
+  const unsigned rest = vec - (unsigned)t.token * per;
+  t.kv = rest >= (unsigned)A.C.heads;
+  t.head = (int)(rest - (t.kv ? (unsigned)A.C.heads : 0u));
+  return t;
+}
+
+// The tokens of a CTA's run, at most one more than its items' share.
+template <int LPV, int U>
+__device__ __forceinline__ void run_places(const CacheIO& A, TokenPlace* places, int* first_token) {
+  const long long first = (long long)blockIdx.x * (kCacheThreads * U);
+  const long long last = min(first + kCacheThreads * U, A.items) - 1;
+  const long long per = 2LL * A.C.heads * LPV;
+  const int t0 = (int)(first / per), t1 = (int)(last / per);
+  for (int t = t0 + threadIdx.x; t <= t1; t += kCacheThreads) places[t - t0] = find_place(A, t);
+  *first_token = t0;
+}
+
+template <bool F32, bool E4M3, int LPV, int U>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheIO A) {
+  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV) + 2];
+  const long long first = (long long)blockIdx.x * (kCacheThreads * U) + threadIdx.x;
+  uint4 raw[U][F32 ? 2 : 1];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long i = first + u * kCacheThreads;
+#pragma unroll
+    for (int w = 0; w < (F32 ? 2 : 1); ++w) raw[u][w] = make_uint4(0, 0, 0, 0);
+    if (i < A.items) {
+      const Item t = item_of<LPV>(A, i);
+      const uint4* p = reinterpret_cast<const uint4*>(A.kv[t.kv] + t.token * A.token_bytes +
+                                                      ((long long)t.head * LPV + t.lane) * (F32 ? 32 : 16));
+#pragma unroll
+      for (int w = 0; w < (F32 ? 2 : 1); ++w) raw[u][w] = __ldcs(p + w);
+    }
+  }
+  int t0;
+  run_places<LPV, U>(A, places, &t0);
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long i = first + u * kCacheThreads;
+    const bool live = i < A.items;
+    const Item t = item_of<LPV>(A, live ? i : 0);
+    float x[8];
+    if (F32) {
+      const uint4 a = raw[u][0], b = raw[u][F32 ? 1 : 0];
+      x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+      x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y), x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+    } else {
+      const uint4 a = raw[u][0];
+      x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
+      x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
+    }
+    uint32_t amax = 0;   // as bits: NaN above infinity above every number
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = LPV / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (!live) continue;
+    const TokenPlace at = places[t.token - t0];
+    if (t.lane == 0 && amax >= 0x7f800000u && A.flags && at.row >= 0) atomicOr(&A.flags[at.row], (uint32_t)SPEC_F_NAN);
+    if (at.page < 0) continue;
+    const long long vec = (long long)t.head * A.C.page_size + at.slot;
+    unsigned char* pool = t.kv ? A.C.v : A.C.k;
+    if (!E4M3) {
+      uint4 w = raw[u][0];
+      if (F32)
+        w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      *reinterpret_cast<uint4*>(pool + at.page * A.C.page_bytes + (vec * LPV + t.lane) * 16) = w;
+    } else {
+      // amax = 1.f * 2^E; 448 = 1.75 * 2^8
+      int s = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u);
+      s = max(s, -126);
+      const bool bad = amax >= 0x7f800000u;
+      const float inv = bad ? 0.f : __uint_as_float((uint32_t)(127 - s) << 23);
+      uint32_t lo, hi;
+      uint16_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = bad ? 0.f : x[2 * e] * inv, b = bad ? 0.f : x[2 * e + 1] * inv;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[e]) : "f"(b), "f"(a));
+      }
+      lo = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+      hi = (uint32_t)h[2] | (uint32_t)h[3] << 16;
+      *reinterpret_cast<uint2*>(pool + at.page * A.C.page_bytes + (vec * LPV + t.lane) * 8) = make_uint2(lo, hi);
+      if (t.lane == 0) (t.kv ? A.C.v_exp : A.C.k_exp)[at.page * A.C.exp_bytes + vec] = (uint8_t)(bad ? 255 : s + 127);
+    }
+  }
+}
+
+template <bool E4M3, int LPV, int U>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheIO A) {
+  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV) + 2];
+  int t0;
+  run_places<LPV, U>(A, places, &t0);
+  __syncthreads();
+  const long long first = (long long)blockIdx.x * (kCacheThreads * U) + threadIdx.x;
+  uint4 raw[U];
+  uint32_t e[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long i = first + u * kCacheThreads;
+    raw[u] = make_uint4(0, 0, 0, 0);
+    e[u] = 127;
+    if (i >= A.items) continue;
+    const Item t = item_of<LPV>(A, i);
+    const TokenPlace at = places[t.token - t0];
+    if (at.page < 0) continue;
+    const long long vec = (long long)t.head * A.C.page_size + at.slot;
+    const unsigned char* p = (t.kv ? A.C.v : A.C.k) + at.page * A.C.page_bytes;
+    if (E4M3) {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p + (vec * LPV + t.lane) * 8));
+      raw[u].x = w.x;
+      raw[u].y = w.y;
+      e[u] = __ldg((t.kv ? A.C.v_exp : A.C.k_exp) + at.page * A.C.exp_bytes + vec);
+    } else {
+      raw[u] = __ldcs(reinterpret_cast<const uint4*>(p + (vec * LPV + t.lane) * 16));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long i = first + u * kCacheThreads;
+    if (i >= A.items) continue;
+    const Item t = item_of<LPV>(A, i);
+    uint4 w = raw[u];
+    if (E4M3) {
+      const float s = exp_value(e[u]);
+      const float4 a = e4m3x4_float(raw[u].x), b = e4m3x4_float(raw[u].y);
+      w = make_uint4(pack_bf16(a.x * s, a.y * s), pack_bf16(a.z * s, a.w * s), pack_bf16(b.x * s, b.y * s),
+                     pack_bf16(b.z * s, b.w * s));
+    }
+    __stcs(reinterpret_cast<uint4*>(A.kv[t.kv] + t.token * A.token_bytes + ((long long)t.head * LPV + t.lane) * 16), w);
+  }
+}
+
+// Items a thread: four keep four independent loads in flight; one where four
+// would leave SMs without a CTA (fewer than two CTAs each).
+static bool many_items(long long items) { return items >= 2LL * 152 * kCacheThreads * 4; }
+
+template <int LPV, int U>
+static void launch_write(const CacheIO& A, bool f32, bool e4m3, cudaStream_t st) {
+  const unsigned grid = (unsigned)((A.items + kCacheThreads * U - 1) / (kCacheThreads * U));
+  if (f32) {
+    if (e4m3) cache_write_kernel<true, true, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+    else cache_write_kernel<true, false, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+  } else {
+    if (e4m3) cache_write_kernel<false, true, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+    else cache_write_kernel<false, false, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+  }
+}
+
+template <int LPV, int U>
+static void launch_read(const CacheIO& A, bool e4m3, cudaStream_t st) {
+  const unsigned grid = (unsigned)((A.items + kCacheThreads * U - 1) / (kCacheThreads * U));
+  if (e4m3) cache_read_kernel<true, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+  else cache_read_kernel<false, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
+}
+
+static int cache_launch(bool write, void* k, void* v, int dtype, long long token_stride, int N, const spec_cache_t* cache,
+                        uint32_t* flags, void* cuda_stream) {
+  CacheIO A;
+  const int rc = paged_check(cache, N, &A.C);
+  if (rc != SPEC_OK) return rc;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_E_DTYPE;
+  if (token_stride < 0) return SPEC_E_DIM;
+  const int es = dtype == SPEC_F32 ? 4 : 2;
+  const long long dense = (long long)A.C.heads * A.C.D;
+  if (token_stride && token_stride < dense) return SPEC_E_DIM;
+  if (N == 0 || A.C.B == 0) return SPEC_OK;
+  if (!k || !v) return SPEC_E_NULL;
+  A.token_bytes = (token_stride ? token_stride : dense) * es;
+  if (!paged_aligned(k, 16) || !paged_aligned(v, 16) || A.token_bytes % 16 || (flags && !paged_aligned(flags, 4)))
+    return SPEC_E_ALIGN;
+  const int lpv = A.C.D / 8;
+  A.items = (long long)N * 2 * A.C.heads * lpv;
+  if (A.items / lpv > 0x7fffffffLL) return SPEC_E_DIM;
+  const int arc = check_arch();
+  if (arc != SPEC_OK) return arc;
+  A.kv[0] = static_cast<unsigned char*>(k);
+  A.kv[1] = static_cast<unsigned char*>(v);
+  A.N = N;
+  A.flags = flags;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  const bool e4m3 = cache->dtype == SPEC_E4M3, f32 = dtype == SPEC_F32, many = many_items(A.items);
+  if (write) {
+    if (lpv == 16) many ? launch_write<16, 4>(A, f32, e4m3, st) : launch_write<16, 1>(A, f32, e4m3, st);
+    else many ? launch_write<8, 4>(A, f32, e4m3, st) : launch_write<8, 1>(A, f32, e4m3, st);
+  } else {
+    if (lpv == 16) many ? launch_read<16, 4>(A, e4m3, st) : launch_read<16, 1>(A, e4m3, st);
+    else many ? launch_read<8, 4>(A, e4m3, st) : launch_read<8, 1>(A, e4m3, st);
+  }
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
+}
+
+}  // namespace specv
+
+extern "C" int spec_cache_write(const void* k, const void* v, int dtype, int64_t token_stride, int N,
+                                const spec_cache_t* cache, uint32_t* flags, void* cuda_stream) {
+  return specv::cache_launch(true, const_cast<void*>(k), const_cast<void*>(v), dtype, token_stride, N, cache, flags,
+                             cuda_stream);
+}
+
+extern "C" int spec_cache_read(uint16_t* k, uint16_t* v, int N, const spec_cache_t* cache, uint32_t* flags,
+                               void* cuda_stream) {
+  return specv::cache_launch(false, k, v, SPEC_BF16, 0, N, cache, flags, cuda_stream);
+}
