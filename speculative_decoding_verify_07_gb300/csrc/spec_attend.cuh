@@ -1,0 +1,222 @@
+// What the attention kernels share: arguments, the division of the work over
+// CTAs, tensor maps of the cache, and bounded waits.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/spec_verify.h"
+#include "spec_device.cuh"
+#include "spec_host.h"
+#include "spec_paged.cuh"
+
+namespace specv {
+
+struct AttendArgs {
+  PagedCache C;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  uint32_t* flags;
+  long long q_token;     // elements from token to token of q
+  int N, group, hq;
+  int box;               // cache rows one copy brings: they lie in one page
+  float scale_log2;      // scale * log2(e): scores are powers of two
+  unsigned* joined;      // workspace: per CTA, how many parts of its last item have come
+  float* parts;          // workspace: per CTA, two partial results
+};
+
+// Workspace: a counter a CTA, then the partial results.
+constexpr int kAttendCtas = 512;       // no launch has more
+constexpr size_t kAttendCounters = kAttendCtas * sizeof(unsigned);
+
+// ------------------------------------------------------- division of the work
+//
+// An item is (row, cache head, tile of M query rows), query rows being the
+// row's (token, head of the group) pairs; its work is the tiles of KT positions
+// that its last query row sees, one at least.  The tiles of all items, in the
+// order row, head, query tile, position, are divided evenly among the CTAs, so
+// a long context is shared by many and short ones are taken in turn.  The parts
+// of an item that lie in several CTAs are joined, in the order of their
+// positions, by the CTA that finishes last.
+
+struct AttendRow {
+  int first, n, kv;     // its packed tokens, and what is cached with them
+};
+
+__device__ __forceinline__ AttendRow attend_row(const AttendArgs& A, int r) {
+  AttendRow R;
+  R.first = __ldg(A.C.cu + r);
+  R.n = __ldg(A.C.cu + r + 1) - R.first;
+  R.kv = __ldg(A.C.kv_len + r);
+  if (R.first < 0 || R.n < 0 || R.n > A.N - R.first) R.n = 0;
+  return R;
+}
+
+// How many positions the row's i-th new token sees; none that the page table cannot hold.
+__device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow& R, int i) {
+  return max(0, min(R.kv - R.n + i + 1, A.C.max_pages * A.C.page_size));
+}
+
+template <int M, int KT>
+__device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow& R, int qt) {
+  const int last = min((qt + 1) * M, R.n * A.group) - 1;
+  return max(1, (attend_sees(A, R, last / A.group) + KT - 1) / KT);
+}
+
+template <int M>
+__device__ __forceinline__ int attend_qtiles(const AttendArgs& A, const AttendRow& R) {
+  return (R.n * A.group + M - 1) / M;
+}
+
+template <int M, int KT>
+__device__ __forceinline__ long long attend_row_tiles(const AttendArgs& A, int r) {
+  const AttendRow R = attend_row(A, r);
+  const int qts = attend_qtiles<M>(A, R);
+  long long sum = 0;
+  for (int q = 0; q < qts; ++q) sum += attend_tiles<M, KT>(A, R, q);
+  return sum * A.C.heads;
+}
+
+// A CTA's share: tiles [begin, end) of `total`, the first of them at `offset` in row `row`.
+struct AttendShare {
+  long long begin, end, total, offset;
+  int row, ctas;     // ctas: those that have work
+};
+
+__device__ __forceinline__ long long share_begin(long long total, int cta, int ctas) { return total * cta / ctas; }
+__device__ __forceinline__ int share_of(long long total, long long tile, int ctas) {
+  return (int)(((tile + 1) * ctas - 1) / total);
+}
+
+template <int M, int KT, int THREADS>
+__device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
+  const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += attend_row_tiles<M, KT>(A, r);
+  sums[t] = mine;
+  __syncthreads();
+  const int used = (A.C.B + each - 1) / each;
+  long long before = 0, total = 0;
+#pragma unroll 8
+  for (int i = 0; i < used; ++i) {
+    const long long s = sums[i];
+    before += i < t ? s : 0;
+    total += s;
+  }
+  const int ctas = (int)min((long long)gridDim.x, total), cta = min((int)blockIdx.x, ctas);
+  const long long begin = total ? share_begin(total, cta, ctas) : 0;
+  if (t == 0) {
+    out->ctas = ctas;
+    out->total = total;
+    out->begin = begin;
+    out->end = cta < ctas ? share_begin(total, cta + 1, ctas) : begin;
+    out->row = 0;
+    out->offset = 0;
+  }
+  __syncthreads();
+  if (begin >= before && begin < before + mine) {
+    long long at = before;
+    for (int r = r0; r < r1; ++r) {
+      const long long w = attend_row_tiles<M, KT>(A, r);
+      if (begin < at + w) {
+        out->row = r;
+        out->offset = begin - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks a CTA's share, one segment (a run of position tiles of one item) after another.
+template <int M, int KT>
+struct AttendWalk {
+  const AttendArgs& A;
+  AttendRow R;
+  int row, head, qt, tiles;      // the item, and its position tiles
+  int a, b;                      // this segment's
+  long long at, end;             // the next tile of all, and the share's end
+  int next_a;
+
+  __device__ __forceinline__ AttendWalk(const AttendArgs& args, const AttendShare& S)
+      : A(args), row(S.row), head(0), qt(0), tiles(0), a(0), b(0), at(S.begin), end(S.end), next_a(0) {
+    if (at >= end) return;
+    R = attend_row(A, row);
+    long long off = S.offset;
+    const long long per_head = attend_row_tiles<M, KT>(A, row) / A.C.heads;
+    head = (int)(off / per_head);
+    off -= head * per_head;
+    for (;;) {
+      tiles = attend_tiles<M, KT>(A, R, qt);
+      if (off < tiles) break;
+      off -= tiles;
+      ++qt;
+    }
+    next_a = (int)off;
+  }
+  // The next segment; false at the end of the share.
+  __device__ __forceinline__ bool next() {
+    if (at >= end) return false;
+    if (next_a >= tiles) {
+      next_a = 0;
+      if (++qt >= attend_qtiles<M>(A, R)) {
+        qt = 0;
+        if (++head >= A.C.heads) {
+          head = 0;
+          do R = attend_row(A, ++row); while (R.n == 0);
+        }
+      }
+      tiles = attend_tiles<M, KT>(A, R, qt);
+    }
+    a = next_a;
+    b = (int)min((long long)tiles, a + (end - at));
+    at += b - a;
+    next_a = b;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return a == 0 && b == tiles; }
+  // The first tile of this item among all.
+  __device__ __forceinline__ long long item_begin() const { return at - b; }
+};
+
+// ---------------------------------------------------------------------- copies
+
+__device__ __forceinline__ void tma_load_4d(uint32_t smem, const CUtensorMap* map, int x, int y, int z, int w,
+                                            unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Waits for the phase; sets *failed and returns when it does not come within
+// two seconds, or when another wait of this CTA has given up.
+__device__ __forceinline__ void mbar_await(unsigned long long* bar, uint32_t parity, volatile int* failed) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long began = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return;
+    if (global_ns() - began > 2000000000ull) *failed = 1;
+  }
+}
+
+using PFN_attend_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A tensor map of one pool: [pages, heads, page_size, head_dim], boxes of up to
+// 128 bytes by `box` rows, swizzled as their width asks.
+int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box);
+
+// The launches.  `maps`: keys, values.
+int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
+
+}  // namespace specv

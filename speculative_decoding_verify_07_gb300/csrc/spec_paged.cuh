@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/spec_verify.h"
+#include "spec_device.cuh"
 
 namespace specv {
 
@@ -115,8 +116,5 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 }  // namespace specv
