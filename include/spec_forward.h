@@ -112,6 +112,8 @@ size_t spec_attend_workspace_size(int heads, int group, int head_dim);
  *   flags [B] uint32 or NULL: SPEC_F_BAD_IDX (OR-ed) where a visible position
  *        has no valid page; such positions are left out.
  * What a query does not see never reaches it, infinities and NaN included.
+ * Values of an 8-bit cache under exponent bytes above 221 (2^103 and more) are
+ * taken for NaN.
  * Scores, their maximum and sum and the output sums are float32; softmax
  * weights are rounded to bf16 for the product with the values.  One call's
  * results do not depend on timing.

@@ -33,8 +33,8 @@ int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int
              : SPEC_E_CUDA;
 }
 
-// Partial results of the launch with the most: 304 CTAs of two parts of 64 rows.
-static size_t attend_parts(int D) { return (size_t)304 * 2 * 64 * (D + 2) * sizeof(float); }
+// Partial results of the launch with the most: 456 CTAs of two parts of 32 rows.
+static size_t attend_parts(int D) { return (size_t)456 * 2 * 32 * (D + 2) * sizeof(float); }
 
 }  // namespace specv
 
@@ -73,9 +73,9 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   A.joined = static_cast<unsigned*>(workspace);
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
   const bool e4m3 = cache->dtype == SPEC_E4M3;
-  // the longest run of positions that never leaves a page, up to a tile's 64
+  // the longest run of positions that never leaves a page, up to a warp's 16
   A.box = 1;
-  while (A.box < 64 && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
+  while (A.box < 16 && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
   CUtensorMap maps[2];
   if (A.C.pages > 0) {
     for (int i = 0; i < 2; ++i)

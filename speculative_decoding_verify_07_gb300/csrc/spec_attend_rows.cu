@@ -1,29 +1,35 @@
-// Attention of a few query rows (16, 32 or 64: tokens times the group) over a
-// long cache: verify and decode steps.
+// Attention of a few query rows (up to 32: tokens times the group) over a long
+// cache: verify and decode steps.
 //
 // Bound by the cache's bytes: for M rows a position of one head costs
-// 4 * M * D operations for 4 D bytes (2 D in 8 bits), 16 to 128 a byte, which
+// 4 * M * D operations for 4 D bytes (2 D in 8 bits), 16 to 64 a byte, which
 // the warp-level matrix instructions deliver beside the loads; the wide
 // tcgen05 tile of 128 rows would spend its time on padding.
 //
-// One producer warp brings tiles of 64 positions by TMA, a box a run of
-// positions within a page, through a ring of stages.  Four consumer warps
-// divide the positions (16 each, or 32 where 64 rows need two warps in the other
-// direction) and keep their own running maximum, sum and weighted values in
-// registers, so no warp waits for another within an item; they are joined in
-// shared memory at its end.  The maximum only moves when a score passes it by
-// 2^8, which keeps weights below 2^8 and rescales the sums a few times a row
-// instead of at every tile.  8-bit codes become bf16 in registers: the code's
-// bits, shifted, are a bf16 number 2^-120 too small, and one packed product
-// corrects that exactly; the scales go to the scores (keys) and the weights
-// (values) in float32.
+// The four warps of a CTA divide each tile of 64 positions, 16 each, and share
+// nothing until an item ends: every warp brings its own positions by TMA (a box
+// a run of positions within a page) through a ring of its own, several tiles
+// ahead and across the ends of items, and keeps its own running maximum, sum
+// and weighted values in registers.  The maximum only moves when a score
+// passes it by 2^8, which keeps weights below 2^8 and rescales the sums a few
+// times a row instead of at every tile.
+//
+// 8-bit codes become fp16 in registers by the conversion instruction (exact),
+// so the products are fp16: the queries are brought into its range by a power
+// of two for the tile, and the values' scales 2^e go into the exponent,
+//   t_j = log2(weight_j) + e_j,   p_j = 2^(t_j - max t),   sum += p_j 2^-e_j,
+// so that the weights of large terms keep all 11 bits whatever the scales.
 #include "spec_attend.cuh"
 
 namespace specv {
 
 constexpr int kRowsKT = 64;
-constexpr int kRowsThreads = 160;
+constexpr int kRowsWarps = 4;
+constexpr int kRowsThreads = kRowsWarps * 32;
+constexpr int kRowsKeys = kRowsKT / kRowsWarps;                  // positions of a tile that a warp takes
 constexpr float kRowsSlack = 8.f;
+constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
+constexpr unsigned kRowsTop = 221;   // so the largest exponent byte whose 2^-e is a normal number; above it is NaN
 
 template <int D, bool E4M3, int MT>
 struct RowsShape {
@@ -31,28 +37,31 @@ struct RowsShape {
   static constexpr int row_bytes = D * (E4M3 ? 1 : 2);
   static constexpr int halves = row_bytes > 128 ? 2 : 1;         // 128-byte columns of a row
   static constexpr int half_bytes = row_bytes / halves;
-  static constexpr int half_tile = kRowsKT * half_bytes;
-  static constexpr int kv_tile = kRowsKT * row_bytes;
-  static constexpr int stage = 2 * kv_tile;
+  static constexpr int half_tile = kRowsKeys * half_bytes;
+  static constexpr int kv_tile = kRowsKeys * row_bytes;
+  static constexpr int stage = 2 * kv_tile;                      // of one warp
   static constexpr int q_bytes = M * D * 2;
   static constexpr int pitch = D + 8;                            // floats a row of the joined values
   static constexpr int o_bytes = M * pitch * 4;
-  static constexpr int ctas = MT == 4 ? 1 : 2;                   // an SM
-  static constexpr int most = (224 * 1024 / ctas - q_bytes - o_bytes - 4096) / (stage + 2 * kRowsKT);
+  static constexpr int ctas = E4M3 && MT == 1 ? 3 : 2;           // an SM
+  static constexpr int most = (225 * 1024 / ctas - 1024 - q_bytes - o_bytes - 6144) / (kRowsWarps * stage);
   static constexpr int stages = most > 6 ? 6 : most;
-  static constexpr int smem = 1024 + stages * (stage + 2 * kRowsKT) + q_bytes + o_bytes;
-  static constexpr int wm = MT == 4 ? 2 : 1;                     // warps across the query rows
-  static constexpr int wk = 4 / wm;                              // and across the positions
-  static constexpr int mt = MT / wm;                             // 16-row tiles a warp
-  static constexpr int keys = kRowsKT / wk;                      // positions a warp
+  static constexpr int smem = 1024 + stages * kRowsWarps * stage + q_bytes + o_bytes;
   static constexpr int part_floats = M * (D + 2);
 };
 
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma_16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -73,402 +82,429 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
   return v;
 }
 
-// Codes in the upper bytes of two halves as bf16: sign, then the seven bits of
-// magnitude at the top of bf16's mantissa and below its exponent, times 2^120.
-__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t high) {
-  uint32_t w = ((high >> 4) & 0x07f007f0u) | (high & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7b807b80u));
-  return w;
+// Two pairs of e4m3 codes as fp16.
+__device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(*lo), "=r"(*hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// What a warp brings next: its 16 positions of a tile, looked up a tile before
+// their copies begin.
+template <int M, bool E4M3>
+struct RowsFetch {
+  AttendWalk<M, kRowsKT> I;
+  int t;                 // the tile
+  bool more;
+  int page, slot;        // of position `lane`, lanes 0 to 15
+  uint32_t ke, ve;       // its exponents
+
+  __device__ __forceinline__ RowsFetch(const AttendArgs& A, const AttendShare& S) : I(A, S), t(0) {
+    more = I.next();
+    t = I.a;
+  }
+  __device__ __forceinline__ void look(int warp, int lane) {
+    page = -1;
+    ke = ve = 0;
+    if (!more) return;
+    const AttendArgs& A = I.A;
+    const int limit = attend_sees(A, I.R, (min((I.qt + 1) * M, I.R.n * A.group) - 1) / A.group);
+    const int pos = t * kRowsKT + warp * kRowsKeys + lane;
+    if (lane < kRowsKeys && pos < limit) {
+      page = paged_lookup(A.C, I.row, pos, &slot);
+      if (page < 0 && A.flags) atomicOr(&A.flags[I.row], (uint32_t)SPEC_F_BAD_IDX);
+      if (E4M3 && page >= 0) {
+        const long long e = page * A.C.exp_bytes + (long long)I.head * A.C.page_size + slot;
+        ke = __ldg(A.C.k_exp + e);
+        ve = __ldg(A.C.v_exp + e);
+      }
+    }
+  }
+  __device__ __forceinline__ void step() {
+    if (++t >= I.b) {
+      more = I.next();
+      t = I.a;
+    }
+  }
+};
 
 template <int D, bool E4M3, int MT>
-__global__ void __launch_bounds__(kRowsThreads, (MT == 4 ? 1 : 2)) attend_rows_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap,
-                                                                      const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
+    attend_rows_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = RowsShape<D, E4M3, MT>;
-  constexpr int M = S::M, KT = kRowsKT, MTW = S::mt;
+  constexpr int M = S::M, KT = kRowsKT, NK = kRowsKeys;
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) unsigned long long full[S::stages], empty[S::stages];
-  __shared__ unsigned long long there[S::stages];     // which positions of the stage are there
+  __shared__ __align__(8) unsigned long long full[kRowsWarps][S::stages];
+  __shared__ unsigned there[kRowsWarps][S::stages];                      // bits: positions of the stage that are there; NaN values
+  __shared__ __align__(8) float scales[kRowsWarps][S::stages][E4M3 ? 3 : 1][E4M3 ? NK : 1];   // keys' 2^e, values' e and 2^-e
   __shared__ AttendShare share;
   __shared__ long long sums[kRowsThreads];
-  __shared__ float sm_m[S::wk][M], sm_l[S::wk][M];
+  __shared__ float sm_m[kRowsWarps][M], sm_l[kRowsWarps][M];
   __shared__ int sees[M];
-  __shared__ int failed, odd, last_part;
+  __shared__ int failed, odd, last_part, first_nan;
+  __shared__ unsigned q_top;
   unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  unsigned char* const q_sm = base + S::stages * S::stage;
+  unsigned char* const q_sm = base + S::stages * kRowsWarps * S::stage;
   float* const o_sm = reinterpret_cast<float*>(q_sm + S::q_bytes);
-  unsigned char* const e_sm = q_sm + S::q_bytes + S::o_bytes;      // [stage][k, v][KT] exponents
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  unsigned char* const ring = base + warp * S::stages * S::stage;
 
   if (threadIdx.x == 0) {
     failed = 0;
-    for (int i = 0; i < S::stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
-    }
+    for (int i = 0; i < kRowsWarps * S::stages; ++i) mbar_init(&full[0][0] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   attend_share<M, KT, kRowsThreads>(A, &share, sums);
-  AttendWalk<M, KT> W(A, share);
 
-  if (warp == 4) {
-    // ------------------------------------------------------------- producer
-    int stage = 0;
-    uint32_t phase = 0;
-    const int boxes = KT / A.box;
-    // a box of one 64-byte row would not begin at a multiple of 128 bytes: its lane copies it
-    const bool by_hand = S::half_bytes == 64 && A.box == 1;
-    while (W.next()) {
-      const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
-      for (int t = W.a; t < W.b; ++t) {
-        const int key0 = t * KT;
-        // the pages of this lane's boxes, and of its positions where these have exponents
-        int page[2], slot[2];
-        uint8_t ke[2], ve[2];
-        bool ok[2];
+  RowsFetch<M, E4M3> F(A, share);
+  F.look(warp, lane);
+  // a box of one 64-byte row would not begin at a multiple of 128 bytes: its lane copies it
+  const bool by_hand = S::half_bytes == 64 && A.box == 1;
+  const int box = min(A.box, NK), copies_of = NK / box * 2 * S::halves;
+  auto bring = [&](int stage) {
+    if (!F.more) return;
+    const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
+    const unsigned nans = E4M3 ? __ballot_sync(0xffffffffu, F.ve > kRowsTop) : 0;
+    unsigned char* const to = ring + stage * S::stage;
+    unsigned bytes = 0;
+    if (E4M3 && lane < NK) {
+      float* s = &scales[warp][stage][0][0] + lane;
+      s[0] = exp_value(F.ke);
+      const int e = F.ve > kRowsTop ? 127 : max((int)F.ve, 1);
+      s[NK * (E4M3 ? 1 : 0)] = (float)(e - 127);
+      s[2 * NK * (E4M3 ? 1 : 0)] = __uint_as_float((uint32_t)(254 - e - kRowsShift) << 23);
+    }
+    if (by_hand) {
+      if (F.page >= 0) {
+        const long long at = ((long long)F.I.head * A.C.page_size + F.slot) * D + F.page * A.C.page_bytes;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int pos = key0 + lane + 32 * j;
-          page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &slot[j]) : -1;
-          ok[j] = page[j] >= 0;
-          ke[j] = ve[j] = 0;
-          if (E4M3 && ok[j]) {
-            const long long e = page[j] * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot[j];
-            ke[j] = __ldg(A.C.k_exp + e);
-            ve[j] = __ldg(A.C.v_exp + e);
-          }
-          if (!ok[j] && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+        for (int c = 0; c < S::half_bytes / 16; ++c) {
+          unsigned char* p = to + lane * S::half_bytes + (c ^ (lane >> 1 & 3)) * 16;
+          *reinterpret_cast<uint4*>(p) = __ldg(reinterpret_cast<const uint4*>(A.C.k + at) + c);
+          *reinterpret_cast<uint4*>(p + S::kv_tile) = __ldg(reinterpret_cast<const uint4*>(A.C.v + at) + c);
         }
-        const unsigned long long mask = (unsigned long long)__ballot_sync(0xffffffffu, ok[1]) << 32 | __ballot_sync(0xffffffffu, ok[0]);
-        mbar_await(&empty[stage], phase ^ 1, &failed);
-        if (E4M3) {
-          unsigned char* e = e_sm + stage * 2 * KT;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            e[lane + 32 * j] = ke[j];
-            e[KT + lane + 32 * j] = ve[j];
-          }
+      }
+    } else if (!failed) {
+      for (int b = 0; b < NK; b += box) bytes += (mask >> b & 1) * box * 2 * S::row_bytes;
+    }
+    if (lane == 0) {
+      there[warp][stage] = mask | nans << 16;
+      mbar_arrive_expect_tx(&full[warp][stage], bytes);
+    }
+    __syncwarp();
+    if (bytes) {
+      for (int i0 = 0; i0 < copies_of; i0 += 32) {
+        const int i = i0 + lane, part = i % (2 * S::halves), at = i / (2 * S::halves) * box;
+        const int page = __shfl_sync(0xffffffffu, F.page, at & 15), slot = __shfl_sync(0xffffffffu, F.slot, at & 15);
+        if (i < copies_of && page >= 0) {
+          const int half = part % S::halves;
+          const bool v = part >= S::halves;
+          tma_load_4d(smem_u32(to + (v ? S::kv_tile : 0) + half * S::half_tile + at * S::half_bytes), v ? &vmap : &kmap, half * 64,
+                      slot, F.I.head, page, &full[warp][stage]);
         }
-        if (by_hand) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (!ok[j]) continue;
-            const int k = lane + 32 * j;
-            const long long vec = ((long long)W.head * A.C.page_size + slot[j]) * D + page[j] * A.C.page_bytes;
-#pragma unroll
-            for (int c = 0; c < S::half_bytes / 16; ++c) {
-              unsigned char* to = base + stage * S::stage + k * S::half_bytes + (c ^ (k >> 1 & 3)) * 16;
-              *reinterpret_cast<uint4*>(to) = __ldg(reinterpret_cast<const uint4*>(A.C.k + vec) + c);
-              *reinterpret_cast<uint4*>(to + S::kv_tile) = __ldg(reinterpret_cast<const uint4*>(A.C.v + vec) + c);
-            }
-          }
-          __syncwarp();
-        }
-        int copies = 0;
-        if (!failed && !by_hand)
-          for (int b = lane; b < boxes; b += 32) copies += (int)(mask >> (b * A.box)) & 1;
-        copies = __reduce_add_sync(0xffffffffu, copies);
-        if (lane == 0) {
-          there[stage] = mask;
-          mbar_arrive_expect_tx(&full[stage], copies * 2 * A.box * S::row_bytes);
-        }
-        __syncwarp();
-        if (copies) {
-          const uint32_t dst = smem_u32(base + stage * S::stage);
-          for (int b0 = 0; b0 < boxes; b0 += 32) {
-            // a box begins at position b * box, which another lane looked up
-            const int b = b0 + lane, at = (b * A.box) & 63;
-            const int p0 = __shfl_sync(0xffffffffu, page[0], at & 31), p1 = __shfl_sync(0xffffffffu, page[1], at & 31);
-            const int s0 = __shfl_sync(0xffffffffu, slot[0], at & 31), s1 = __shfl_sync(0xffffffffu, slot[1], at & 31);
-            const int p = at < 32 ? p0 : p1, s = at < 32 ? s0 : s1;
-            if (b < boxes && (mask >> at & 1)) {
-#pragma unroll
-              for (int h = 0; h < S::halves; ++h) {
-                const uint32_t to = dst + h * S::half_tile + at * S::half_bytes;
-                tma_load_4d(to, &kmap, h * 64, s, W.head, p, &full[stage]);
-                tma_load_4d(to + S::kv_tile, &vmap, h * 64, s, W.head, p, &full[stage]);
-              }
-            }
-          }
-        }
-        if (++stage == S::stages) stage = 0, phase ^= 1;
       }
     }
-    // the copies in flight land before the CTA may end
-    for (int i = 0; i < S::stages; ++i) {
-      mbar_await(&empty[stage], phase ^ 1, &failed);
-      if (++stage == S::stages) stage = 0, phase ^= 1;
-    }
-    return;
-  }
+    F.step();
+    F.look(warp, lane);
+  };
+  for (int i = 0; i < S::stages; ++i) bring(i);
 
-  // --------------------------------------------------------------- consumers
   int stage = 0;
   uint32_t phase = 0;
-  const int mw = warp % S::wm, kw = warp / S::wm;         // this warp's place across rows and positions
   const int q4 = lane % 4, r8 = lane / 4;
+  AttendWalk<M, KT> W(A, share);
   while (W.next()) {
     const int rows = min(M, W.R.n * A.group - W.qt * M);  // query rows of this tile
-    // Q as the matrix instruction's A fragments, 16 bytes a lane, and what each row sees.
-    for (int i = threadIdx.x; i < M * D / 8; i += 128) {
+    if (threadIdx.x == 0) odd = 0, q_top = 0, first_nan = 0x7fffffff;
+    if (threadIdx.x < M) {
+      const int g = min(W.qt * M + (int)threadIdx.x, W.R.n * A.group - 1);
+      sees[threadIdx.x] = attend_sees(A, W.R, g / A.group);
+    }
+    // Q as the matrix instruction's A fragments, 16 bytes a lane.
+    constexpr int each = M * D / 8 / kRowsThreads;
+    uint2 qw[each][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < each; ++u) {
+      const int i = u * kRowsThreads + threadIdx.x;
       const int fl = i % 32, ks = i / 32 % (D / 16), m0 = i / 32 / (D / 16) * 16 + fl / 4, q = fl % 4;
-      uint2 w[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int m = m0 + 8 * h;
-        w[h] = make_uint2(0, 0);
+        qw[u][h] = make_uint2(0, 0);
         if (m < rows) {
           const int g = W.qt * M + m, token = g / A.group, head = W.head * A.group + g - token * A.group;
           const uint16_t* p = A.q + (W.R.first + token) * A.q_token + (long long)head * D;
           if (E4M3) {
             // a lane's four of k-step ks: those that its 16-byte load of codes brings (see below)
             const int d = D == 128 ? 32 * q + 16 * (ks / 4) + 4 * (ks % 4) : 16 * q + 4 * ks;
-            w[h] = *reinterpret_cast<const uint2*>(p + d);
+            qw[u][h] = *reinterpret_cast<const uint2*>(p + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = (e < 2 ? qw[u][h].x : qw[u][h].y) >> (e % 2 * 16) & 0x7fffu;
+              top = max(top, x < 0x7f80u ? x : 0u);
+            }
           } else {
-            w[h].x = *reinterpret_cast<const uint32_t*>(p + ks * 16 + 2 * q);
-            w[h].y = *reinterpret_cast<const uint32_t*>(p + ks * 16 + 2 * q + 8);
+            qw[u][h].x = *reinterpret_cast<const uint32_t*>(p + ks * 16 + 2 * q);
+            qw[u][h].y = *reinterpret_cast<const uint32_t*>(p + ks * 16 + 2 * q + 8);
           }
         }
       }
-      *reinterpret_cast<uint4*>(q_sm + i * 16) = make_uint4(w[0].x, w[1].x, w[0].y, w[1].y);
     }
-    if (threadIdx.x < M) {
-      const int g = min(W.qt * M + (int)threadIdx.x, W.R.n * A.group - 1);
-      sees[threadIdx.x] = attend_sees(A, W.R, g / A.group);
+    float score_scale = A.scale_log2, q_scale = 1.f;
+    if (E4M3) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      __syncthreads();
+      if (lane == 0) atomicMax(&q_top, top);
+      __syncthreads();
+      // the largest magnitude to 2^13 .. 2^14 (what is 2^-27 of it is still a normal number)
+      const int up = min(13 - ((int)(q_top >> 7) - 127), 126);
+      q_scale = __uint_as_float((uint32_t)(127 + up) << 23);
+      score_scale *= __uint_as_float((uint32_t)(127 - up) << 23);
     }
-    if (threadIdx.x == 0) odd = 0;
-    rows_sync();
+#pragma unroll
+    for (int u = 0; u < each; ++u) {
+      uint32_t w[4] = {qw[u][0].x, qw[u][1].x, qw[u][0].y, qw[u][1].y};
+      if (E4M3)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * q_scale, bf16_hi(w[e]) * q_scale);
+      *reinterpret_cast<uint4*>(q_sm + (u * kRowsThreads + threadIdx.x) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();
     const int fewest = sees[0];                           // the first row's token comes first
-    int lim[MTW][2];
+    int lim[MT][2];
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
-    for (int i = 0; i < MTW; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) lim[i][h] = sees[(mw * MTW + i) * 16 + 8 * h + r8];
-
-    float o[MTW][D / 8][4], m[MTW][2], l[MTW][2];
-#pragma unroll
-    for (int i = 0; i < MTW; ++i) {
+    for (int i = 0; i < MT; ++i) {
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][d][e] = 0.f;
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lim[i][h] = sees[i * 16 + 8 * h + r8];
+        m[i][h] = -INFINITY;
+        l[i][h] = 0.f;
+      }
     }
 
     for (int t = W.a; t < W.b; ++t) {
-      mbar_await(&full[stage], phase, &failed);
-      const uint32_t ks_base = smem_u32(base + stage * S::stage), vs_base = ks_base + S::kv_tile;
-      const unsigned long long mask = there[stage];
-      const bool edge = (t + 1) * KT > fewest || mask != ~0ull;
+      mbar_await(&full[warp][stage], phase, &failed);
+      unsigned char* const k_sm = ring + stage * S::stage;
+      const uint32_t ks_base = smem_u32(k_sm), vs_base = ks_base + S::kv_tile;
+      const unsigned bits = there[warp][stage], mask = bits & 0xffffu;
+      if (E4M3 && bits >> 16) odd = 1;
+      const int key0 = t * KT + warp * NK;                // this warp's first position
+      const bool edge = key0 + NK > fewest || mask != 0xffffu;
+      if (edge) {
+        // A value of weight zero must be finite: positions that are not there are cleared, and what is not finite of
+        // those that only some rows see is cleared and remembered.
+        bool found = false;
 #pragma unroll
-      for (int step = 0; step < S::keys / 16; ++step) {
-        const int k0 = kw * S::keys + step * 16;          // this warp's 16 positions of the tile
-        if (edge) {
-          // A value of weight zero must be finite: positions that are not there are cleared, and what is not
-          // finite of those that only some rows see is cleared and remembered.
-          bool found = false;
-#pragma unroll
-          for (int i = lane; i < 16 * (S::row_bytes / 16); i += 32) {
-            const int k = k0 + i / (S::row_bytes / 16), c = i % (S::row_bytes / 16);
-            unsigned char* p = base + stage * S::stage + S::kv_tile + (c * 16 / S::half_bytes) * S::half_tile + k * S::half_bytes;
-            const int cc = c % (S::half_bytes / 16);
-            p += (S::half_bytes == 128 ? cc ^ (k & 7) : cc ^ (k >> 1 & 3)) * 16;
+        for (int i = lane; i < NK * (S::row_bytes / 16); i += 32) {
+          const int k = i / (S::row_bytes / 16), c = i % (S::row_bytes / 16), cc = c % (S::half_bytes / 16);
+          unsigned char* p = k_sm + S::kv_tile + c / (S::half_bytes / 16) * S::half_tile + k * S::half_bytes +
+                             (S::half_bytes == 128 ? cc ^ (k & 7) : cc ^ (k >> 1 & 3)) * 16;
+          if (!(mask >> k & 1)) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+          } else if (!E4M3 && key0 + k >= fewest) {
             uint4 w = *reinterpret_cast<uint4*>(p);
-            if (!(mask >> k & 1)) {
-              *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-            } else if (!E4M3 && t * KT + k >= fewest) {
-              uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-              bool bad = false;
+            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+            bool bad = false;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if ((x[j] & 0x7f80u) == 0x7f80u) x[j] &= 0xffff0000u, bad = true;
-                if ((x[j] & 0x7f800000u) == 0x7f800000u) x[j] &= 0xffffu, bad = true;
-              }
-              if (bad) *reinterpret_cast<uint4*>(p) = w;
-              found = found || bad;
+            for (int j = 0; j < 4; ++j) {
+              if ((x[j] & 0x7f80u) == 0x7f80u) x[j] &= 0xffff0000u, bad = true;
+              if ((x[j] & 0x7f800000u) == 0x7f800000u) x[j] &= 0xffffu, bad = true;
             }
+            if (bad) *reinterpret_cast<uint4*>(p) = w;
+            found = found || bad;
           }
-          if (found) odd = 1;
-          __syncwarp();
         }
-        float s[MTW][2][4];
+        if (found) odd = 1;
+        __syncwarp();
+      }
+      float s[MT][2][4];
 #pragma unroll
-        for (int i = 0; i < MTW; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-        const uint32_t qa = smem_u32(q_sm) + (mw * MTW) * D * 32 + lane * 16;
-        if (!E4M3) {
+          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+      const uint32_t qa = smem_u32(q_sm) + lane * 16;
+      if (!E4M3) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t kb[4];
-            const int k = k0 + (lane / 16) * 8 + lane % 8, c = (ks % 4) * 2 + (lane / 8 & 1);
-            ldsm4(kb, ks_base + (ks / 4) * S::half_tile + k * 128 + ((c ^ (k & 7)) << 4));
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kb[4];
+          const int k = (lane / 16) * 8 + lane % 8, c = (ks % 4) * 2 + (lane / 8 & 1);
+          ldsm4(kb, ks_base + (ks / 4) * S::half_tile + k * 128 + ((c ^ (k & 7)) << 4));
 #pragma unroll
-            for (int i = 0; i < MTW; ++i) {
-              const uint4 f = lds128(qa + (i * (D / 16) + ks) * 512);
+          for (int i = 0; i < MT; ++i) {
+            const uint4 f = lds128(qa + (i * (D / 16) + ks) * 512);
+            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+            mma_16<false>(s[i][0], a, kb[0], kb[1]);
+            mma_16<false>(s[i][1], a, kb[2], kb[3]);
+          }
+        }
+      } else {
+        // A lane loads 16 codes of its position (16-byte column 2 q + j of 8, or q of 4); which dimension stands at
+        // which place of the sum does not matter, so its bytes 4 i .. 4 i + 3 are its four of k-step 4 j + i.
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint4 kc[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int k = 8 * n + r8;
+            const int c = D == 128 ? (2 * q4 + j) ^ (k & 7) : q4 ^ (k >> 1 & 3);
+            kc[n] = lds128(ks_base + k * S::row_bytes + c * 16);
+          }
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            uint32_t kb[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              e4m3_f16(i4 == 0 ? kc[n].x : i4 == 1 ? kc[n].y : i4 == 2 ? kc[n].z : kc[n].w, &kb[n][0], &kb[n][1]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              const uint4 f = lds128(qa + (i * (D / 16) + 4 * j + i4) * 512);
               const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-              mma_bf16(s[i][0], a, kb[0], kb[1]);
-              mma_bf16(s[i][1], a, kb[2], kb[3]);
-            }
-          }
-        } else {
-          // A lane loads 16 codes of its position (16-byte column 2 q + j of 8, or q of 4); which dimension stands
-          // at which place of the sum does not matter, so its bytes 4 i .. 4 i + 3 are its four of k-step 4 j + i.
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint4 kc[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int k = k0 + 8 * n + r8;
-              const int c = D == 128 ? (2 * q4 + j) ^ (k & 7) : q4 ^ (k >> 1 & 3);
-              kc[n] = lds128(ks_base + k * S::row_bytes + c * 16);
-            }
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-              uint32_t kb[2][2];
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                const uint32_t w = i4 == 0 ? kc[n].x : i4 == 1 ? kc[n].y : i4 == 2 ? kc[n].z : kc[n].w;
-                kb[n][0] = e4m3_bf16(__byte_perm(w, 0, 0x1404));
-                kb[n][1] = e4m3_bf16(__byte_perm(w, 0, 0x3424));
-              }
-#pragma unroll
-              for (int i = 0; i < MTW; ++i) {
-                const uint4 f = lds128(qa + (i * (D / 16) + 4 * j + i4) * 512);
-                const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-                mma_bf16(s[i][0], a, kb[0][0], kb[0][1]);
-                mma_bf16(s[i][1], a, kb[1][0], kb[1][1]);
-              }
-            }
-          }
-        }
-        // scores in powers of two, masked; the scales of this lane's columns
-        float vs[2][2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int k = k0 + 8 * n + 2 * q4;
-          float ksc[2] = {A.scale_log2, A.scale_log2};
-          if (E4M3) {
-            const unsigned char* e = e_sm + stage * 2 * KT + k;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              ksc[j] *= exp_value(e[j]);
-              vs[n][j] = exp_value(e[KT + j]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < MTW; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[i][n][e] *= ksc[e & 1];
-              if (edge && (t * KT + k + (e & 1) >= lim[i][e >> 1] || !(mask >> (k + (e & 1)) & 1))) s[i][n][e] = -INFINITY;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < MTW; ++i) {
-          float top[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]), fmaxf(s[i][1][2 * h], s[i][1][2 * h + 1]));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          }
-          if (__any_sync(0xffffffffu, top[0] > m[i][0] + kRowsSlack || top[1] > m[i][1] + kRowsSlack)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float to = fmaxf(m[i][h], top[h]);
-              const float keep = to == -INFINITY ? 1.f : exp2_fast(m[i][h] - to);
-              m[i][h] = to;
-              l[i][h] *= keep;
-#pragma unroll
-              for (int d = 0; d < D / 8; ++d) o[i][d][2 * h] *= keep, o[i][d][2 * h + 1] *= keep;
-            }
-          }
-          uint32_t p[2][2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float from = m[i][h] == -INFINITY ? 0.f : m[i][h];
-              float a = exp2_fast(s[i][n][2 * h] - from), b = exp2_fast(s[i][n][2 * h + 1] - from);
-              l[i][h] += a + b;
-              if (E4M3) {
-                // a scale that is not seen may be NaN
-                a = edge && a == 0.f ? 0.f : a * vs[n][0];
-                b = edge && b == 0.f ? 0.f : b * vs[n][1];
-              }
-              p[n][h] = pack_bf16(a, b);
-            }
-          const uint32_t pa[4] = {p[0][0], p[0][1], p[1][0], p[1][1]};
-          // the values' fragments are loaded again for a second 16-row tile: registers are short
-          if (!E4M3) {
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-              uint32_t vb[4];
-              const int k = k0 + (lane / 8 & 1) * 8 + lane % 8, c = (d % 4) * 2 + lane / 16;
-              ldsm4_t(vb, vs_base + (d / 4) * S::half_tile + k * 128 + ((c ^ (k & 7)) << 4));
-              mma_bf16(o[i][2 * d], pa, vb[0], vb[1]);
-              mma_bf16(o[i][2 * d + 1], pa, vb[2], vb[3]);
-            }
-          } else {
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-              // pairs of dimensions move as one 16-bit element; even and odd ones are tiles of their own
-              uint32_t vb[4];
-              const int k = k0 + (lane / 8 & 1) * 8 + lane % 8, c = 2 * d + lane / 16;
-              ldsm4_t(vb, vs_base + k * S::row_bytes + ((D == 128 ? c ^ (k & 7) : c ^ (k >> 1 & 3)) << 4));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                mma_bf16(o[i][4 * d + 2 * j], pa, e4m3_bf16(vb[2 * j] << 8 & 0xff00ff00u), e4m3_bf16(vb[2 * j + 1] << 8 & 0xff00ff00u));
-                mma_bf16(o[i][4 * d + 2 * j + 1], pa, e4m3_bf16(vb[2 * j] & 0xff00ff00u), e4m3_bf16(vb[2 * j + 1] & 0xff00ff00u));
-              }
+              mma_16<true>(s[i][0], a, kb[0][0], kb[0][1]);
+              mma_16<true>(s[i][1], a, kb[1][0], kb[1][1]);
             }
           }
         }
       }
-      if (edge) fence_proxy_async();     // what was cleared is written before the next copy lands here
+      // scores in powers of two (of 8-bit values: with the exponent), masked
+      float inv[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int k = 8 * n + 2 * q4;
+        float by[2] = {score_scale, score_scale}, plus[2] = {0.f, 0.f};
+        if (E4M3) {
+          const float* f = &scales[warp][stage][0][0] + k;
+          const float2 a = *reinterpret_cast<const float2*>(f), b = *reinterpret_cast<const float2*>(f + NK),
+                       c = *reinterpret_cast<const float2*>(f + 2 * NK);
+          by[0] *= a.x, by[1] *= a.y;
+          plus[0] = b.x, plus[1] = b.y;
+          inv[n][0] = c.x, inv[n][1] = c.y;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[i][n][e] = E4M3 ? fmaf(s[i][n][e], by[e & 1], plus[e & 1]) : s[i][n][e] * by[e & 1];
+            if (edge && (key0 + k + (e & 1) >= lim[i][e >> 1] || !(mask >> (k + (e & 1)) & 1))) s[i][n][e] = -INFINITY;
+          }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        float high[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          high[h] = fmaxf(fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]), fmaxf(s[i][1][2 * h], s[i][1][2 * h + 1]));
+          high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 1));
+          high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 2));
+        }
+        if (__any_sync(0xffffffffu, high[0] > m[i][0] + kRowsSlack || high[1] > m[i][1] + kRowsSlack)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float to = fmaxf(m[i][h], high[h]);
+            const float keep = to == -INFINITY ? 1.f : exp2_fast(m[i][h] - to);
+            m[i][h] = to;
+            l[i][h] *= keep;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) o[i][d][2 * h] *= keep, o[i][d][2 * h + 1] *= keep;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float from = m[i][h] == -INFINITY ? 0.f : m[i][h];
+            const float a = exp2_fast(s[i][n][2 * h] - from), b = exp2_fast(s[i][n][2 * h + 1] - from);
+            if (E4M3) {
+              l[i][h] = fmaf(b, inv[n][1], fmaf(a, inv[n][0], l[i][h]));
+              pa[i][2 * n + h] = pack_f16(a, b);
+            } else {
+              l[i][h] += a + b;
+              pa[i][2 * n + h] = pack_bf16(a, b);
+            }
+          }
+      }
+      if (!E4M3) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t vb[4];
+          const int k = (lane / 8 & 1) * 8 + lane % 8, c = (d % 4) * 2 + lane / 16;
+          ldsm4_t(vb, vs_base + (d / 4) * S::half_tile + k * 128 + ((c ^ (k & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            mma_16<false>(o[i][2 * d], pa[i], vb[0], vb[1]);
+            mma_16<false>(o[i][2 * d + 1], pa[i], vb[2], vb[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          // pairs of dimensions move as one 16-bit element; even and odd ones are tiles of their own
+          uint32_t vb[4];
+          const int k = (lane / 8 & 1) * 8 + lane % 8, c = 2 * d + lane / 16;
+          ldsm4_t(vb, vs_base + k * S::row_bytes + ((D == 128 ? c ^ (k & 7) : c ^ (k >> 1 & 3)) << 4));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t e0, o0, e1, o1;
+            e4m3_f16(__byte_perm(vb[2 * j], 0, 0x3120), &e0, &o0);
+            e4m3_f16(__byte_perm(vb[2 * j + 1], 0, 0x3120), &e1, &o1);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              mma_16<true>(o[i][4 * d + 2 * j], pa[i], e0, e1);
+              mma_16<true>(o[i][4 * d + 2 * j + 1], pa[i], o0, o1);
+            }
+          }
+        }
+      }
+      if (edge || by_hand) fence_proxy_async();     // what was written here comes before the next copy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
+      bring(stage);
       if (++stage == S::stages) stage = 0, phase ^= 1;
     }
 
     // ------------------------------------------------ join the warps' positions
 #pragma unroll
-    for (int i = 0; i < MTW; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 1);
         l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
         if (q4 == 0) {
-          const int row = (mw * MTW + i) * 16 + 8 * h + r8;
-          sm_m[kw][row] = m[i][h];
-          sm_l[kw][row] = l[i][h];
+          const int row = i * 16 + 8 * h + r8;
+          sm_m[warp][row] = m[i][h];
+          sm_l[warp][row] = l[i][h];
         }
       }
-    rows_sync();
-    float mine[MTW][2];
+    __syncthreads();
+    float mine[MT][2];
 #pragma unroll
-    for (int i = 0; i < MTW; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = (mw * MTW + i) * 16 + 8 * h + r8;
+        const int row = i * 16 + 8 * h + r8;
         float top = sm_m[0][row];
 #pragma unroll
-        for (int w = 1; w < S::wk; ++w) top = fmaxf(top, sm_m[w][row]);
+        for (int w = 1; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
         mine[i][h] = top == -INFINITY ? 1.f : exp2_fast(m[i][h] - top);
       }
-    for (int w = 0; w < S::wk; ++w) {
-      if (kw == w) {
+    for (int w = 0; w < kRowsWarps; ++w) {
+      if (warp == w) {
 #pragma unroll
-        for (int i = 0; i < MTW; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float* row = o_sm + ((mw * MTW + i) * 16 + 8 * h + r8) * S::pitch;
+            float* row = o_sm + (i * 16 + 8 * h + r8) * S::pitch;
 #pragma unroll
             for (int d = 0; d < D / 8; d += 2) {
               // in 16 bits columns 8 d + 2 q of two tiles; in 8 bits 8 d + 4 q .. + 3 of an even and an odd tile
@@ -491,65 +527,78 @@ __global__ void __launch_bounds__(kRowsThreads, (MT == 4 ? 1 : 2)) attend_rows_k
             }
           }
       }
-      rows_sync();
+      __syncthreads();
     }
     if (odd) {
-      // values that are not finite at positions that only some rows see
-      for (int k = max(fewest, W.a * KT); k < min(sees[M - 1], W.b * KT); ++k) {
-        int slot;
-        const int page = paged_lookup(A.C, W.row, k, &slot);
-        if (page < 0) continue;
-        const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D;
-        for (int d = threadIdx.x; d < D; d += 128) {
-          const float x = __uint_as_float((uint32_t)v[d] << 16);
-          if (isfinite(x)) continue;
-          for (int row = 0; row < M; ++row)
-            if (k < sees[row]) o_sm[row * S::pitch + d] += x;
+      const int k1 = min(sees[M - 1], W.b * KT);
+      if (E4M3) {
+        // values of NaN: rows that see the first of them
+        for (int k = W.a * KT + threadIdx.x; k < k1; k += kRowsThreads) {
+          int slot;
+          const int page = paged_lookup(A.C, W.row, k, &slot);
+          if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > kRowsTop) atomicMin(&first_nan, k);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < M * D; i += kRowsThreads)
+          if (first_nan < sees[i / D]) o_sm[i / D * S::pitch + i % D] = __uint_as_float(0x7fc00000u);
+      } else {
+        // values that are not finite at positions that only some rows see
+        for (int k = max(fewest, W.a * KT); k < k1; ++k) {
+          int slot;
+          const int page = paged_lookup(A.C, W.row, k, &slot);
+          if (page < 0) continue;
+          const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D;
+          for (int d = threadIdx.x; d < D; d += kRowsThreads) {
+            const float x = __uint_as_float((uint32_t)v[d] << 16);
+            if (isfinite(x)) continue;
+            for (int row = 0; row < M; ++row)
+              if (k < sees[row]) o_sm[row * S::pitch + d] += x;
+          }
         }
       }
-      rows_sync();
+      __syncthreads();
     }
-    // each thread keeps its place of the joined result: row, and columns of 8
     const bool whole = W.whole();
     const long long item = W.item_begin();
     const int c0 = whole ? 0 : share_of(share.total, item, share.ctas);
     const int c1 = whole ? 0 : share_of(share.total, item + W.tiles - 1, share.ctas);
     if (!whole) {
       float* part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
-      for (int i = threadIdx.x; i < M * D / 4; i += 128) {
+      for (int i = threadIdx.x; i < M * D / 4; i += kRowsThreads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         __stcg(reinterpret_cast<float4*>(part + row * D + d), *reinterpret_cast<float4*>(o_sm + row * S::pitch + d));
       }
       if (threadIdx.x < M) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < S::wk; ++w) top = fmaxf(top, sm_m[w][threadIdx.x]);
+        for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][threadIdx.x]);
 #pragma unroll
-        for (int w = 0; w < S::wk; ++w) sum += sm_l[w][threadIdx.x] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][threadIdx.x] - top));
+        for (int w = 0; w < kRowsWarps; ++w)
+          sum += sm_l[w][threadIdx.x] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][threadIdx.x] - top));
         __stcg(part + M * D + threadIdx.x, top);
         __stcg(part + M * D + M + threadIdx.x, sum);
       }
       __threadfence();
-      rows_sync();
+      __syncthreads();
       if (threadIdx.x == 0) {
         const unsigned had = atomicAdd(&A.joined[c0], 1u);
         last_part = had == (unsigned)(c1 - c0);
         if (last_part) A.joined[c0] = 0;
         __threadfence();
       }
-      rows_sync();
+      __syncthreads();
     }
     if (whole || last_part) {
-      for (int i = threadIdx.x; i < rows * (D / 8); i += 128) {
+      for (int i = threadIdx.x; i < rows * (D / 8); i += kRowsThreads) {
         const int row = i / (D / 8), d = i % (D / 8) * 8;
         float x[8], top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = 0.f;
         if (whole) {
 #pragma unroll
-          for (int w = 0; w < S::wk; ++w) top = fmaxf(top, sm_m[w][row]);
+          for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
 #pragma unroll
-          for (int w = 0; w < S::wk; ++w) sum += sm_l[w][row] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][row] - top));
+          for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w][row] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][row] - top));
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = o_sm[row * S::pitch + d + e];
         } else {
@@ -569,15 +618,17 @@ __global__ void __launch_bounds__(kRowsThreads, (MT == 4 ? 1 : 2)) attend_rows_k
         }
         const int g = W.qt * M + row, token = g / A.group;
         const long long at = (long long)(W.R.first + token) * A.hq + W.head * A.group + g - token * A.group;
-        const float inv = sum == 0.f ? 1.f : 1.f / sum;
+        float by = sum == 0.f ? 1.f : 1.f / sum;
+        if (E4M3) by *= __uint_as_float((127 - kRowsShift) << 23);
         *reinterpret_cast<uint4*>(A.out + at * D + d) =
-            make_uint4(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv), pack_bf16(x[4] * inv, x[5] * inv),
-                       pack_bf16(x[6] * inv, x[7] * inv));
-        if (d == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
+                       pack_bf16(x[6] * by, x[7] * by));
+        if (d == 0 && A.lse)
+          A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum) + (E4M3 ? kRowsShift : 0)) * 0.6931471805599453f;
       }
     }
     if (threadIdx.x == 0 && failed && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
-    rows_sync();
+    __syncthreads();
   }
 }
 
@@ -594,13 +645,14 @@ static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
+template <int D, bool E4M3>
+static int launch_rows_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
+  return rows <= 16 ? launch_rows<D, E4M3, 1>(A, maps, st) : launch_rows<D, E4M3, 2>(A, maps, st);
+}
+
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  if (A.C.D == 128) {
-    if (e4m3) return rows <= 16 ? launch_rows<128, true, 1>(A, maps, st) : rows <= 32 ? launch_rows<128, true, 2>(A, maps, st) : launch_rows<128, true, 4>(A, maps, st);
-    return rows <= 16 ? launch_rows<128, false, 1>(A, maps, st) : rows <= 32 ? launch_rows<128, false, 2>(A, maps, st) : launch_rows<128, false, 4>(A, maps, st);
-  }
-  if (e4m3) return rows <= 16 ? launch_rows<64, true, 1>(A, maps, st) : rows <= 32 ? launch_rows<64, true, 2>(A, maps, st) : launch_rows<64, true, 4>(A, maps, st);
-  return rows <= 16 ? launch_rows<64, false, 1>(A, maps, st) : rows <= 32 ? launch_rows<64, false, 2>(A, maps, st) : launch_rows<64, false, 4>(A, maps, st);
+  if (A.C.D == 128) return e4m3 ? launch_rows_of<128, true>(A, rows, maps, st) : launch_rows_of<128, false>(A, rows, maps, st);
+  return e4m3 ? launch_rows_of<64, true>(A, rows, maps, st) : launch_rows_of<64, false>(A, rows, maps, st);
 }
 
 }  // namespace specv
