@@ -73,9 +73,9 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   A.joined = static_cast<unsigned*>(workspace);
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
   const bool e4m3 = cache->dtype == SPEC_E4M3;
-  // the longest run of positions that never leaves a page, up to a warp's 16
+  // the longest run of positions that never leaves a page, up to what a warp takes
   A.box = 1;
-  while (A.box < 16 && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
+  while (A.box < (e4m3 ? 32 : 16) && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
   CUtensorMap maps[2];
   if (A.C.pages > 0) {
     for (int i = 0; i < 2; ++i)

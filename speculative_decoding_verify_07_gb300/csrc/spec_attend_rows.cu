@@ -6,8 +6,8 @@
 // the warp-level matrix instructions deliver beside the loads; the wide
 // tcgen05 tile of 128 rows would spend its time on padding.
 //
-// The four warps of a CTA divide each tile of 64 positions, 16 each, and share
-// nothing until an item ends: every warp brings its own positions by TMA (a box
+// The four warps of a CTA divide each tile of positions, 16 each (32 of an 8-bit
+// cache: as many bytes), and share nothing until an item ends: every warp brings its own positions by TMA (a box
 // a run of positions within a page) through a ring of its own, several tiles
 // ahead and across the ends of items, and keeps its own running maximum, sum
 // and weighted values in registers.  The maximum only moves when a score
@@ -23,10 +23,8 @@
 
 namespace specv {
 
-constexpr int kRowsKT = 64;
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kRowsKeys = kRowsKT / kRowsWarps;                  // positions of a tile that a warp takes
 constexpr float kRowsSlack = 8.f;
 constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
 constexpr unsigned kRowsTop = 221;   // so the largest exponent byte whose 2^-e is a normal number; above it is NaN
@@ -34,16 +32,18 @@ constexpr unsigned kRowsTop = 221;   // so the largest exponent byte whose 2^-e 
 template <int D, bool E4M3, int MT>
 struct RowsShape {
   static constexpr int M = 16 * MT;
+  static constexpr int NK = E4M3 ? 32 : 16;                      // positions that a warp takes at a time
+  static constexpr int KT = NK * kRowsWarps;
   static constexpr int row_bytes = D * (E4M3 ? 1 : 2);
   static constexpr int halves = row_bytes > 128 ? 2 : 1;         // 128-byte columns of a row
   static constexpr int half_bytes = row_bytes / halves;
-  static constexpr int half_tile = kRowsKeys * half_bytes;
-  static constexpr int kv_tile = kRowsKeys * row_bytes;
+  static constexpr int half_tile = NK * half_bytes;
+  static constexpr int kv_tile = NK * row_bytes;
   static constexpr int stage = 2 * kv_tile;                      // of one warp
   static constexpr int q_bytes = M * D * 2;
   static constexpr int pitch = D + 8;                            // floats a row of the joined values
   static constexpr int o_bytes = M * pitch * 4;
-  static constexpr int ctas = E4M3 && MT == 1 ? 3 : 2;           // an SM
+  static constexpr int ctas = 2;          // an SM
   static constexpr int most = (225 * 1024 / ctas - 1024 - q_bytes - o_bytes - 6144) / (kRowsWarps * stage);
   static constexpr int stages = most > 6 ? 6 : most;
   static constexpr int smem = 1024 + stages * kRowsWarps * stage + q_bytes + o_bytes;
@@ -93,42 +93,40 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// What a warp brings next: its 16 positions of a tile, looked up a tile before
+// What a warp brings next: its positions of a tile, looked up a tile before
 // their copies begin.
-template <int M, bool E4M3>
+template <int M, int NK, bool E4M3>
 struct RowsFetch {
-  AttendWalk<M, kRowsKT> I;
-  int t;                 // the tile
+  AttendWalk<M, NK * kRowsWarps> I;
+  int t, limit;          // the tile, and the positions that its item sees
   bool more;
-  int page, slot;        // of position `lane`, lanes 0 to 15
+  int page, slot;        // of position `lane` (NK of them)
   uint32_t ke, ve;       // its exponents
 
-  __device__ __forceinline__ RowsFetch(const AttendArgs& A, const AttendShare& S) : I(A, S), t(0) {
+  __device__ __forceinline__ RowsFetch(const AttendArgs& A, const AttendShare& S) : I(A, S) { segment(); }
+  __device__ __forceinline__ void segment() {
     more = I.next();
     t = I.a;
+    if (more) limit = attend_sees(I.A, I.R, (min((I.qt + 1) * M, I.R.n * I.A.group) - 1) / I.A.group);
   }
   __device__ __forceinline__ void look(int warp, int lane) {
     page = -1;
     ke = ve = 0;
     if (!more) return;
     const AttendArgs& A = I.A;
-    const int limit = attend_sees(A, I.R, (min((I.qt + 1) * M, I.R.n * A.group) - 1) / A.group);
-    const int pos = t * kRowsKT + warp * kRowsKeys + lane;
-    if (lane < kRowsKeys && pos < limit) {
+    const int pos = (t * kRowsWarps + warp) * NK + lane;
+    if ((NK == 32 || lane < NK) && pos < limit) {
       page = paged_lookup(A.C, I.row, pos, &slot);
       if (page < 0 && A.flags) atomicOr(&A.flags[I.row], (uint32_t)SPEC_F_BAD_IDX);
       if (E4M3 && page >= 0) {
-        const long long e = page * A.C.exp_bytes + (long long)I.head * A.C.page_size + slot;
+        const long long e = page * A.C.exp_bytes + (unsigned)(I.head * A.C.page_size + slot);
         ke = __ldg(A.C.k_exp + e);
         ve = __ldg(A.C.v_exp + e);
       }
     }
   }
   __device__ __forceinline__ void step() {
-    if (++t >= I.b) {
-      more = I.next();
-      t = I.a;
-    }
+    if (++t >= I.b) segment();
   }
 };
 
@@ -136,10 +134,10 @@ template <int D, bool E4M3, int MT>
 __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     attend_rows_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = RowsShape<D, E4M3, MT>;
-  constexpr int M = S::M, KT = kRowsKT, NK = kRowsKeys;
+  constexpr int M = S::M, KT = S::KT, NK = S::NK, NS = NK / 16;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) unsigned long long full[kRowsWarps][S::stages];
-  __shared__ unsigned there[kRowsWarps][S::stages];                      // bits: positions of the stage that are there; NaN values
+  __shared__ unsigned there[kRowsWarps][S::stages][2];                   // bits: positions of the stage that are there; NaN values
   __shared__ __align__(8) float scales[kRowsWarps][S::stages][E4M3 ? 3 : 1][E4M3 ? NK : 1];   // keys' 2^e, values' e and 2^-e
   __shared__ AttendShare share;
   __shared__ long long sums[kRowsThreads];
@@ -160,18 +158,20 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   }
   attend_share<M, KT, kRowsThreads>(A, &share, sums);
 
-  RowsFetch<M, E4M3> F(A, share);
+  RowsFetch<M, NK, E4M3> F(A, share);
   F.look(warp, lane);
   // a box of one 64-byte row would not begin at a multiple of 128 bytes: its lane copies it
   const bool by_hand = S::half_bytes == 64 && A.box == 1;
-  const int box = min(A.box, NK), copies_of = NK / box * 2 * S::halves;
+  const int box = min(A.box, NK), copies_of = by_hand ? 0 : NK / box * 2 * S::halves;
+  const unsigned starts = by_hand ? 0u : box == 32 ? 1u : box == 16 ? 0x10001u : box == 8 ? 0x01010101u : box == 4 ? 0x11111111u : box == 2 ? 0x55555555u : ~0u;
+  constexpr unsigned all = NK == 32 ? ~0u : 0xffffu;
   auto bring = [&](int stage) {
     if (!F.more) return;
     const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
     const unsigned nans = E4M3 ? __ballot_sync(0xffffffffu, F.ve > kRowsTop) : 0;
     unsigned char* const to = ring + stage * S::stage;
-    unsigned bytes = 0;
-    if (E4M3 && lane < NK) {
+    const unsigned bytes = failed ? 0 : __popc(mask & starts & all) * (box * 2 * S::row_bytes);
+    if (E4M3) {
       float* s = &scales[warp][stage][0][0] + lane;
       s[0] = exp_value(F.ke);
       const int e = F.ve > kRowsTop ? 127 : max((int)F.ve, 1);
@@ -188,18 +188,17 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
           *reinterpret_cast<uint4*>(p + S::kv_tile) = __ldg(reinterpret_cast<const uint4*>(A.C.v + at) + c);
         }
       }
-    } else if (!failed) {
-      for (int b = 0; b < NK; b += box) bytes += (mask >> b & 1) * box * 2 * S::row_bytes;
     }
     if (lane == 0) {
-      there[warp][stage] = mask | nans << 16;
+      there[warp][stage][0] = mask;
+      there[warp][stage][1] = nans;
       mbar_arrive_expect_tx(&full[warp][stage], bytes);
     }
     __syncwarp();
     if (bytes) {
       for (int i0 = 0; i0 < copies_of; i0 += 32) {
         const int i = i0 + lane, part = i % (2 * S::halves), at = i / (2 * S::halves) * box;
-        const int page = __shfl_sync(0xffffffffu, F.page, at & 15), slot = __shfl_sync(0xffffffffu, F.slot, at & 15);
+        const int page = __shfl_sync(0xffffffffu, F.page, at % NK), slot = __shfl_sync(0xffffffffu, F.slot, at % NK);
         if (i < copies_of && page >= 0) {
           const int half = part % S::halves;
           const bool v = part >= S::halves;
@@ -296,10 +295,10 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
       mbar_await(&full[warp][stage], phase, &failed);
       unsigned char* const k_sm = ring + stage * S::stage;
       const uint32_t ks_base = smem_u32(k_sm), vs_base = ks_base + S::kv_tile;
-      const unsigned bits = there[warp][stage], mask = bits & 0xffffu;
-      if (E4M3 && bits >> 16) odd = 1;
+      const unsigned mask = there[warp][stage][0];
+      if (E4M3 && there[warp][stage][1]) odd = 1;
       const int key0 = t * KT + warp * NK;                // this warp's first position
-      const bool edge = key0 + NK > fewest || mask != 0xffffu;
+      const bool edge = key0 + NK > fewest || mask != all;
       if (edge) {
         // A value of weight zero must be finite: positions that are not there are cleared, and what is not finite of
         // those that only some rows see is cleared and remembered.
@@ -327,13 +326,15 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         if (found) odd = 1;
         __syncwarp();
       }
-      float s[MT][2][4];
+      float s[NS][MT][2][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int z = 0; z < NS; ++z)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[z][i][n][e] = 0.f;
       const uint32_t qa = smem_u32(q_sm) + lane * 16;
       if (!E4M3) {
 #pragma unroll
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
           for (int i = 0; i < MT; ++i) {
             const uint4 f = lds128(qa + (i * (D / 16) + ks) * 512);
             const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-            mma_16<false>(s[i][0], a, kb[0], kb[1]);
-            mma_16<false>(s[i][1], a, kb[2], kb[3]);
+            mma_16<false>(s[0][i][0], a, kb[0], kb[1]);
+            mma_16<false>(s[0][i][1], a, kb[2], kb[3]);
           }
         }
       } else {
@@ -354,64 +355,78 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         // which place of the sum does not matter, so its bytes 4 i .. 4 i + 3 are its four of k-step 4 j + i.
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-          uint4 kc[2];
+          uint4 kc[NS][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int k = 8 * n + r8;
-            const int c = D == 128 ? (2 * q4 + j) ^ (k & 7) : q4 ^ (k >> 1 & 3);
-            kc[n] = lds128(ks_base + k * S::row_bytes + c * 16);
-          }
+          for (int z = 0; z < NS; ++z)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int k = 16 * z + 8 * n + r8;
+              const int c = D == 128 ? (2 * q4 + j) ^ (k & 7) : q4 ^ (k >> 1 & 3);
+              kc[z][n] = lds128(ks_base + k * S::row_bytes + c * 16);
+            }
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            uint32_t kb[2][2];
+            uint32_t kb[NS][2][2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-              e4m3_f16(i4 == 0 ? kc[n].x : i4 == 1 ? kc[n].y : i4 == 2 ? kc[n].z : kc[n].w, &kb[n][0], &kb[n][1]);
+            for (int z = 0; z < NS; ++z)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+                e4m3_f16(i4 == 0 ? kc[z][n].x : i4 == 1 ? kc[z][n].y : i4 == 2 ? kc[z][n].z : kc[z][n].w, &kb[z][n][0], &kb[z][n][1]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
               const uint4 f = lds128(qa + (i * (D / 16) + 4 * j + i4) * 512);
               const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-              mma_16<true>(s[i][0], a, kb[0][0], kb[0][1]);
-              mma_16<true>(s[i][1], a, kb[1][0], kb[1][1]);
+#pragma unroll
+              for (int z = 0; z < NS; ++z) {
+                mma_16<true>(s[z][i][0], a, kb[z][0][0], kb[z][0][1]);
+                mma_16<true>(s[z][i][1], a, kb[z][1][0], kb[z][1][1]);
+              }
             }
           }
         }
       }
       // scores in powers of two (of 8-bit values: with the exponent), masked
-      float inv[2][2];
+      float inv[NS][2][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int k = 8 * n + 2 * q4;
-        float by[2] = {score_scale, score_scale}, plus[2] = {0.f, 0.f};
-        if (E4M3) {
-          const float* f = &scales[warp][stage][0][0] + k;
-          const float2 a = *reinterpret_cast<const float2*>(f), b = *reinterpret_cast<const float2*>(f + NK),
-                       c = *reinterpret_cast<const float2*>(f + 2 * NK);
-          by[0] *= a.x, by[1] *= a.y;
-          plus[0] = b.x, plus[1] = b.y;
-          inv[n][0] = c.x, inv[n][1] = c.y;
-        }
+      for (int z = 0; z < NS; ++z)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[i][n][e] = E4M3 ? fmaf(s[i][n][e], by[e & 1], plus[e & 1]) : s[i][n][e] * by[e & 1];
-            if (edge && (key0 + k + (e & 1) >= lim[i][e >> 1] || !(mask >> (k + (e & 1)) & 1))) s[i][n][e] = -INFINITY;
+        for (int n = 0; n < 2; ++n) {
+          const int k = 16 * z + 8 * n + 2 * q4;
+          float by[2] = {score_scale, score_scale}, plus[2] = {0.f, 0.f};
+          if (E4M3) {
+            const float* f = &scales[warp][stage][0][0] + k;
+            const float2 a = *reinterpret_cast<const float2*>(f), b = *reinterpret_cast<const float2*>(f + NK),
+                         c = *reinterpret_cast<const float2*>(f + 2 * NK);
+            by[0] *= a.x, by[1] *= a.y;
+            plus[0] = b.x, plus[1] = b.y;
+            inv[z][n][0] = c.x, inv[z][n][1] = c.y;
           }
-      }
-      uint32_t pa[MT][4];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& x = s[z][i][n][e];
+              x = E4M3 ? fmaf(x, by[e & 1], plus[e & 1]) : x * by[e & 1];
+              if (edge && (key0 + k + (e & 1) >= lim[i][e >> 1] || !(mask >> (k + (e & 1)) & 1))) x = -INFINITY;
+            }
+        }
+      uint32_t pa[NS][MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         float high[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          high[h] = fmaxf(fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]), fmaxf(s[i][1][2 * h], s[i][1][2 * h + 1]));
-          high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 1));
-          high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 2));
+          high[h] = fmaxf(fmaxf(s[0][i][0][2 * h], s[0][i][0][2 * h + 1]), fmaxf(s[0][i][1][2 * h], s[0][i][1][2 * h + 1]));
+#pragma unroll
+          for (int z = 1; z < NS; ++z)
+            high[h] = fmaxf(high[h], fmaxf(fmaxf(s[z][i][0][2 * h], s[z][i][0][2 * h + 1]), fmaxf(s[z][i][1][2 * h], s[z][i][1][2 * h + 1])));
         }
+        // a lane's own maximum tells whether the row's has passed; the lanes of a row agree on it only then
         if (__any_sync(0xffffffffu, high[0] > m[i][0] + kRowsSlack || high[1] > m[i][1] + kRowsSlack)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 1));
+            high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 2));
             const float to = fmaxf(m[i][h], high[h]);
             const float keep = to == -INFINITY ? 1.f : exp2_fast(m[i][h] - to);
             m[i][h] = to;
@@ -420,20 +435,22 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
             for (int d = 0; d < D / 8; ++d) o[i][d][2 * h] *= keep, o[i][d][2 * h + 1] *= keep;
           }
         }
+        const float from[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int z = 0; z < NS; ++z)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float from = m[i][h] == -INFINITY ? 0.f : m[i][h];
-            const float a = exp2_fast(s[i][n][2 * h] - from), b = exp2_fast(s[i][n][2 * h + 1] - from);
-            if (E4M3) {
-              l[i][h] = fmaf(b, inv[n][1], fmaf(a, inv[n][0], l[i][h]));
-              pa[i][2 * n + h] = pack_f16(a, b);
-            } else {
-              l[i][h] += a + b;
-              pa[i][2 * n + h] = pack_bf16(a, b);
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float a = exp2_fast(s[z][i][n][2 * h] - from[h]), b = exp2_fast(s[z][i][n][2 * h + 1] - from[h]);
+              if (E4M3) {
+                l[i][h] = fmaf(b, inv[z][n][1], fmaf(a, inv[z][n][0], l[i][h]));
+                pa[z][i][2 * n + h] = pack_f16(a, b);
+              } else {
+                l[i][h] += a + b;
+                pa[z][i][2 * n + h] = pack_bf16(a, b);
+              }
             }
-          }
       }
       if (!E4M3) {
 #pragma unroll
@@ -443,29 +460,31 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
           ldsm4_t(vb, vs_base + (d / 4) * S::half_tile + k * 128 + ((c ^ (k & 7)) << 4));
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            mma_16<false>(o[i][2 * d], pa[i], vb[0], vb[1]);
-            mma_16<false>(o[i][2 * d + 1], pa[i], vb[2], vb[3]);
+            mma_16<false>(o[i][2 * d], pa[0][i], vb[0], vb[1]);
+            mma_16<false>(o[i][2 * d + 1], pa[0][i], vb[2], vb[3]);
           }
         }
       } else {
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          // pairs of dimensions move as one 16-bit element; even and odd ones are tiles of their own
-          uint32_t vb[4];
-          const int k = (lane / 8 & 1) * 8 + lane % 8, c = 2 * d + lane / 16;
-          ldsm4_t(vb, vs_base + k * S::row_bytes + ((D == 128 ? c ^ (k & 7) : c ^ (k >> 1 & 3)) << 4));
+        for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t e0, o0, e1, o1;
-            e4m3_f16(__byte_perm(vb[2 * j], 0, 0x3120), &e0, &o0);
-            e4m3_f16(__byte_perm(vb[2 * j + 1], 0, 0x3120), &e1, &o1);
+          for (int z = 0; z < NS; ++z) {
+            // pairs of dimensions move as one 16-bit element; even and odd ones are tiles of their own
+            uint32_t vb[4];
+            const int k = 16 * z + (lane / 8 & 1) * 8 + lane % 8, c = 2 * d + lane / 16;
+            ldsm4_t(vb, vs_base + k * S::row_bytes + ((D == 128 ? c ^ (k & 7) : c ^ (k >> 1 & 3)) << 4));
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              mma_16<true>(o[i][4 * d + 2 * j], pa[i], e0, e1);
-              mma_16<true>(o[i][4 * d + 2 * j + 1], pa[i], o0, o1);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t e0, o0, e1, o1;
+              e4m3_f16(__byte_perm(vb[2 * j], 0, 0x3120), &e0, &o0);
+              e4m3_f16(__byte_perm(vb[2 * j + 1], 0, 0x3120), &e1, &o1);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                mma_16<true>(o[i][4 * d + 2 * j], pa[z][i], e0, e1);
+                mma_16<true>(o[i][4 * d + 2 * j + 1], pa[z][i], o0, o1);
+              }
             }
           }
-        }
       }
       if (edge || by_hand) fence_proxy_async();     // what was written here comes before the next copy
       __syncwarp();
