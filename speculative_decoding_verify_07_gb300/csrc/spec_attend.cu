@@ -3,6 +3,8 @@
 
 namespace specv {
 
+constexpr int kAttendRowsMost = 32;
+
 // cuTensorMapEncodeTiled, looked up once: the library does not link the driver.
 static PFN_attend_encode encoder() {
   static PFN_attend_encode fn = [] {
@@ -33,8 +35,8 @@ int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int
              : SPEC_E_CUDA;
 }
 
-// Partial results of the launch with the most: 456 CTAs of two parts of 32 rows.
-static size_t attend_parts(int D) { return (size_t)456 * 2 * 32 * (D + 2) * sizeof(float); }
+// Partial results of the launch with the most: 152 CTAs of two parts of 256 rows.
+static size_t attend_parts(int D) { return (size_t)152 * 2 * 256 * (D + 2) * sizeof(float); }
 
 }  // namespace specv
 
@@ -73,13 +75,19 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   A.joined = static_cast<unsigned*>(workspace);
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
   const bool e4m3 = cache->dtype == SPEC_E4M3;
-  // the longest run of positions that never leaves a page, up to what a warp takes
+  // A tile of 16 or 32 query rows where they suffice, of 128 or 256 where not.
+  const long long rows = (long long)max_tokens * group;
+  const bool wide = rows > kAttendRowsMost;
+  // the longest run of positions that never leaves a page, up to what is copied at a time
+  const int most = wide ? 128 : e4m3 ? 32 : 16;
   A.box = 1;
-  while (A.box < (e4m3 ? 32 : 16) && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
+  while (A.box < most && A.C.page_size % (2 * A.box) == 0) A.box *= 2;
   CUtensorMap maps[2];
   if (A.C.pages > 0) {
     for (int i = 0; i < 2; ++i)
       if (attend_map(&maps[i], i ? A.C.v : A.C.k, A.C, e4m3, A.box) != SPEC_OK) return SPEC_E_CUDA;
   }
-  return launch_attend_rows(A, e4m3, max_tokens * group, maps, reinterpret_cast<cudaStream_t>(cuda_stream));
+  const int most_rows = rows > 0x7fffffff ? 0x7fffffff : (int)rows;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  return wide ? launch_attend_wide(A, e4m3, most_rows, maps, st) : launch_attend_rows(A, e4m3, most_rows, maps, st);
 }

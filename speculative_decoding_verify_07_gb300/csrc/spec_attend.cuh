@@ -193,6 +193,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem, const CUtensorMap* ma
       : "memory");
 }
 
+// The positions of the j-th 32 of a tile at which boxes of `box` rows begin.
+__device__ __forceinline__ unsigned attend_starts(int box, int j) {
+  if (box >= 32) return j * 32 % box == 0 ? 1u : 0u;
+  return box == 16 ? 0x10001u : box == 8 ? 0x01010101u : box == 4 ? 0x11111111u : box == 2 ? 0x55555555u : ~0u;
+}
+
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -218,5 +224,6 @@ int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int
 
 // The launches.  `maps`: keys, values.
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
+int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
 
 }  // namespace specv

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   // a box of one 64-byte row would not begin at a multiple of 128 bytes: its lane copies it
   const bool by_hand = S::half_bytes == 64 && A.box == 1;
   const int box = min(A.box, NK), copies_of = by_hand ? 0 : NK / box * 2 * S::halves;
-  const unsigned starts = by_hand ? 0u : box == 32 ? 1u : box == 16 ? 0x10001u : box == 8 ? 0x01010101u : box == 4 ? 0x11111111u : box == 2 ? 0x55555555u : ~0u;
+  const unsigned starts = by_hand ? 0u : attend_starts(box, 0);
   constexpr unsigned all = NK == 32 ? ~0u : 0xffffu;
   auto bring = [&](int stage) {
     if (!F.more) return;

@@ -1,0 +1,582 @@
+// Attention of many query rows over the cache: chunks of a prompt, long drafts,
+// wide groups.
+//
+// Bound by the tensor cores: 4 D operations for each (query row, position).  A
+// CTA has one or two tiles of 128 query rows and walks the positions in tiles of
+// 128 with tcgen05: S = Q K^T into tensor memory, softmax by one thread a row,
+// P back into tensor memory over S, O += P V.  With two query tiles the matrix
+// unit works for one while the other's softmax runs.  P is bf16 (the values are;
+// it adds one rounding of 2^-9 to the weights), everything else float32.
+//
+// The maximum only moves when a row's scores pass it by 2^8, so O, which stays
+// in tensor memory, is rescaled a few times a row and not at every tile.
+//
+// Warps: four for each query tile's softmax, four that bring keys and values,
+// one that issues the matrix instructions.  A 16-bit cache comes by TMA, a box a
+// run of positions within a page, into the swizzled layout that the matrix unit
+// reads.  8-bit codes are loaded, widened to bf16 with their power-of-two scale
+// (exact) and stored in the same layout, so the rest of the kernel is the same.
+#include "spec_attend.cuh"
+
+namespace specv {
+
+constexpr int kWideKT = 128;
+constexpr float kWideSlack = 8.f;
+
+template <int D, bool E4M3, int QT>
+struct WideShape {
+  static constexpr int M = 128 * QT;
+  static constexpr int halves = D / 64;                       // 128-byte columns of a bf16 row
+  static constexpr int half_tile = kWideKT * 128;
+  static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
+  // what is left of the 227 KB after Q, the alignment and the small arrays
+  static constexpr int most = (227 * 1024 - 1024 - (E4M3 ? 3072 : 768) - QT * tile) / (2 * tile);
+  static constexpr int stages = most > 4 ? 4 : most;
+  static constexpr int smem = 1024 + QT * tile + stages * 2 * tile;
+  static constexpr int threads = QT * 128 + 128 + 32;
+  static constexpr int columns = QT * 128 + QT * D <= 256 ? 256 : 512;   // of tensor memory
+  static constexpr int part_floats = M * (D + 2);
+};
+
+// Shared-memory operand with 128-byte swizzle: address, distance between
+// 64-element columns (of a transposed operand) and between groups of 8 rows.
+__device__ __forceinline__ uint64_t wide_desc(uint32_t smem, uint32_t columns) {
+  return (uint64_t)((smem >> 4) & 0x3fff) | (uint64_t)(columns >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// bf16 x bf16 -> float32, 128 rows by n columns.
+__device__ __forceinline__ constexpr uint32_t wide_instr(int n, bool b_transposed) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_transposed ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(unsigned long long* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float exp2_wide(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two e4m3 codes in the upper bytes of 16-bit halves, as bf16 times `scale` (a
+// power of two in both halves).  The code's bits, shifted, are a bf16 number
+// 2^-120 too small; both products are exact.
+__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t high, uint32_t scale) {
+  uint32_t w = ((high >> 4) & 0x07f007f0u) | (high & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7b807b80u));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(scale));
+  return w;
+}
+
+struct WideBars {
+  unsigned long long k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
+  unsigned long long s_full[2], p_full[2], o_full[2], q_full;
+};
+
+template <int D, bool E4M3, int QT>
+__global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
+    attend_wide_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using S = WideShape<D, E4M3, QT>;
+  constexpr int M = S::M, KT = kWideKT, ST = S::stages;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) WideBars bar;
+  __shared__ unsigned there[8][4];       // which positions of the tile are there, for the last eight tiles
+  __shared__ AttendShare share;
+  __shared__ long long row_at[E4M3 ? KT : 1];         // 8-bit cache: where a position's codes are
+  __shared__ uint32_t row_scale[2][E4M3 ? KT : 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed, odd, strange_now, last_part, first_nan;
+  unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* const k_sm = base + QT * S::tile;
+  unsigned char* const v_sm = k_sm + ST * S::tile;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int bring_warp = QT * 4, mma_warp = QT * 4 + 4;
+
+  if (threadIdx.x == 0) {
+    failed = odd = 0;
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.k_full[i], E4M3 ? 128 : 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_ready[i], E4M3 ? 128 : 96);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    mbar_init(&bar.q_full, QT * 128);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == mma_warp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "n"(S::columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tmem_before();
+  }
+  attend_share<M, KT, S::threads>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
+  fence_proxy_async();
+  tmem_after();
+  const uint32_t tmem = tmem_base;
+  AttendWalk<M, KT> W(A, share);
+
+  if (warp >= bring_warp && warp < mma_warp) {
+    // ------------------------------------------------------ keys and values
+    int n = 0;                                   // tiles so far
+    const int tid = threadIdx.x - bring_warp * 32;
+    while (W.next()) {
+      const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
+      const int fewest = attend_sees(A, W.R, W.qt * M / A.group);
+      for (int t = W.a; t < W.b; ++t, ++n) {
+        const int st = n % ST;
+        const uint32_t again = (n / ST & 1) ^ 1;
+        if (E4M3) {
+          // one position a thread: where it is and its scales
+          const int pos = t * KT + tid;
+          int slot = 0;
+          const int page = pos < limit ? paged_lookup(A.C, W.row, pos, &slot) : -1;
+          const unsigned mask = __ballot_sync(0xffffffffu, page >= 0);
+          uint32_t ke = 127, ve = 127;
+          long long at = -1;
+          if (page >= 0) {
+            const long long e = page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot;
+            ke = A.C.k_exp[e];
+            ve = A.C.v_exp[e];
+            at = page * A.C.page_bytes + ((long long)W.head * A.C.page_size + slot) * D;
+            if (ve > 254) odd = 1;
+          } else if (pos < limit && A.flags) {
+            atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+          }
+          if (lane == 0) there[n & 7][tid / 32] = mask;
+          asm volatile("bar.sync 2, 128;" ::: "memory");      // the last tile's rows have been read
+          row_at[E4M3 ? tid : 0] = at;
+          // bf16's exponent is the byte itself; values of NaN are cleared here and handled at the end
+          row_scale[0][E4M3 ? tid : 0] = (ke > 254 ? 0x7fc0u : max(ke, 1u) << 7) * 0x10001u;
+          row_scale[1][E4M3 ? tid : 0] = (ve > 254 ? 0u : max(ve, 1u) << 7) * 0x10001u;
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          constexpr int chunks = D / 16, per = KT * chunks / 128;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint4 w[per];
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+              const int row = (i * 128 + tid) / chunks, c = tid % chunks;
+              const long long from = row_at[E4M3 ? row : 0];
+              w[i] = make_uint4(0, 0, 0, 0);
+              if (from >= 0) w[i] = __ldcg(reinterpret_cast<const uint4*>((v ? A.C.v : A.C.k) + from) + c);
+            }
+            mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], again, &failed);
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+              const int row = (i * 128 + tid) / chunks, c = tid % chunks;
+              const uint32_t scale = row_scale[v][E4M3 ? row : 0];
+              unsigned char* to = (v ? v_sm : k_sm) + st * S::tile + c / 4 * S::half_tile + row * 128;
+              const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[2 * j] = e4m3_bf16(__byte_perm(x[j], 0, 0x1404), scale);
+                y[2 * j + 1] = e4m3_bf16(__byte_perm(x[j], 0, 0x3424), scale);
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint4*>(to + (((c % 4 * 2 + j) ^ (row & 7)) << 4)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            }
+            fence_proxy_async();
+            mbar_arrive(v ? &bar.v_ready[st] : &bar.k_full[st]);
+          }
+        } else if (warp == bring_warp) {
+          // copies: this lane's positions, then its boxes
+          int page[4], slot[4];
+          unsigned mask[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int pos = t * KT + 32 * j + lane;
+            slot[j] = 0;
+            page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &slot[j]) : -1;
+            if (page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+            mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
+          }
+          if (lane < 4) there[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
+          const int boxes = KT / A.box;
+          unsigned copies = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) copies += __popc(mask[j] & attend_starts(A.box, j));
+          const uint32_t bytes = failed ? 0 : copies * A.box * D * 2;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            unsigned long long* full = v ? &bar.v_full[st] : &bar.k_full[st];
+            mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], again, &failed);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            const uint32_t to = smem_u32((v ? v_sm : k_sm) + st * S::tile);
+            for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
+              const int at = ((b0 + lane) * A.box) & 127, from = at & 31;
+              int p = -1, s = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
+                if (at / 32 == j) p = pj, s = sj;
+              }
+              if (b0 + lane < boxes && p >= 0) {
+#pragma unroll
+                for (int h = 0; h < S::halves; ++h)
+                  tma_load_4d(to + h * S::half_tile + at * 128, v ? &vmap : &kmap, h * 64, s, W.head, p, full);
+              }
+            }
+          }
+        } else {
+          // three warps see that no value of weight zero can be NaN: positions that are not there are cleared, and
+          // what is not finite of those that only some rows see is cleared and remembered
+          mbar_await(&bar.v_full[st], n / ST & 1, &failed);
+          const unsigned* mask = there[n & 7];
+          if ((t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u) {
+            bool found = false;
+            for (int i = tid - 32; i < KT * S::halves * 8; i += 96) {
+              const int k = i / (S::halves * 8), c = i % (S::halves * 8);
+              unsigned char* p = v_sm + st * S::tile + c / 8 * S::half_tile + k * 128 + (c % 8) * 16;   // any order of a row's columns
+              if (!(mask[k / 32] >> (k & 31) & 1)) {
+                *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+              } else if (t * KT + k >= fewest) {
+                uint4 w = *reinterpret_cast<uint4*>(p);
+                uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+                bool bad = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if ((x[j] & 0x7f80u) == 0x7f80u) x[j] &= 0xffff0000u, bad = true;
+                  if ((x[j] & 0x7f800000u) == 0x7f800000u) x[j] &= 0xffffu, bad = true;
+                }
+                if (bad) *reinterpret_cast<uint4*>(p) = w;
+                found = found || bad;
+              }
+            }
+            if (found) odd = 1;
+            fence_proxy_async();
+          }
+          mbar_arrive(&bar.v_ready[st]);
+        }
+      }
+    }
+  } else if (warp == mma_warp) {
+    // ----------------------------------------------------- matrix products
+    int n = 0, segment = 0;
+    uint32_t p_phase = 0;
+    constexpr uint32_t s_instr = wide_instr(KT, false), o_instr = wide_instr(D, true);
+    auto scores = [&](int qt, int st) {
+      if (lane == 0) {
+        const uint64_t a = wide_desc(smem_u32(base + qt * S::tile), 0), b = wide_desc(smem_u32(k_sm + st * S::tile), 0);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t at = (k / 4 * S::half_tile + k % 4 * 32) >> 4;
+          mma_ss(tmem + qt * 128, a + at, b + at, s_instr, k > 0);
+        }
+        mma_commit(&bar.s_full[qt]);
+      }
+    };
+    while (W.next()) {
+      mbar_await(&bar.q_full, segment & 1, &failed);
+      mbar_await(&bar.k_full[n % ST], n / ST & 1, &failed);
+      tmem_after();
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) scores(qt, n % ST);
+      if (lane == 0) mma_commit(&bar.k_empty[n % ST]);
+      for (int t = W.a; t < W.b; ++t, ++n) {
+        const int st = n % ST, st1 = (n + 1) % ST;
+        const bool more = t + 1 < W.b;
+        mbar_await(&bar.v_ready[st], n / ST & 1, &failed);
+        if (more) mbar_await(&bar.k_full[st1], (n + 1) / ST & 1, &failed);
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+          mbar_await(&bar.p_full[qt], p_phase, &failed);
+          tmem_after();
+          if (lane == 0) {
+            const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+              mma_ts(tmem + QT * 128 + qt * D, tmem + qt * 128 + k * 8, b + (k * 2048 >> 4), o_instr, t > W.a || k > 0);
+            mma_commit(&bar.o_full[qt]);
+          }
+          if (more) scores(qt, st1);
+        }
+        if (lane == 0) {
+          mma_commit(&bar.v_empty[st]);
+          if (more) mma_commit(&bar.k_empty[st1]);
+        }
+        p_phase ^= 1;
+      }
+      ++segment;
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int qt = warp / 4, row = threadIdx.x % 128;            // query tile, and this thread's row of it
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16), s_at = lanes + qt * 128, o_at = lanes + QT * 128 + qt * D;
+    const float scale = A.scale_log2;
+    int n = 0;
+    while (W.next()) {
+      const int mine = W.qt * M + qt * 128 + row, rows = W.R.n * A.group;
+      const bool real = mine < rows;
+      const int token = min(mine, rows - 1) / A.group, head = W.head * A.group + min(mine, rows - 1) - token * A.group;
+      const int lim = attend_sees(A, W.R, token), fewest = attend_sees(A, W.R, min(W.qt * M + qt * 128, rows - 1) / A.group);
+      {
+        // the scores of the last tile have been waited for, so Q may be replaced
+        unsigned char* to = base + qt * S::tile + row * 128;
+        const uint4* q = reinterpret_cast<const uint4*>(A.q + (W.R.first + token) * A.q_token + (long long)head * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(to + c / 8 * S::half_tile + (((c % 8) ^ (row & 7)) << 4)) = real ? q[c] : make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+        mbar_arrive(&bar.q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int t = W.a; t < W.b; ++t, ++n) {
+        mbar_await(&bar.s_full[qt], n & 1, &failed);
+        tmem_after();
+        const unsigned* mask = there[n & 7];
+        const bool edge = (t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u;
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tmem_ld32(s_at + c * 32, s);
+          const unsigned seen = edge ? mask[c] & (lim - t * KT - c * 32 >= 32 ? ~0u : lim - t * KT - c * 32 <= 0 ? 0u : (1u << (lim - t * KT - c * 32)) - 1) : ~0u;
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, seen >> i & 1 ? __uint_as_float(s[i]) * scale : -INFINITY);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]) * scale);
+          }
+        }
+        float keep = 1.f;
+        if (top > m + kWideSlack) {
+          keep = exp2_wide(m - top);
+          m = top;
+        }
+        if (__any_sync(0xffffffffu, keep != 1.f)) {
+          l *= keep;
+          if (t > W.a) {
+            mbar_await(&bar.o_full[qt], (n - 1) & 1, &failed);
+            tmem_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st32(o_at + c * 32, o);
+            }
+          }
+        }
+        const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32], p[16];
+          tmem_ld32(s_at + c * 32, s);
+          const unsigned seen = edge ? mask[c] & (lim - t * KT - c * 32 >= 32 ? ~0u : lim - t * KT - c * 32 <= 0 ? 0u : (1u << (lim - t * KT - c * 32)) - 1) : ~0u;
+          tmem_wait_ld();
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float a = exp2_wide(fmaf(__uint_as_float(s[i]), scale, -from)), b = exp2_wide(fmaf(__uint_as_float(s[i + 1]), scale, -from));
+            if (edge) {
+              a = seen >> i & 1 ? a : 0.f;
+              b = seen >> (i + 1) & 1 ? b : 0.f;
+            }
+            sum[i / 2 % 4] += a + b;
+            p[i / 2] = pack_bf16(a, b);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st16(s_at + c * 16, p);
+        }
+        tmem_wait_st();
+        tmem_before();
+        mbar_arrive(&bar.p_full[qt]);
+      }
+      // ------------------------------------------------------------ the end
+      mbar_await(&bar.o_full[qt], (n - 1) & 1, &failed);
+      tmem_after();
+      asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+      if (threadIdx.x == 0) {
+        strange_now = odd;
+        first_nan = 0x7fffffff;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+      const bool strange = strange_now;        // the same for all, whatever the next tiles bring
+      const int k1 = min(lim, W.b * KT);
+      int bad_from = 0x7fffffff;          // 8-bit cache: the first value of NaN
+      if (strange) {
+        if (E4M3) {
+          for (int k = W.a * KT + threadIdx.x; k < W.b * KT; k += QT * 128) {
+            int slot;
+            const int page = k < attend_sees(A, W.R, W.R.n - 1) ? paged_lookup(A.C, W.row, k, &slot) : -1;
+            if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > 254) atomicMin(&first_nan, k);
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+        bad_from = first_nan;
+      }
+      const bool whole = W.whole();
+      const long long item = W.item_begin();
+      const int c0 = whole ? 0 : share_of(share.total, item, share.ctas);
+      const int c1 = whole ? 0 : share_of(share.total, item + W.tiles - 1, share.ctas);
+      float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
+      const long long out_row = (long long)(W.R.first + token) * A.hq + head;
+      const float inv = l == 0.f ? 1.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(o_at + c * 32, r);
+        tmem_wait_ld();
+        float* o = reinterpret_cast<float*>(r);
+        if (strange) {
+          if (E4M3) {
+            if (bad_from < k1)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
+          } else {
+            for (int k = max(attend_sees(A, W.R, W.qt * M / A.group), W.a * KT); k < k1; ++k) {
+              int slot;
+              const int page = paged_lookup(A.C, W.row, k, &slot);
+              if (page < 0) continue;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D + c * 32;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x = __uint_as_float((uint32_t)v[i] << 16);
+                if (!isfinite(x)) o[i] += x;
+              }
+            }
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            __stcg(reinterpret_cast<float4*>(part + (qt * 128 + row) * D + c * 32 + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        } else if (real) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(A.out + out_row * D + c * 32 + i) =
+                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+        }
+      }
+      if (whole && real && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      if (!whole) {
+        __stcg(part + M * D + qt * 128 + row, m);
+        __stcg(part + M * D + M + qt * 128 + row, l);
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+        if (threadIdx.x == 0) {
+          const unsigned had = atomicAdd(&A.joined[c0], 1u);
+          last_part = had == (unsigned)(c1 - c0);
+          if (last_part) A.joined[c0] = 0;
+          __threadfence();
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+        if (last_part && real) {
+          float high = -INFINITY, sum = 0.f;
+          for (int c = c0; c <= c1; ++c) high = fmaxf(high, __ldcg(A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats + M * D + qt * 128 + row));
+          const float ref = high == -INFINITY ? 0.f : high;
+          for (int c = c0; c <= c1; ++c) {
+            const float* p = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats + M * D + qt * 128 + row;
+            sum += __ldcg(p + M) * exp2_wide(__ldcg(p) - ref);
+          }
+          const float by = sum == 0.f ? 1.f : 1.f / sum;
+          for (int d = 0; d < D; d += 8) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int c = c0; c <= c1; ++c) {
+              const float* p = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats;
+              const float f = exp2_wide(__ldcg(p + M * D + qt * 128 + row) - ref);
+              const float4 a = __ldcg(reinterpret_cast<const float4*>(p + (qt * 128 + row) * D + d));
+              const float4 b = __ldcg(reinterpret_cast<const float4*>(p + (qt * 128 + row) * D + d + 4));
+              x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
+              x[4] += b.x * f, x[5] += b.y * f, x[6] += b.z * f, x[7] += b.w * f;
+            }
+            *reinterpret_cast<uint4*>(A.out + out_row * D + d) =
+                make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
+                           pack_bf16(x[6] * by, x[7] * by));
+          }
+          if (A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      if (failed && threadIdx.x == 0 && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
+      tmem_before();
+    }
+  }
+  tmem_before();
+  __syncthreads();
+  if (warp == mma_warp) {
+    tmem_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::columns) : "memory");
+  }
+}
+
+template <int D, bool E4M3, int QT>
+static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_t st) {
+  using S = WideShape<D, E4M3, QT>;
+  static_assert(S::stages >= 2, "a ring needs two stages");
+  const auto kernel = attend_wide_kernel<D, E4M3, QT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_E_CUDA;
+  }
+  kernel<<<152, S::threads, S::smem, st>>>(A, maps[0], maps[1]);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
+}
+
+template <int D, bool E4M3>
+static int launch_wide_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
+  return rows <= 128 ? launch_wide<D, E4M3, 1>(A, maps, st) : launch_wide<D, E4M3, 2>(A, maps, st);
+}
+
+int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st) {
+  if (A.C.D == 128) return e4m3 ? launch_wide_of<128, true>(A, rows, maps, st) : launch_wide_of<128, false>(A, rows, maps, st);
+  return e4m3 ? launch_wide_of<64, true>(A, rows, maps, st) : launch_wide_of<64, false>(A, rows, maps, st);
+}
+
+}  // namespace specv
