@@ -2,20 +2,23 @@
 // wide groups.
 //
 // Bound by the tensor cores: 4 D operations for each (query row, position).  A
-// CTA has one or two tiles of 128 query rows and walks the positions in tiles of
-// 128 with tcgen05: S = Q K^T into tensor memory, softmax by one thread a row,
-// P back into tensor memory over S, O += P V.  With two query tiles the matrix
-// unit works for one while the other's softmax runs.  P is bf16 (the values are;
+// CTA walks the positions in tiles of 128 with tcgen05: S = Q K^T into tensor
+// memory, softmax by one thread a row, P back into tensor memory over S,
+// O += P V.  Two groups of four softmax warps keep the matrix unit busy, which
+// works for one while the other computes: on two tiles of 128 query rows, or,
+// where the item has no more than 128, on every other tile of positions of the
+// same rows, with two O that are joined at the end.  P is bf16 (the values are;
 // it adds one rounding of 2^-9 to the weights), everything else float32.
 //
 // The maximum only moves when a row's scores pass it by 2^8, so O, which stays
 // in tensor memory, is rescaled a few times a row and not at every tile.
 //
-// Warps: four for each query tile's softmax, four that bring keys and values,
-// one that issues the matrix instructions.  A 16-bit cache comes by TMA, a box a
-// run of positions within a page, into the swizzled layout that the matrix unit
-// reads.  8-bit codes are loaded, widened to bf16 with their power-of-two scale
-// (exact) and stored in the same layout, so the rest of the kernel is the same.
+// Warps: eight for softmax, which take registers from the others to hold a row
+// of S; four that bring keys and values; one that issues the matrix
+// instructions.  A 16-bit cache comes by TMA, a box a run of positions within a
+// page, into the swizzled layout that the matrix unit reads.  8-bit codes are
+// loaded, widened to bf16 with their power-of-two scale (exact) and stored in
+// the same layout, so the rest of the kernel is the same.
 #include "spec_attend.cuh"
 
 namespace specv {
@@ -23,20 +26,24 @@ namespace specv {
 constexpr int kWideKT = 128;
 constexpr float kWideSlack = 8.f;
 
-template <int D, bool E4M3, int QT>
+template <int D, bool E4M3, bool SPLIT>
 struct WideShape {
+  static constexpr int QT = SPLIT ? 1 : 2;                    // tiles of query rows
   static constexpr int M = 128 * QT;
   static constexpr int halves = D / 64;                       // 128-byte columns of a bf16 row
   static constexpr int half_tile = kWideKT * 128;
   static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
   // what is left of the 227 KB after Q, the alignment and the small arrays
-  static constexpr int most = (227 * 1024 - 1024 - (E4M3 ? 3072 : 768) - QT * tile) / (2 * tile);
+  static constexpr int most = (227 * 1024 - 1024 - (E4M3 ? 2560 : 512) - QT * tile) / (2 * tile);
   static constexpr int stages = most > 4 ? 4 : most;
   static constexpr int smem = 1024 + QT * tile + stages * 2 * tile;
-  static constexpr int threads = QT * 128 + 128 + 32;
-  static constexpr int columns = QT * 128 + QT * D <= 256 ? 256 : 512;   // of tensor memory
+  static constexpr int columns = 512;                         // of tensor memory: two S of 128, two O of D
   static constexpr int part_floats = M * (D + 2);
 };
+
+constexpr int kWideThreads = 512;      // two groups of softmax warps, one that brings, one of which a warp multiplies
+// A group's registers: 2 * 128 * (184 + 72) = 512 * 128, what the block was launched with.
+constexpr int kWideMore = 184, kWideLess = 72;
 
 // Shared-memory operand with 128-byte swizzle: address, distance between
 // 64-element columns (of a transposed operand) and between groups of 8 rows.
@@ -76,15 +83,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
-      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
@@ -101,6 +105,22 @@ __device__ __forceinline__ float exp2_wide(float x) {
   return y;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ void wide_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
+
 // Two e4m3 codes in the upper bytes of 16-bit halves, as bf16 times `scale` (a
 // power of two in both halves).  The code's bits, shifted, are a bf16 number
 // 2^-120 too small; both products are exact.
@@ -116,11 +136,11 @@ struct WideBars {
   unsigned long long s_full[2], p_full[2], o_full[2], q_full;
 };
 
-template <int D, bool E4M3, int QT>
-__global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
+template <int D, bool E4M3, bool SPLIT>
+__global__ void __launch_bounds__(kWideThreads, 1)
     attend_wide_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using S = WideShape<D, E4M3, QT>;
-  constexpr int M = S::M, KT = kWideKT, ST = S::stages;
+  using S = WideShape<D, E4M3, SPLIT>;
+  constexpr int M = S::M, KT = kWideKT, ST = S::stages, QT = S::QT;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) WideBars bar;
   __shared__ unsigned there[8][4];       // which positions of the tile are there, for the last eight tiles
@@ -133,7 +153,7 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
   unsigned char* const k_sm = base + QT * S::tile;
   unsigned char* const v_sm = k_sm + ST * S::tile;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int bring_warp = QT * 4, mma_warp = QT * 4 + 4;
+  constexpr int bring_warp = 8, mma_warp = 12;
 
   if (threadIdx.x == 0) {
     failed = odd = 0;
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tmem_before();
   }
-  attend_share<M, KT, S::threads>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
+  attend_share<M, KT, kWideThreads>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
   fence_proxy_async();
   tmem_after();
   const uint32_t tmem = tmem_base;
@@ -165,6 +185,7 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
 
   if (warp >= bring_warp && warp < mma_warp) {
     // ------------------------------------------------------ keys and values
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLess));
     int n = 0;                                   // tiles so far
     const int tid = threadIdx.x - bring_warp * 32;
     while (W.next()) {
@@ -301,97 +322,112 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
         }
       }
     }
-  } else if (warp == mma_warp) {
-    // ----------------------------------------------------- matrix products
-    int n = 0, segment = 0;
-    uint32_t p_phase = 0;
-    constexpr uint32_t s_instr = wide_instr(KT, false), o_instr = wide_instr(D, true);
-    auto scores = [&](int qt, int st) {
-      if (lane == 0) {
-        const uint64_t a = wide_desc(smem_u32(base + qt * S::tile), 0), b = wide_desc(smem_u32(k_sm + st * S::tile), 0);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t at = (k / 4 * S::half_tile + k % 4 * 32) >> 4;
-          mma_ss(tmem + qt * 128, a + at, b + at, s_instr, k > 0);
+  } else if (warp >= mma_warp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLess));
+    if (warp == mma_warp) {
+      // ----------------------------------------------------- matrix products
+      // Step i of a segment is for group i % 2: two steps a tile, or one.
+      int n = 0, segment = 0;
+      uint32_t p_phase[2] = {0, 0};
+      constexpr uint32_t s_instr = wide_instr(KT, false), o_instr = wide_instr(D, true);
+      constexpr int per = SPLIT ? 1 : 2;
+      auto scores = [&](int step) {
+        const int group = step & 1, at_n = n + step / per, st = at_n % ST;
+        mbar_await(&bar.k_full[st], at_n / ST & 1, &failed);
+        tmem_after();
+        if (lane == 0) {
+          const uint64_t a = wide_desc(smem_u32(base + (SPLIT ? 0 : group) * S::tile), 0), b = wide_desc(smem_u32(k_sm + st * S::tile), 0);
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t at = (k / 4 * S::half_tile + k % 4 * 32) >> 4;
+            mma_ss(tmem + group * 128, a + at, b + at, s_instr, k > 0);
+          }
+          mma_commit(&bar.s_full[group]);
+          if (SPLIT || group == 1) mma_commit(&bar.k_empty[st]);
         }
-        mma_commit(&bar.s_full[qt]);
-      }
-    };
-    while (W.next()) {
-      mbar_await(&bar.q_full, segment & 1, &failed);
-      mbar_await(&bar.k_full[n % ST], n / ST & 1, &failed);
-      tmem_after();
-#pragma unroll
-      for (int qt = 0; qt < QT; ++qt) scores(qt, n % ST);
-      if (lane == 0) mma_commit(&bar.k_empty[n % ST]);
-      for (int t = W.a; t < W.b; ++t, ++n) {
-        const int st = n % ST, st1 = (n + 1) % ST;
-        const bool more = t + 1 < W.b;
-        mbar_await(&bar.v_ready[st], n / ST & 1, &failed);
-        if (more) mbar_await(&bar.k_full[st1], (n + 1) / ST & 1, &failed);
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-          mbar_await(&bar.p_full[qt], p_phase, &failed);
+      };
+      while (W.next()) {
+        mbar_await(&bar.q_full, segment & 1, &failed);
+        const int steps = (W.b - W.a) * per;
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int step = 0; step < steps; ++step) {
+          const int group = step & 1, at_n = n + step / per, st = at_n % ST;
+          mbar_await(&bar.v_ready[st], at_n / ST & 1, &failed);
+          mbar_await(&bar.p_full[group], p_phase[group], &failed);
+          p_phase[group] ^= 1;
           tmem_after();
           if (lane == 0) {
             const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
-#pragma unroll
+  #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
-              mma_ts(tmem + QT * 128 + qt * D, tmem + qt * 128 + k * 8, b + (k * 2048 >> 4), o_instr, t > W.a || k > 0);
-            mma_commit(&bar.o_full[qt]);
+              mma_ts(tmem + 256 + group * D, tmem + group * 128 + k * 8, b + (k * 2048 >> 4), o_instr, step > 1 || k > 0);
+            mma_commit(&bar.o_full[group]);
+            if (SPLIT || group == 1) mma_commit(&bar.v_empty[st]);
           }
-          if (more) scores(qt, st1);
+          if (step + 2 < steps) scores(step + 2);
         }
-        if (lane == 0) {
-          mma_commit(&bar.v_empty[st]);
-          if (more) mma_commit(&bar.k_empty[st1]);
-        }
-        p_phase ^= 1;
+        n += W.b - W.a;
+        ++segment;
       }
-      ++segment;
     }
   } else {
     // -------------------------------------------------------------- softmax
-    const int qt = warp / 4, row = threadIdx.x % 128;            // query tile, and this thread's row of it
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16), s_at = lanes + qt * 128, o_at = lanes + QT * 128 + qt * D;
-    const float scale = A.scale_log2;
-    int n = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideMore));
+    const int group = warp / 4, row = threadIdx.x % 128, qt = SPLIT ? 0 : group;   // this thread's row of its query tile
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16), s_at = lanes + group * 128, o_at = lanes + 256;
+    // a negative scale turns the queries' signs, so the largest score is that of the largest product
+    const float scale = fabsf(A.scale_log2);
+    const uint32_t turn = A.scale_log2 < 0.f ? 0x80008000u : 0u;
+    float* const stats = reinterpret_cast<float*>(base);
+    int done = 0, n = 0;          // this group's steps so far; tiles
     while (W.next()) {
       const int mine = W.qt * M + qt * 128 + row, rows = W.R.n * A.group;
       const bool real = mine < rows;
       const int token = min(mine, rows - 1) / A.group, head = W.head * A.group + min(mine, rows - 1) - token * A.group;
       const int lim = attend_sees(A, W.R, token), fewest = attend_sees(A, W.R, min(W.qt * M + qt * 128, rows - 1) / A.group);
-      {
-        // the scores of the last tile have been waited for, so Q may be replaced
+      if (!SPLIT || group == 0) {
+        // the products with the last Q are done: their results have been waited for
         unsigned char* to = base + qt * S::tile + row * 128;
         const uint4* q = reinterpret_cast<const uint4*>(A.q + (W.R.first + token) * A.q_token + (long long)head * D);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(to + c / 8 * S::half_tile + (((c % 8) ^ (row & 7)) << 4)) = real ? q[c] : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 w = real ? q[c] : make_uint4(0, 0, 0, 0);
+          w.x ^= turn, w.y ^= turn, w.z ^= turn, w.w ^= turn;
+          *reinterpret_cast<uint4*>(to + c / 8 * S::half_tile + (((c % 8) ^ (row & 7)) << 4)) = w;
+        }
         fence_proxy_async();
         mbar_arrive(&bar.q_full);
       }
       float m = -INFINITY, l = 0.f;
-      for (int t = W.a; t < W.b; ++t, ++n) {
-        mbar_await(&bar.s_full[qt], n & 1, &failed);
+      const int began = done;
+      for (int t = W.a + (SPLIT ? group : 0); t < W.b; t += SPLIT ? 2 : 1, ++done) {
+        mbar_await(&bar.s_full[group], done & 1, &failed);
         tmem_after();
-        const unsigned* mask = there[n & 7];
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
+        const unsigned* mask = there[(n + t - W.a) & 7];
         const bool edge = (t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u;
-        float top = -INFINITY;
+        unsigned seen[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld32(s_at + c * 32, s);
-          const unsigned seen = edge ? mask[c] & (lim - t * KT - c * 32 >= 32 ? ~0u : lim - t * KT - c * 32 <= 0 ? 0u : (1u << (lim - t * KT - c * 32)) - 1) : ~0u;
-          tmem_wait_ld();
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, seen >> i & 1 ? __uint_as_float(s[i]) * scale : -INFINITY);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]) * scale);
-          }
+          const int left = lim - t * KT - c * 32;
+          seen[c] = mask[c] & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1);
         }
+        tmem_wait_ld();
+        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) high[i & 3] = fmaxf(high[i & 3], seen[i / 32] >> (i & 31) & 1 ? __uint_as_float(s[i]) : -INFINITY);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) high[j] = fmaxf(high[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
+        }
+        float top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+        if (top != -INFINITY) top *= scale;
         float keep = 1.f;
         if (top > m + kWideSlack) {
           keep = exp2_wide(m - top);
@@ -399,67 +435,83 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
         }
         if (__any_sync(0xffffffffu, keep != 1.f)) {
           l *= keep;
-          if (t > W.a) {
-            mbar_await(&bar.o_full[qt], (n - 1) & 1, &failed);
+          if (done > began) {
+            mbar_await(&bar.o_full[group], (done - 1) & 1, &failed);
             tmem_after();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_at + c * 32, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_at + group * D + c * 16, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-              tmem_st32(o_at + c * 32, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st16(o_at + group * D + c * 16, o);
             }
           }
         }
-        const float from = m == -INFINITY ? 0.f : m;
+        const float from = m == -INFINITY ? 0.f : -m;
+        const float2 scale2 = make_float2(scale, scale), from2 = make_float2(from, from);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32], p[16];
-          tmem_ld32(s_at + c * 32, s);
-          const unsigned seen = edge ? mask[c] & (lim - t * KT - c * 32 >= 32 ? ~0u : lim - t * KT - c * 32 <= 0 ? 0u : (1u << (lim - t * KT - c * 32)) - 1) : ~0u;
-          tmem_wait_ld();
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            float a = exp2_wide(fmaf(__uint_as_float(s[i]), scale, -from)), b = exp2_wide(fmaf(__uint_as_float(s[i + 1]), scale, -from));
+            float2 x = fma2(make_float2(__uint_as_float(s[c * 32 + i]), __uint_as_float(s[c * 32 + i + 1])), scale2, from2);
+            x.x = exp2_wide(x.x);
+            x.y = exp2_wide(x.y);
             if (edge) {
-              a = seen >> i & 1 ? a : 0.f;
-              b = seen >> (i + 1) & 1 ? b : 0.f;
+              x.x = seen[c] >> i & 1 ? x.x : 0.f;
+              x.y = seen[c] >> (i + 1) & 1 ? x.y : 0.f;
             }
-            sum[i / 2 % 4] += a + b;
-            p[i / 2] = pack_bf16(a, b);
+            sum[i / 2 & 1] = add2(sum[i / 2 & 1], x);
+            p[i / 2] = pack_bf16(x.x, x.y);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st16(s_at + c * 16, p);
         }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tmem_before();
-        mbar_arrive(&bar.p_full[qt]);
+        mbar_arrive(&bar.p_full[group]);
       }
+      n += W.b - W.a;
       // ------------------------------------------------------------ the end
-      mbar_await(&bar.o_full[qt], (n - 1) & 1, &failed);
+      if (done > began) mbar_await(&bar.o_full[group], (done - 1) & 1, &failed);
       tmem_after();
-      asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+      if (SPLIT) {
+        wide_sync();            // the other group's products with Q are done too: its place is free until the next item
+        stats[group * 256 + row] = m;
+        stats[group * 256 + 128 + row] = l;
+      }
+      wide_sync();
       if (threadIdx.x == 0) {
         strange_now = odd;
         first_nan = 0x7fffffff;
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+      wide_sync();
       const bool strange = strange_now;        // the same for all, whatever the next tiles bring
       const int k1 = min(lim, W.b * KT);
-      int bad_from = 0x7fffffff;          // 8-bit cache: the first value of NaN
-      if (strange) {
-        if (E4M3) {
-          for (int k = W.a * KT + threadIdx.x; k < W.b * KT; k += QT * 128) {
-            int slot;
-            const int page = k < attend_sees(A, W.R, W.R.n - 1) ? paged_lookup(A.C, W.row, k, &slot) : -1;
-            if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > 254) atomicMin(&first_nan, k);
-          }
+      if (strange && E4M3) {
+        for (int k = W.a * KT + threadIdx.x; k < W.b * KT; k += 256) {
+          int slot;
+          const int page = k < attend_sees(A, W.R, W.R.n - 1) ? paged_lookup(A.C, W.row, k, &slot) : -1;
+          if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > 254) atomicMin(&first_nan, k);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
-        bad_from = first_nan;
+        wide_sync();
+      }
+      // this thread's columns of its row: all of them, or half of what two groups have
+      constexpr int cols = SPLIT ? D / 2 : D;
+      const int d0 = SPLIT ? group * cols : 0;
+      float f0 = 1.f, f1 = 0.f;
+      bool two = false;
+      if (SPLIT) {
+        const float m0 = stats[row], m1 = stats[256 + row];
+        two = W.b - W.a > 1;
+        m = two ? fmaxf(m0, m1) : m0;
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = exp2_wide(m0 - ref);
+        f1 = exp2_wide(m1 - ref);
+        l = stats[128 + row] * f0 + (two ? stats[384 + row] * f1 : 0.f);
       }
       const bool whole = W.whole();
       const long long item = W.item_begin();
@@ -469,14 +521,22 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
       const long long out_row = (long long)(W.R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < cols / 32; ++c) {
+        const int d = d0 + c * 32;
         uint32_t r[32];
-        tmem_ld32(o_at + c * 32, r);
+        tmem_ld32(o_at + (SPLIT ? 0 : group * D) + d, r);
         tmem_wait_ld();
         float* o = reinterpret_cast<float*>(r);
+        if (SPLIT) {
+          uint32_t r1[32];
+          if (two) tmem_ld32(o_at + D + d, r1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + (two ? __uint_as_float(r1[i]) * f1 : 0.f);
+        }
         if (strange) {
           if (E4M3) {
-            if (bad_from < k1)
+            if (first_nan < k1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
           } else {
@@ -484,7 +544,7 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
               int slot;
               const int page = paged_lookup(A.C, W.row, k, &slot);
               if (page < 0) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D + c * 32;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D + d;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float x = __uint_as_float((uint32_t)v[i] << 16);
@@ -493,31 +553,35 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
             }
           }
         }
-        if (!whole) {
+        if (!real) {
+          // (rows of padding)
+        } else if (!whole) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            __stcg(reinterpret_cast<float4*>(part + (qt * 128 + row) * D + c * 32 + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
-        } else if (real) {
+            __stcg(reinterpret_cast<float4*>(part + (qt * 128 + row) * D + d + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(A.out + out_row * D + c * 32 + i) =
+            *reinterpret_cast<uint4*>(A.out + out_row * D + d + i) =
                 make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
                            pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
         }
       }
-      if (whole && real && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      if (whole && real && d0 == 0 && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       if (!whole) {
-        __stcg(part + M * D + qt * 128 + row, m);
-        __stcg(part + M * D + M + qt * 128 + row, l);
+        if (real && d0 == 0) {
+          __stcg(part + M * D + qt * 128 + row, m);
+          __stcg(part + M * D + M + qt * 128 + row, l);
+        }
         __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+        wide_sync();
         if (threadIdx.x == 0) {
           const unsigned had = atomicAdd(&A.joined[c0], 1u);
           last_part = had == (unsigned)(c1 - c0);
           if (last_part) A.joined[c0] = 0;
           __threadfence();
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(QT * 128) : "memory");
+        wide_sync();
         if (last_part && real) {
           float high = -INFINITY, sum = 0.f;
           for (int c = c0; c <= c1; ++c) high = fmaxf(high, __ldcg(A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats + M * D + qt * 128 + row));
@@ -527,7 +591,7 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
             sum += __ldcg(p + M) * exp2_wide(__ldcg(p) - ref);
           }
           const float by = sum == 0.f ? 1.f : 1.f / sum;
-          for (int d = 0; d < D; d += 8) {
+          for (int d = d0; d < d0 + cols; d += 8) {
             float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             for (int c = c0; c <= c1; ++c) {
               const float* p = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats;
@@ -541,11 +605,12 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
                 make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
                            pack_bf16(x[6] * by, x[7] * by));
           }
-          if (A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
+          if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
         }
       }
       if (failed && threadIdx.x == 0 && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
       tmem_before();
+      if (SPLIT) wide_sync();      // both O have been read before either is written again
     }
   }
   tmem_before();
@@ -556,22 +621,22 @@ __global__ void __launch_bounds__(WideShape<D, E4M3, QT>::threads, 1)
   }
 }
 
-template <int D, bool E4M3, int QT>
+template <int D, bool E4M3, bool SPLIT>
 static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_t st) {
-  using S = WideShape<D, E4M3, QT>;
+  using S = WideShape<D, E4M3, SPLIT>;
   static_assert(S::stages >= 2, "a ring needs two stages");
-  const auto kernel = attend_wide_kernel<D, E4M3, QT>;
+  const auto kernel = attend_wide_kernel<D, E4M3, SPLIT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess) {
     cudaGetLastError();
     return SPEC_E_CUDA;
   }
-  kernel<<<152, S::threads, S::smem, st>>>(A, maps[0], maps[1]);
+  kernel<<<152, kWideThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
 template <int D, bool E4M3>
 static int launch_wide_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  return rows <= 128 ? launch_wide<D, E4M3, 1>(A, maps, st) : launch_wide<D, E4M3, 2>(A, maps, st);
+  return rows <= 128 ? launch_wide<D, E4M3, true>(A, maps, st) : launch_wide<D, E4M3, false>(A, maps, st);
 }
 
 int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st) {
