@@ -33,10 +33,12 @@ struct WideShape {
   static constexpr int halves = D / 64;                       // 128-byte columns of a bf16 row
   static constexpr int half_tile = kWideKT * 128;
   static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
-  // what is left of the 227 KB after Q, the alignment and the small arrays
-  static constexpr int most = (227 * 1024 - 1024 - (E4M3 ? 2560 : 512) - QT * tile) / (2 * tile);
-  static constexpr int stages = most > 4 ? 4 : most;
-  static constexpr int smem = 1024 + QT * tile + stages * 2 * tile;
+  // what is left of the 227 KB after Q, the alignment and the small arrays, in tiles: keys have the odd one, they are
+  // waited for first
+  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 3072 : 1024) - QT * tile) / tile;
+  static constexpr int k_stages = (room + 1) / 2 > 4 ? 4 : (room + 1) / 2;
+  static constexpr int v_stages = room / 2 > 4 ? 4 : room / 2;
+  static constexpr int smem = 1024 + (QT + k_stages + v_stages) * tile;
   static constexpr int columns = 512;                         // of tensor memory: two S of 128, two O of D
   static constexpr int part_floats = M * (D + 2);
 };
@@ -67,6 +69,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
       : "memory");
+}
+// One thread of the converged warp, and known to the compiler as one: operands
+// of the matrix instructions then go straight to uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -140,10 +149,10 @@ template <int D, bool E4M3, bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads, 1)
     attend_wide_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = WideShape<D, E4M3, SPLIT>;
-  constexpr int M = S::M, KT = kWideKT, ST = S::stages, QT = S::QT;
+  constexpr int M = S::M, KT = kWideKT, KST = S::k_stages, VST = S::v_stages, QT = S::QT;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) WideBars bar;
-  __shared__ unsigned there[8][4];       // which positions of the tile are there, for the last eight tiles
+  __shared__ unsigned there[8][4], v_there[8][4];      // which positions of the tile are there, for the last eight tiles
   __shared__ AttendShare share;
   __shared__ long long row_at[E4M3 ? KT : 1];         // 8-bit cache: where a position's codes are
   __shared__ uint32_t row_scale[2][E4M3 ? KT : 1];
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ int failed, odd, strange_now, last_part, first_nan;
   unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   unsigned char* const k_sm = base + QT * S::tile;
-  unsigned char* const v_sm = k_sm + ST * S::tile;
+  unsigned char* const v_sm = k_sm + KST * S::tile;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr int bring_warp = 8, mma_warp = 12;
 
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(&bar.k_full[i], E4M3 ? 128 : 1);
       mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.v_full[i], 1);
-      mbar_init(&bar.v_ready[i], E4M3 ? 128 : 96);
+      mbar_init(&bar.v_ready[i], E4M3 ? 128 : 64);
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -188,12 +197,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLess));
     int n = 0;                                   // tiles so far
     const int tid = threadIdx.x - bring_warp * 32;
+    int next_page[4], next_slot[4];              // 16-bit cache: this lane's positions of the next tile
+    auto look = [&](int t, int limit) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int pos = t * KT + 32 * j + lane;
+        next_slot[j] = 0;
+        next_page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &next_slot[j]) : -1;
+        if (next_page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+      }
+    };
     while (W.next()) {
       const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
       const int fewest = attend_sees(A, W.R, W.qt * M / A.group);
+      if (!E4M3 && warp < bring_warp + 2) look(W.a, limit);
       for (int t = W.a; t < W.b; ++t, ++n) {
-        const int st = n % ST;
-        const uint32_t again = (n / ST & 1) ^ 1;
+        const int kst = n % KST, vst = n % VST;
+        const uint32_t k_again = (n / KST & 1) ^ 1, v_again = (n / VST & 1) ^ 1;
         if (E4M3) {
           // one position a thread: where it is and its scales
           const int pos = t * KT + tid;
@@ -229,12 +249,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               w[i] = make_uint4(0, 0, 0, 0);
               if (from >= 0) w[i] = __ldcg(reinterpret_cast<const uint4*>((v ? A.C.v : A.C.k) + from) + c);
             }
-            mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], again, &failed);
+            mbar_await(v ? &bar.v_empty[vst] : &bar.k_empty[kst], v ? v_again : k_again, &failed);
 #pragma unroll
             for (int i = 0; i < per; ++i) {
               const int row = (i * 128 + tid) / chunks, c = tid % chunks;
               const uint32_t scale = row_scale[v][E4M3 ? row : 0];
-              unsigned char* to = (v ? v_sm : k_sm) + st * S::tile + c / 4 * S::half_tile + row * 128;
+              unsigned char* to = (v ? v_sm + vst * S::tile : k_sm + kst * S::tile) + c / 4 * S::half_tile + row * 128;
               const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
               uint32_t y[8];
 #pragma unroll
@@ -247,59 +267,54 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 *reinterpret_cast<uint4*>(to + (((c % 4 * 2 + j) ^ (row & 7)) << 4)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
             }
             fence_proxy_async();
-            mbar_arrive(v ? &bar.v_ready[st] : &bar.k_full[st]);
+            mbar_arrive(v ? &bar.v_ready[vst] : &bar.k_full[kst]);
           }
-        } else if (warp == bring_warp) {
-          // copies: this lane's positions, then its boxes
+        } else if (warp < bring_warp + 2) {
+          // one warp copies keys, one values: this lane's positions, then its boxes
+          const bool v = warp > bring_warp;
           int page[4], slot[4];
-          unsigned mask[4];
+          unsigned mask[4], copies = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int pos = t * KT + 32 * j + lane;
-            slot[j] = 0;
-            page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &slot[j]) : -1;
-            if (page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+            page[j] = next_page[j];
+            slot[j] = next_slot[j];
             mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
+            copies += __popc(mask[j] & attend_starts(A.box, j));
           }
-          if (lane < 4) there[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
+          if (t + 1 < W.b) look(t + 1, limit);
+          if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
           const int boxes = KT / A.box;
-          unsigned copies = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) copies += __popc(mask[j] & attend_starts(A.box, j));
           const uint32_t bytes = failed ? 0 : copies * A.box * D * 2;
+          unsigned long long* full = v ? &bar.v_full[vst] : &bar.k_full[kst];
+          mbar_await(v ? &bar.v_empty[vst] : &bar.k_empty[kst], v ? v_again : k_again, &failed);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          const uint32_t to = smem_u32(v ? v_sm + vst * S::tile : k_sm + kst * S::tile);
+          for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
+            const int at = ((b0 + lane) * A.box) & 127, from = at & 31;
+            int p = -1, s = 0;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            unsigned long long* full = v ? &bar.v_full[st] : &bar.k_full[st];
-            mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], again, &failed);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
-            const uint32_t to = smem_u32((v ? v_sm : k_sm) + st * S::tile);
-            for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
-              const int at = ((b0 + lane) * A.box) & 127, from = at & 31;
-              int p = -1, s = 0;
+            for (int j = 0; j < 4; ++j) {
+              const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
+              if (at / 32 == j) p = pj, s = sj;
+            }
+            if (b0 + lane < boxes && p >= 0) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
-                if (at / 32 == j) p = pj, s = sj;
-              }
-              if (b0 + lane < boxes && p >= 0) {
-#pragma unroll
-                for (int h = 0; h < S::halves; ++h)
-                  tma_load_4d(to + h * S::half_tile + at * 128, v ? &vmap : &kmap, h * 64, s, W.head, p, full);
-              }
+              for (int h = 0; h < S::halves; ++h)
+                tma_load_4d(to + h * S::half_tile + at * 128, v ? &vmap : &kmap, h * 64, s, W.head, p, full);
             }
           }
         } else {
-          // three warps see that no value of weight zero can be NaN: positions that are not there are cleared, and
+          // two warps see that no value of weight zero can be NaN: positions that are not there are cleared, and
           // what is not finite of those that only some rows see is cleared and remembered
-          mbar_await(&bar.v_full[st], n / ST & 1, &failed);
-          const unsigned* mask = there[n & 7];
+          mbar_await(&bar.v_full[vst], n / VST & 1, &failed);
+          const unsigned* mask = v_there[n & 7];
           if ((t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u) {
             bool found = false;
-            for (int i = tid - 32; i < KT * S::halves * 8; i += 96) {
+            for (int i = tid - 64; i < KT * S::halves * 8; i += 64) {
               const int k = i / (S::halves * 8), c = i % (S::halves * 8);
-              unsigned char* p = v_sm + st * S::tile + c / 8 * S::half_tile + k * 128 + (c % 8) * 16;   // any order of a row's columns
+              unsigned char* p = v_sm + vst * S::tile + c / 8 * S::half_tile + k * 128 + (c % 8) * 16;   // any order of a row's columns
               if (!(mask[k / 32] >> (k & 31) & 1)) {
                 *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
               } else if (t * KT + k >= fewest) {
@@ -318,7 +333,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (found) odd = 1;
             fence_proxy_async();
           }
-          mbar_arrive(&bar.v_ready[st]);
+          mbar_arrive(&bar.v_ready[vst]);
         }
       }
     }
@@ -327,15 +342,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (warp == mma_warp) {
       // ----------------------------------------------------- matrix products
       // Step i of a segment is for group i % 2: two steps a tile, or one.
+      const bool leader = elect_one();
       int n = 0, segment = 0;
       uint32_t p_phase[2] = {0, 0};
       constexpr uint32_t s_instr = wide_instr(KT, false), o_instr = wide_instr(D, true);
       constexpr int per = SPLIT ? 1 : 2;
       auto scores = [&](int step) {
-        const int group = step & 1, at_n = n + step / per, st = at_n % ST;
-        mbar_await(&bar.k_full[st], at_n / ST & 1, &failed);
+        const int group = step & 1, at_n = n + step / per, st = at_n % KST;
+        mbar_await(&bar.k_full[st], at_n / KST & 1, &failed);
         tmem_after();
-        if (lane == 0) {
+        if (leader) {
           const uint64_t a = wide_desc(smem_u32(base + (SPLIT ? 0 : group) * S::tile), 0), b = wide_desc(smem_u32(k_sm + st * S::tile), 0);
   #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -352,12 +368,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         scores(0);
         if (steps > 1) scores(1);
         for (int step = 0; step < steps; ++step) {
-          const int group = step & 1, at_n = n + step / per, st = at_n % ST;
-          mbar_await(&bar.v_ready[st], at_n / ST & 1, &failed);
+          const int group = step & 1, at_n = n + step / per, st = at_n % VST;
+          mbar_await(&bar.v_ready[st], at_n / VST & 1, &failed);
           mbar_await(&bar.p_full[group], p_phase[group], &failed);
           p_phase[group] ^= 1;
           tmem_after();
-          if (lane == 0) {
+          if (leader) {
             const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
   #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
@@ -558,7 +574,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         } else if (!whole) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            __stcg(reinterpret_cast<float4*>(part + (qt * 128 + row) * D + d + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            __stcg(reinterpret_cast<float4*>(part) + (d + i) / 4 * M + qt * 128 + row, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
@@ -591,19 +607,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sum += __ldcg(p + M) * exp2_wide(__ldcg(p) - ref);
           }
           const float by = sum == 0.f ? 1.f : 1.f / sum;
-          for (int d = d0; d < d0 + cols; d += 8) {
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          // neighbouring threads have neighbouring rows, and a part keeps four columns of all rows together
+#pragma unroll 1
+          for (int d = d0; d < d0 + cols; d += 32) {
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
               const float* p = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats;
+              float4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = __ldcg(reinterpret_cast<const float4*>(p) + (d / 4 + i) * M + qt * 128 + row);
               const float f = exp2_wide(__ldcg(p + M * D + qt * 128 + row) - ref);
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(p + (qt * 128 + row) * D + d));
-              const float4 b = __ldcg(reinterpret_cast<const float4*>(p + (qt * 128 + row) * D + d + 4));
-              x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
-              x[4] += b.x * f, x[5] += b.y * f, x[6] += b.z * f, x[7] += b.w * f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i].x += y[i].x * f, x[i].y += y[i].y * f, x[i].z += y[i].z * f, x[i].w += y[i].w * f;
             }
-            *reinterpret_cast<uint4*>(A.out + out_row * D + d) =
-                make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
-                           pack_bf16(x[6] * by, x[7] * by));
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              *reinterpret_cast<uint4*>(A.out + out_row * D + d + 4 * i) =
+                  make_uint4(pack_bf16(x[i].x * by, x[i].y * by), pack_bf16(x[i].z * by, x[i].w * by),
+                             pack_bf16(x[i + 1].x * by, x[i + 1].y * by), pack_bf16(x[i + 1].z * by, x[i + 1].w * by));
           }
           if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
         }
@@ -624,7 +648,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 template <int D, bool E4M3, bool SPLIT>
 static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_t st) {
   using S = WideShape<D, E4M3, SPLIT>;
-  static_assert(S::stages >= 2, "a ring needs two stages");
+  static_assert(S::v_stages >= 2, "a ring needs two stages");
   const auto kernel = attend_wide_kernel<D, E4M3, SPLIT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess) {
     cudaGetLastError();
