@@ -20,7 +20,7 @@ static PFN_attend_encode encoder() {
   return fn;
 }
 
-int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box) {
+int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box, bool swizzled) {
   const PFN_attend_encode encode = encoder();
   if (!encode) return SPEC_E_CUDA;
   const cuuint64_t es = e4m3 ? 1 : 2, row = C.D * es;
@@ -29,7 +29,8 @@ int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int
   const cuuint32_t width = (cuuint32_t)(row > 128 ? 128 : row);
   const cuuint32_t boxes[4] = {(cuuint32_t)(width / es), (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
   return encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, boxes,
-                ones, CU_TENSOR_MAP_INTERLEAVE_NONE, width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? SPEC_OK
              : SPEC_E_CUDA;
@@ -85,7 +86,7 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   CUtensorMap maps[2];
   if (A.C.pages > 0) {
     for (int i = 0; i < 2; ++i)
-      if (attend_map(&maps[i], i ? A.C.v : A.C.k, A.C, e4m3, A.box) != SPEC_OK) return SPEC_E_CUDA;
+      if (attend_map(&maps[i], i ? A.C.v : A.C.k, A.C, e4m3, A.box, !(wide && e4m3)) != SPEC_OK) return SPEC_E_CUDA;
   }
   const int most_rows = rows > 0x7fffffff ? 0x7fffffff : (int)rows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);

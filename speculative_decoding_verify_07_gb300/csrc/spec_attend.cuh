@@ -219,8 +219,8 @@ using PFN_attend_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint
                                        CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // A tensor map of one pool: [pages, heads, page_size, head_dim], boxes of up to
-// 128 bytes by `box` rows, swizzled as their width asks.
-int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box);
+// 128 bytes by `box` rows, in the order they have or swizzled as their width asks.
+int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box, bool swizzled);
 
 // The launches.  `maps`: keys, values.
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);

@@ -14,16 +14,18 @@
 // in tensor memory, is rescaled a few times a row and not at every tile.
 //
 // Warps: eight for softmax, which take registers from the others to hold a row
-// of S; four that bring keys and values; one that issues the matrix
-// instructions.  A 16-bit cache comes by TMA, a box a run of positions within a
-// page, into the swizzled layout that the matrix unit reads.  8-bit codes are
-// loaded, widened to bf16 with their power-of-two scale (exact) and stored in
-// the same layout, so the rest of the kernel is the same.
+// of S; one that issues the matrix instructions; one each that copies keys and
+// values by TMA, a box a run of positions within a page; four that make the
+// copies ready.  A 16-bit cache lands in the swizzled layout that the matrix unit
+// reads, and only the values at the edge of what rows see are looked over.  8-bit
+// codes land in half of their stage and are widened in place to bf16 with their
+// power-of-two scale (exact), so the rest of the kernel is the same.
 #include "spec_attend.cuh"
 
 namespace specv {
 
 constexpr int kWideKT = 128;
+constexpr int kNowhere = 0x7fffffff;
 constexpr float kWideSlack = 8.f;
 
 template <int D, bool E4M3, bool SPLIT>
@@ -35,7 +37,7 @@ struct WideShape {
   static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
   // what is left of the 227 KB after Q, the alignment and the small arrays, in tiles: keys have the odd one, they are
   // waited for first
-  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 3072 : 1024) - QT * tile) / tile;
+  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 2560 : 1024) - QT * tile) / tile;
   static constexpr int k_stages = (room + 1) / 2 > 4 ? 4 : (room + 1) / 2;
   static constexpr int v_stages = room / 2 > 4 ? 4 : room / 2;
   static constexpr int smem = 1024 + (QT + k_stages + v_stages) * tile;
@@ -130,19 +132,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ void wide_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
 
-// Two e4m3 codes in the upper bytes of 16-bit halves, as bf16 times `scale` (a
+// Two e4m3 codes in the upper bytes of 16-bit halves as bf16, times `scale` (a
 // power of two in both halves).  The code's bits, shifted, are a bf16 number
-// 2^-120 too small; both products are exact.
+// 2^-120 of its size, which the scale makes up for; the product is exact.
 __device__ __forceinline__ uint32_t e4m3_bf16(uint32_t high, uint32_t scale) {
   uint32_t w = ((high >> 4) & 0x07f007f0u) | (high & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7b807b80u));
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(scale));
   return w;
 }
+constexpr uint32_t kWideExp = 134;     // the largest exponent byte whose scale, times 2^120, is a bf16 number
 
 struct WideBars {
-  unsigned long long k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-  unsigned long long s_full[2], p_full[2], o_full[2], q_full;
+  unsigned long long k_raw[4], k_full[4], k_empty[4];      // keys: codes copied, ready, read
+  unsigned long long v_raw[4], v_full[4], v_empty[4];      // values: copied, ready, read
+  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2];
 };
 
 template <int D, bool E4M3, bool SPLIT>
@@ -154,31 +157,35 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ __align__(8) WideBars bar;
   __shared__ unsigned there[8][4], v_there[8][4];      // which positions of the tile are there, for the last eight tiles
   __shared__ AttendShare share;
-  __shared__ long long row_at[E4M3 ? KT : 1];         // 8-bit cache: where a position's codes are
-  __shared__ uint32_t row_scale[2][E4M3 ? KT : 1];
+  __shared__ uint8_t exps[2][4][E4M3 ? KT : 1];       // 8-bit cache: a stage's exponents, 0 where nothing is
   __shared__ uint32_t tmem_base;
-  __shared__ int failed, odd, strange_now, last_part, first_nan;
+  __shared__ int failed, last_part;
+  __shared__ int odd_at[16];     // for the last items: the first position whose value is not finite, where that needs care
   unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   unsigned char* const k_sm = base + QT * S::tile;
   unsigned char* const v_sm = k_sm + KST * S::tile;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int bring_warp = 8, mma_warp = 12;
+  constexpr int ready_warp = 8, mma_warp = 12, k_warp = 13, v_warp = 14;
+  // one 64-byte row of codes would not begin at a multiple of 128 bytes, where a copy has to land: such rows lie apart
+  const int pitch = D == 64 && A.box == 1 ? 128 : D;
 
   if (threadIdx.x == 0) {
-    failed = odd = 0;
+    failed = 0;
+    for (int i = 0; i < 16; ++i) odd_at[i] = kNowhere;
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.k_raw[i], 1);
       mbar_init(&bar.k_full[i], E4M3 ? 128 : 1);
       mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.v_full[i], 1);
-      mbar_init(&bar.v_ready[i], E4M3 ? 128 : 64);
+      mbar_init(&bar.v_raw[i], 1);
+      mbar_init(&bar.v_full[i], 128);
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 128);
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 128);
       mbar_init(&bar.o_full[i], 1);
     }
-    mbar_init(&bar.q_full, QT * 128);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == mma_warp) {
@@ -192,127 +199,65 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = tmem_base;
   AttendWalk<M, KT> W(A, share);
 
-  if (warp >= bring_warp && warp < mma_warp) {
-    // ------------------------------------------------------ keys and values
+  if (warp >= ready_warp && warp < mma_warp) {
+    // --------------------------------------------- keys and values made ready
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLess));
-    int n = 0;                                   // tiles so far
-    const int tid = threadIdx.x - bring_warp * 32;
-    int next_page[4], next_slot[4];              // 16-bit cache: this lane's positions of the next tile
-    auto look = [&](int t, int limit) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int pos = t * KT + 32 * j + lane;
-        next_slot[j] = 0;
-        next_page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &next_slot[j]) : -1;
-        if (next_page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
-      }
-    };
+    int n = 0, segment = 0;                      // tiles and items so far
+    const int tid = threadIdx.x - ready_warp * 32;
     while (W.next()) {
-      const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
       const int fewest = attend_sees(A, W.R, W.qt * M / A.group);
-      if (!E4M3 && warp < bring_warp + 2) look(W.a, limit);
+      if (tid == 0) odd_at[(segment + 6) & 15] = kNowhere;     // (no warp is six items ahead of another)
       for (int t = W.a; t < W.b; ++t, ++n) {
         const int kst = n % KST, vst = n % VST;
-        const uint32_t k_again = (n / KST & 1) ^ 1, v_again = (n / VST & 1) ^ 1;
         if (E4M3) {
-          // one position a thread: where it is and its scales
-          const int pos = t * KT + tid;
-          int slot = 0;
-          const int page = pos < limit ? paged_lookup(A.C, W.row, pos, &slot) : -1;
-          const unsigned mask = __ballot_sync(0xffffffffu, page >= 0);
-          uint32_t ke = 127, ve = 127;
-          long long at = -1;
-          if (page >= 0) {
-            const long long e = page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot;
-            ke = A.C.k_exp[e];
-            ve = A.C.v_exp[e];
-            at = page * A.C.page_bytes + ((long long)W.head * A.C.page_size + slot) * D;
-            if (ve > 254) odd = 1;
-          } else if (pos < limit && A.flags) {
-            atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
-          }
-          if (lane == 0) there[n & 7][tid / 32] = mask;
-          asm volatile("bar.sync 2, 128;" ::: "memory");      // the last tile's rows have been read
-          row_at[E4M3 ? tid : 0] = at;
-          // bf16's exponent is the byte itself; values of NaN are cleared here and handled at the end
-          row_scale[0][E4M3 ? tid : 0] = (ke > 254 ? 0x7fc0u : max(ke, 1u) << 7) * 0x10001u;
-          row_scale[1][E4M3 ? tid : 0] = (ve > 254 ? 0u : max(ve, 1u) << 7) * 0x10001u;
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          constexpr int chunks = D / 16, per = KT * chunks / 128;
-#pragma unroll
+#pragma unroll 1
           for (int v = 0; v < 2; ++v) {
-            uint4 w[per];
+            unsigned char* const tile = v ? v_sm + vst * S::tile : k_sm + kst * S::tile;
+            const uint8_t* const ex = exps[v][v ? vst : kst];
+            mbar_await(v ? &bar.v_raw[vst] : &bar.k_raw[kst], (v ? n / VST : n / KST) & 1, &failed);
+            // The codes lie in the last 128 D bytes of the stage (in all of it where rows lie apart).  Of 128 dimensions
+            // the first 64 go to the other half as they are read; what goes where codes lie is read first.
+            unsigned char* const codes = tile + (S::halves - 1) * S::half_tile;
 #pragma unroll
-            for (int i = 0; i < per; ++i) {
-              const int row = (i * 128 + tid) / chunks, c = tid % chunks;
-              const long long from = row_at[E4M3 ? row : 0];
-              w[i] = make_uint4(0, 0, 0, 0);
-              if (from >= 0) w[i] = __ldcg(reinterpret_cast<const uint4*>((v ? A.C.v : A.C.k) + from) + c);
-            }
-            mbar_await(v ? &bar.v_empty[vst] : &bar.k_empty[kst], v ? v_again : k_again, &failed);
+            for (int h = 0; h < S::halves; ++h) {
+              uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < per; ++i) {
-              const int row = (i * 128 + tid) / chunks, c = tid % chunks;
-              const uint32_t scale = row_scale[v][E4M3 ? row : 0];
-              unsigned char* to = (v ? v_sm + vst * S::tile : k_sm + kst * S::tile) + c / 4 * S::half_tile + row * 128;
-              const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-              uint32_t y[8];
+              for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (i * 32 + tid / 4) * pitch + h * 64 + tid % 4 * 16);
+              if (h == S::halves - 1) asm volatile("bar.sync 2, 128;" ::: "memory");
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y[2 * j] = e4m3_bf16(__byte_perm(x[j], 0, 0x1404), scale);
-                y[2 * j + 1] = e4m3_bf16(__byte_perm(x[j], 0, 0x3424), scale);
+              for (int i = 0; i < 4; ++i) {
+                const int row = i * 32 + tid / 4;
+                const uint32_t e = ex[E4M3 ? row : 0];
+                const uint32_t scale = (e == 0 ? 0u : e > 254 ? 0x7fc0u : (min(e, kWideExp) + 120) << 7) * 0x10001u;
+                uint32_t y[8];
+                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  y[2 * j] = e4m3_bf16(__byte_perm(x[j], 0, 0x1404), scale);
+                  y[2 * j + 1] = e4m3_bf16(__byte_perm(x[j], 0, 0x3424), scale);
+                }
+                if (__any_sync(0xffffffffu, e > kWideExp)) {
+                  const uint32_t rest = (e > kWideExp && e < 255 ? e - kWideExp + 127 : 127u) * 0x00800080u;
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[j]) : "r"(rest));
+                }
+                unsigned char* const to = tile + h * S::half_tile + row * 128;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  *reinterpret_cast<uint4*>(to + (((tid % 4 * 2 + j) ^ (row & 7)) << 4)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
               }
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint4*>(to + (((c % 4 * 2 + j) ^ (row & 7)) << 4)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
             }
             fence_proxy_async();
-            mbar_arrive(v ? &bar.v_ready[vst] : &bar.k_full[kst]);
-          }
-        } else if (warp < bring_warp + 2) {
-          // one warp copies keys, one values: this lane's positions, then its boxes
-          const bool v = warp > bring_warp;
-          int page[4], slot[4];
-          unsigned mask[4], copies = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            page[j] = next_page[j];
-            slot[j] = next_slot[j];
-            mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
-            copies += __popc(mask[j] & attend_starts(A.box, j));
-          }
-          if (t + 1 < W.b) look(t + 1, limit);
-          if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
-          const int boxes = KT / A.box;
-          const uint32_t bytes = failed ? 0 : copies * A.box * D * 2;
-          unsigned long long* full = v ? &bar.v_full[vst] : &bar.k_full[kst];
-          mbar_await(v ? &bar.v_empty[vst] : &bar.k_empty[kst], v ? v_again : k_again, &failed);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          const uint32_t to = smem_u32(v ? v_sm + vst * S::tile : k_sm + kst * S::tile);
-          for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
-            const int at = ((b0 + lane) * A.box) & 127, from = at & 31;
-            int p = -1, s = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
-              if (at / 32 == j) p = pj, s = sj;
-            }
-            if (b0 + lane < boxes && p >= 0) {
-#pragma unroll
-              for (int h = 0; h < S::halves; ++h)
-                tma_load_4d(to + h * S::half_tile + at * 128, v ? &vmap : &kmap, h * 64, s, W.head, p, full);
-            }
+            mbar_arrive(v ? &bar.v_full[vst] : &bar.k_full[kst]);
           }
         } else {
-          // two warps see that no value of weight zero can be NaN: positions that are not there are cleared, and
-          // what is not finite of those that only some rows see is cleared and remembered
-          mbar_await(&bar.v_full[vst], n / VST & 1, &failed);
+          // No value of weight zero may be NaN: positions that are not there are cleared, and what is not finite of
+          // those that only some rows see is cleared and remembered.
+          mbar_await(&bar.v_raw[vst], n / VST & 1, &failed);
           const unsigned* mask = v_there[n & 7];
           if ((t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u) {
-            bool found = false;
-            for (int i = tid - 64; i < KT * S::halves * 8; i += 64) {
+            int found = kNowhere;
+            for (int i = tid; i < KT * S::halves * 8; i += 128) {
               const int k = i / (S::halves * 8), c = i % (S::halves * 8);
               unsigned char* p = v_sm + vst * S::tile + c / 8 * S::half_tile + k * 128 + (c % 8) * 16;   // any order of a row's columns
               if (!(mask[k / 32] >> (k & 31) & 1)) {
@@ -326,20 +271,96 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                   if ((x[j] & 0x7f80u) == 0x7f80u) x[j] &= 0xffff0000u, bad = true;
                   if ((x[j] & 0x7f800000u) == 0x7f800000u) x[j] &= 0xffffu, bad = true;
                 }
-                if (bad) *reinterpret_cast<uint4*>(p) = w;
-                found = found || bad;
+                if (bad) {
+                  *reinterpret_cast<uint4*>(p) = w;
+                  found = min(found, t * KT + k);
+                }
               }
             }
-            if (found) odd = 1;
+            if (found != kNowhere) atomicMin(&odd_at[segment & 15], found);
             fence_proxy_async();
           }
-          mbar_arrive(&bar.v_ready[vst]);
+          mbar_arrive(&bar.v_full[vst]);
         }
       }
+      ++segment;
     }
   } else if (warp >= mma_warp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLess));
-    if (warp == mma_warp) {
+    if (warp == k_warp || warp == v_warp) {
+      // --------------------------------------------- copies of keys or values
+      const bool v = warp == v_warp;
+      const int stages = v ? VST : KST, boxes = KT / A.box;
+      unsigned char* const sm = v ? v_sm : k_sm;
+      const CUtensorMap* map = v ? &vmap : &kmap;
+      int n = 0, segment = 0;
+      int next_page[4], next_slot[4];            // this lane's positions of the next tile
+      uint32_t next_e[4];                        // and their exponents
+      while (W.next()) {
+        const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
+        auto look = [&](int t) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int pos = t * KT + 32 * j + lane;
+            next_slot[j] = 0;
+            next_e[j] = 0;
+            next_page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &next_slot[j]) : -1;
+            if (next_page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+            if (E4M3 && next_page[j] >= 0)
+              next_e[j] = (v ? A.C.v_exp : A.C.k_exp)[next_page[j] * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + next_slot[j])];
+          }
+        };
+        look(W.a);
+        for (int t = W.a; t < W.b; ++t, ++n) {
+          const int st = n % stages;
+          int page[4], slot[4];
+          unsigned mask[4], e[4], copies = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            page[j] = next_page[j];
+            slot[j] = next_slot[j];
+            e[j] = page[j] < 0 ? 0 : max(next_e[j], 1u);
+            mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
+            copies += __popc(mask[j] & attend_starts(A.box, j));
+          }
+          if (t + 1 < W.b) look(t + 1);
+          const uint32_t bytes = failed ? 0 : copies * A.box * D * (E4M3 ? 1 : 2);
+          unsigned long long* full = v ? &bar.v_raw[st] : E4M3 ? &bar.k_raw[st] : &bar.k_full[st];
+          mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], (n / stages & 1) ^ 1, &failed);
+          if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
+          if (E4M3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // a value of NaN is cleared here and put in at the item's end
+              if (v && e[j] > 254) atomicMin(&odd_at[segment & 15], t * KT + 32 * j + lane);
+              exps[v][st][E4M3 ? 32 * j + lane : 0] = (uint8_t)(v && e[j] > 254 ? 0 : e[j]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          const uint32_t to = smem_u32(sm + st * S::tile + (E4M3 ? (S::halves - 1) * S::half_tile : 0));
+          for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
+            const int at = ((b0 + lane) * A.box) & 127, from = at & 31;
+            int p = -1, s = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
+              if (at / 32 == j) p = pj, s = sj;
+            }
+            if (b0 + lane < boxes && p >= 0) {
+              if (E4M3) {
+                tma_load_4d(to + at * pitch, map, 0, s, W.head, p, full);
+              } else {
+#pragma unroll
+                for (int h = 0; h < S::halves; ++h) tma_load_4d(to + h * S::half_tile + at * 128, map, h * 64, s, W.head, p, full);
+              }
+            }
+          }
+        }
+        ++segment;
+      }
+    } else if (warp == mma_warp) {
       // ----------------------------------------------------- matrix products
       // Step i of a segment is for group i % 2: two steps a tile, or one.
       const bool leader = elect_one();
@@ -349,6 +370,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       constexpr int per = SPLIT ? 1 : 2;
       auto scores = [&](int step) {
         const int group = step & 1, at_n = n + step / per, st = at_n % KST;
+        if (step < per || (!SPLIT && step == 1)) mbar_await(&bar.q_full[SPLIT ? 0 : group], segment & 1, &failed);
         mbar_await(&bar.k_full[st], at_n / KST & 1, &failed);
         tmem_after();
         if (leader) {
@@ -363,13 +385,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       };
       while (W.next()) {
-        mbar_await(&bar.q_full, segment & 1, &failed);
         const int steps = (W.b - W.a) * per;
         scores(0);
         if (steps > 1) scores(1);
         for (int step = 0; step < steps; ++step) {
           const int group = step & 1, at_n = n + step / per, st = at_n % VST;
-          mbar_await(&bar.v_ready[st], at_n / VST & 1, &failed);
+          mbar_await(&bar.v_full[st], at_n / VST & 1, &failed);
           mbar_await(&bar.p_full[group], p_phase[group], &failed);
           p_phase[group] ^= 1;
           tmem_after();
@@ -396,34 +417,47 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const float scale = fabsf(A.scale_log2);
     const uint32_t turn = A.scale_log2 < 0.f ? 0x80008000u : 0u;
     float* const stats = reinterpret_cast<float*>(base);
-    int done = 0, n = 0;          // this group's steps so far; tiles
+    int done = 0, n = 0, segment = 0;          // this group's steps so far; tiles; items
+    constexpr int across = D / 8, turns = across;      // lanes a row of Q or of the result, and turns for a warp's 32 rows
     while (W.next()) {
-      const int mine = W.qt * M + qt * 128 + row, rows = W.R.n * A.group;
+      const AttendRow R = W.R;
+      const int item_row = W.row, item_head = W.head, item_qt = W.qt, item_tiles = W.tiles, item_a = W.a, item_b = W.b;
+      const bool whole = W.whole();
+      const long long item = W.item_begin();
+      const int mine = item_qt * M + qt * 128 + row, rows = R.n * A.group;
       const bool real = mine < rows;
-      const int token = min(mine, rows - 1) / A.group, head = W.head * A.group + min(mine, rows - 1) - token * A.group;
-      const int lim = attend_sees(A, W.R, token), fewest = attend_sees(A, W.R, min(W.qt * M + qt * 128, rows - 1) / A.group);
+      const int token = min(mine, rows - 1) / A.group, head = item_head * A.group + min(mine, rows - 1) - token * A.group;
+      const int lim = attend_sees(A, R, token), fewest = attend_sees(A, R, min(item_qt * M + qt * 128, rows - 1) / A.group);
       if (!SPLIT || group == 0) {
         // the products with the last Q are done: their results have been waited for
-        unsigned char* to = base + qt * S::tile + row * 128;
-        const uint4* q = reinterpret_cast<const uint4*>(A.q + (W.R.first + token) * A.q_token + (long long)head * D);
+        uint4 q[turns];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = real ? q[c] : make_uint4(0, 0, 0, 0);
-          w.x ^= turn, w.y ^= turn, w.z ^= turn, w.w ^= turn;
-          *reinterpret_cast<uint4*>(to + c / 8 * S::half_tile + (((c % 8) ^ (row & 7)) << 4)) = w;
+        for (int i = 0; i < turns; ++i) {
+          const int g = item_qt * M + qt * 128 + warp % 4 * 32 + i * (32 / across) + lane / across;
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (g < rows) {
+            const int tk = g / A.group, hd = item_head * A.group + g - tk * A.group;
+            q[i] = __ldg(reinterpret_cast<const uint4*>(A.q + (R.first + tk) * A.q_token + (long long)hd * D) + lane % across);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < turns; ++i) {
+          const int r = warp % 4 * 32 + i * (32 / across) + lane / across, c = lane % across;
+          q[i].x ^= turn, q[i].y ^= turn, q[i].z ^= turn, q[i].w ^= turn;
+          *reinterpret_cast<uint4*>(base + qt * S::tile + c / 8 * S::half_tile + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = q[i];
         }
         fence_proxy_async();
-        mbar_arrive(&bar.q_full);
+        mbar_arrive(&bar.q_full[SPLIT ? 0 : group]);
       }
       float m = -INFINITY, l = 0.f;
       const int began = done;
-      for (int t = W.a + (SPLIT ? group : 0); t < W.b; t += SPLIT ? 2 : 1, ++done) {
+      for (int t = item_a + (SPLIT ? group : 0); t < item_b; t += SPLIT ? 2 : 1, ++done) {
         mbar_await(&bar.s_full[group], done & 1, &failed);
         tmem_after();
         uint32_t s[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
-        const unsigned* mask = there[(n + t - W.a) & 7];
+        const unsigned* mask = there[(n + t - item_a) & 7];
         const bool edge = (t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u;
         unsigned seen[4];
 #pragma unroll
@@ -490,7 +524,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tmem_before();
         mbar_arrive(&bar.p_full[group]);
       }
-      n += W.b - W.a;
+      n += item_b - item_a;
       // ------------------------------------------------------------ the end
       if (done > began) mbar_await(&bar.o_full[group], (done - 1) & 1, &failed);
       tmem_after();
@@ -498,23 +532,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wide_sync();            // the other group's products with Q are done too: its place is free until the next item
         stats[group * 256 + row] = m;
         stats[group * 256 + 128 + row] = l;
-      }
-      wide_sync();
-      if (threadIdx.x == 0) {
-        strange_now = odd;
-        first_nan = 0x7fffffff;
-      }
-      wide_sync();
-      const bool strange = strange_now;        // the same for all, whatever the next tiles bring
-      const int k1 = min(lim, W.b * KT);
-      if (strange && E4M3) {
-        for (int k = W.a * KT + threadIdx.x; k < W.b * KT; k += 256) {
-          int slot;
-          const int page = k < attend_sees(A, W.R, W.R.n - 1) ? paged_lookup(A.C, W.row, k, &slot) : -1;
-          if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > 254) atomicMin(&first_nan, k);
-        }
         wide_sync();
       }
+      const int odd = odd_at[segment & 15], k1 = min(lim, item_b * KT);
       // this thread's columns of its row: all of them, or half of what two groups have
       constexpr int cols = SPLIT ? D / 2 : D;
       const int d0 = SPLIT ? group * cols : 0;
@@ -522,19 +542,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       bool two = false;
       if (SPLIT) {
         const float m0 = stats[row], m1 = stats[256 + row];
-        two = W.b - W.a > 1;
+        two = item_b - item_a > 1;
         m = two ? fmaxf(m0, m1) : m0;
         const float ref = m == -INFINITY ? 0.f : m;
         f0 = exp2_wide(m0 - ref);
         f1 = exp2_wide(m1 - ref);
         l = stats[128 + row] * f0 + (two ? stats[384 + row] * f1 : 0.f);
       }
-      const bool whole = W.whole();
-      const long long item = W.item_begin();
       const int c0 = whole ? 0 : share_of(share.total, item, share.ctas);
-      const int c1 = whole ? 0 : share_of(share.total, item + W.tiles - 1, share.ctas);
+      const int c1 = whole ? 0 : share_of(share.total, item + item_tiles - 1, share.ctas);
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
-      const long long out_row = (long long)(W.R.first + token) * A.hq + head;
+      const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
 #pragma unroll
       for (int c = 0; c < cols / 32; ++c) {
@@ -550,17 +568,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + (two ? __uint_as_float(r1[i]) * f1 : 0.f);
         }
-        if (strange) {
+        if (odd < k1) {
           if (E4M3) {
-            if (first_nan < k1)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
           } else {
-            for (int k = max(attend_sees(A, W.R, W.qt * M / A.group), W.a * KT); k < k1; ++k) {
+            for (int k = odd; k < k1; ++k) {
               int slot;
-              const int page = paged_lookup(A.C, W.row, k, &slot);
+              const int page = paged_lookup(A.C, item_row, k, &slot);
               if (page < 0) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D + d;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)item_head * A.C.page_size + slot) * D + d;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float x = __uint_as_float((uint32_t)v[i] << 16);
@@ -577,11 +594,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             __stcg(reinterpret_cast<float4*>(part) + (d + i) / 4 * M + qt * 128 + row, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(A.out + out_row * D + d + i) =
-                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+          for (int i = 0; i < 32; i += 8) {
+            const uint4 w = make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                                       pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+            const int cc = (d + i) / 8;
+            if (SPLIT) *reinterpret_cast<uint4*>(A.out + out_row * D + d + i) = w;
+            else *reinterpret_cast<uint4*>(base + qt * S::tile + cc / 8 * S::half_tile + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) = w;
+          }
         }
+      }
+      if (!SPLIT && whole) {
+        // the warp's rows leave by way of Q's place, so that neighbouring lanes write neighbouring columns
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < turns; ++i) {
+          const int from = i * (32 / across) + lane / across, r = warp % 4 * 32 + from, c = lane % across;
+          const long long to = __shfl_sync(0xffffffffu, out_row, from);
+          const uint4 w = *reinterpret_cast<const uint4*>(base + qt * S::tile + c / 8 * S::half_tile + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+          if (item_qt * M + qt * 128 + r < rows) *(reinterpret_cast<uint4*>(A.out + to * D) + c) = w;
+        }
+        __syncwarp();
       }
       if (whole && real && d0 == 0 && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       if (!whole) {
@@ -632,8 +664,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      if (failed && threadIdx.x == 0 && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
+      if (failed && threadIdx.x == 0 && A.flags) atomicOr(&A.flags[item_row], (uint32_t)SPEC_F_TIMEOUT);
       tmem_before();
+      ++segment;
       if (SPLIT) wide_sync();      // both O have been read before either is written again
     }
   }
