@@ -203,12 +203,22 @@ __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One try that lets the thread sleep for up to a millisecond: threads that poll
+// take issue slots from those that they wait for.
+__device__ __forceinline__ bool mbar_sleep_wait(unsigned long long* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
+  return ok != 0;
+}
+
 // Waits for the phase; sets *failed and returns when it does not come within
 // two seconds, or when another wait of this CTA has given up.
 __device__ __forceinline__ void mbar_await(unsigned long long* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (mbar_sleep_wait(bar, parity)) return;
   const unsigned long long began = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!mbar_sleep_wait(bar, parity)) {
     if (*failed) return;
     if (global_ns() - began > 2000000000ull) *failed = 1;
   }

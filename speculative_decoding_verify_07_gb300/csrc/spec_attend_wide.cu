@@ -224,13 +224,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (i * 32 + tid / 4) * pitch + h * 64 + tid % 4 * 16);
               if (h == S::halves - 1) asm volatile("bar.sync 2, 128;" ::: "memory");
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < 4; ++i) {
                 const int row = i * 32 + tid / 4;
                 const uint32_t e = ex[E4M3 ? row : 0];
                 const uint32_t scale = (e == 0 ? 0u : e > 254 ? 0x7fc0u : (min(e, kWideExp) + 120) << 7) * 0x10001u;
                 uint32_t y[8];
-                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const uint4 wi = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+                const uint32_t x[4] = {wi.x, wi.y, wi.z, wi.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   y[2 * j] = e4m3_bf16(__byte_perm(x[j], 0, 0x1404), scale);
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // Step i of a segment is for group i % 2: two steps a tile, or one.
       const bool leader = elect_one();
       int n = 0, segment = 0;
-      uint32_t p_phase[2] = {0, 0};
+      uint32_t p_phase = 0;                      // a bit a group
       constexpr uint32_t s_instr = wide_instr(KT, false), o_instr = wide_instr(D, true);
       constexpr int per = SPLIT ? 1 : 2;
       auto scores = [&](int step) {
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tmem_after();
         if (leader) {
           const uint64_t a = wide_desc(smem_u32(base + (SPLIT ? 0 : group) * S::tile), 0), b = wide_desc(smem_u32(k_sm + st * S::tile), 0);
-  #pragma unroll
+#pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint64_t at = (k / 4 * S::half_tile + k % 4 * 32) >> 4;
             mma_ss(tmem + group * 128, a + at, b + at, s_instr, k > 0);
@@ -384,24 +385,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (SPLIT || group == 1) mma_commit(&bar.k_empty[st]);
         }
       };
+      auto values = [&](int step) {
+        const int group = step & 1, at_n = n + step / per, st = at_n % VST;
+        mbar_await(&bar.v_full[st], at_n / VST & 1, &failed);
+        mbar_await(&bar.p_full[group], p_phase >> group & 1, &failed);
+        p_phase ^= 1u << group;
+        tmem_after();
+        if (leader) {
+          const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_ts(tmem + 256 + group * D, tmem + group * 128 + k * 8, b + (k * 2048 >> 4), o_instr, step > 1 || k > 0);
+          mma_commit(&bar.o_full[group]);
+          if (SPLIT || group == 1) mma_commit(&bar.v_empty[st]);
+        }
+      };
       while (W.next()) {
         const int steps = (W.b - W.a) * per;
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int step = 0; step < steps; ++step) {
-          const int group = step & 1, at_n = n + step / per, st = at_n % VST;
-          mbar_await(&bar.v_full[st], at_n / VST & 1, &failed);
-          mbar_await(&bar.p_full[group], p_phase[group], &failed);
-          p_phase[group] ^= 1;
-          tmem_after();
-          if (leader) {
-            const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
-  #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-              mma_ts(tmem + 256 + group * D, tmem + group * 128 + k * 8, b + (k * 2048 >> 4), o_instr, step > 1 || k > 0);
-            mma_commit(&bar.o_full[group]);
-            if (SPLIT || group == 1) mma_commit(&bar.v_empty[st]);
-          }
+#pragma unroll 1
+        for (int step = -2; step < steps; ++step) {
+          // the scores run two steps ahead, each in the place of the weights that the products before have read
+          if (step >= 0) values(step);
           if (step + 2 < steps) scores(step + 2);
         }
         n += W.b - W.a;
@@ -414,7 +418,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int group = warp / 4, row = threadIdx.x % 128, qt = SPLIT ? 0 : group;   // this thread's row of its query tile
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16), s_at = lanes + group * 128, o_at = lanes + 256;
     // a negative scale turns the queries' signs, so the largest score is that of the largest product
-    const float scale = fabsf(A.scale_log2);
+    // (a scale of zero is as good as one of 1e-30, and what is not seen stays at minus infinity)
+    const float scale = fmaxf(fabsf(A.scale_log2), 1e-30f);
     const uint32_t turn = A.scale_log2 < 0.f ? 0x80008000u : 0u;
     float* const stats = reinterpret_cast<float*>(base);
     int done = 0, n = 0, segment = 0;          // this group's steps so far; tiles; items
@@ -459,25 +464,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
         const unsigned* mask = there[(n + t - item_a) & 7];
         const bool edge = (t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u;
-        unsigned seen[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int left = lim - t * KT - c * 32;
-          seen[c] = mask[c] & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1);
-        }
         tmem_wait_ld();
-        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) high[i & 3] = fmaxf(high[i & 3], seen[i / 32] >> (i & 31) & 1 ? __uint_as_float(s[i]) : -INFINITY);
-        } else {
+          for (int c = 0; c < 4; ++c) {
+            const int left = lim - t * KT - c * 32;
+            const unsigned seen = mask[c] & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1);
 #pragma unroll
-          for (int i = 0; i < 128; i += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) high[j] = fmaxf(high[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
+            for (int i = 0; i < 32; ++i)
+              if (!(seen >> i & 1)) s[c * 32 + i] = 0xff800000u;
+          }
         }
+        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) high[j] = fmaxf(high[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
         float top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
-        if (top != -INFINITY) top *= scale;
+        top *= scale;
         float keep = 1.f;
         if (top > m + kWideSlack) {
           keep = exp2_wide(m - top);
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (done > began) {
             mbar_await(&bar.o_full[group], (done - 1) & 1, &failed);
             tmem_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tmem_ld16(o_at + group * D + c * 16, o);
@@ -510,10 +514,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             float2 x = fma2(make_float2(__uint_as_float(s[c * 32 + i]), __uint_as_float(s[c * 32 + i + 1])), scale2, from2);
             x.x = exp2_wide(x.x);
             x.y = exp2_wide(x.y);
-            if (edge) {
-              x.x = seen[c] >> i & 1 ? x.x : 0.f;
-              x.y = seen[c] >> (i + 1) & 1 ? x.y : 0.f;
-            }
             sum[i / 2 & 1] = add2(sum[i / 2 & 1], x);
             p[i / 2] = pack_bf16(x.x, x.y);
           }
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < cols / 32; ++c) {
         const int d = d0 + c * 32;
         uint32_t r[32];
