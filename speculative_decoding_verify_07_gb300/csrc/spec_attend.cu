@@ -3,8 +3,6 @@
 
 namespace specv {
 
-constexpr int kAttendRowsMost = 32;
-
 // cuTensorMapEncodeTiled, looked up once: the library does not link the driver.
 static PFN_attend_encode encoder() {
   static PFN_attend_encode fn = [] {
@@ -72,13 +70,14 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   A.flags = flags;
   A.N = N;
   A.group = group;
+  A.inv_group = 1.f / group;
   A.scale_log2 = scale * 1.4426950408889634f;
   A.joined = static_cast<unsigned*>(workspace);
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
   const bool e4m3 = cache->dtype == SPEC_E4M3;
   // A tile of 16 or 32 query rows where they suffice, of 128 or 256 where not.
   const long long rows = (long long)max_tokens * group;
-  const bool wide = rows > kAttendRowsMost;
+  const bool wide = rows > (e4m3 ? 64 : 32);
   // the longest run of positions that never leaves a page, up to what is copied at a time
   const int most = wide ? 128 : e4m3 ? 32 : 16;
   A.box = 1;

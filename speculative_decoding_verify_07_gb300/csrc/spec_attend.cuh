@@ -23,6 +23,7 @@ struct AttendArgs {
   long long q_token;     // elements from token to token of q
   int N, group, hq;
   int box;               // cache rows one copy brings: they lie in one page
+  float inv_group;
   float scale_log2;      // scale * log2(e): scores are powers of two
   unsigned* joined;      // workspace: per CTA, how many parts of its last item have come
   float* parts;          // workspace: per CTA, two partial results
@@ -55,6 +56,16 @@ __device__ __forceinline__ AttendRow attend_row(const AttendArgs& A, int r) {
   return R;
 }
 
+// a / group, for a >= 0.  (The compiler's division is several times as long, and a
+// kernel of several roles is short of instruction cache.)
+__device__ __forceinline__ int attend_token(const AttendArgs& A, int a) {
+  int q = (int)((float)a * A.inv_group), r = a - q * A.group;
+  const int more = (int)((float)r * A.inv_group);      // what the first product's rounding left
+  q += more;
+  r -= more * A.group;
+  return q + (r >= A.group) - (r < 0);
+}
+
 // How many positions the row's i-th new token sees; none that the page table cannot hold.
 __device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow& R, int i) {
   return max(0, min(R.kv - R.n + i + 1, A.C.max_pages * A.C.page_size));
@@ -63,7 +74,7 @@ __device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow&
 template <int M, int KT>
 __device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow& R, int qt) {
   const int last = min((qt + 1) * M, R.n * A.group) - 1;
-  return max(1, (attend_sees(A, R, last / A.group) + KT - 1) / KT);
+  return max(1, (attend_sees(A, R, attend_token(A, last)) + KT - 1) / KT);
 }
 
 template <int M>
@@ -71,56 +82,62 @@ __device__ __forceinline__ int attend_qtiles(const AttendArgs& A, const AttendRo
   return (R.n * A.group + M - 1) / M;
 }
 
+// The tiles of one head of a row.
 template <int M, int KT>
-__device__ __forceinline__ long long attend_row_tiles(const AttendArgs& A, int r) {
+__device__ __forceinline__ int attend_head_tiles(const AttendArgs& A, int r) {
   const AttendRow R = attend_row(A, r);
   const int qts = attend_qtiles<M>(A, R);
-  long long sum = 0;
+  int sum = 0;
+#pragma unroll 1
   for (int q = 0; q < qts; ++q) sum += attend_tiles<M, KT>(A, R, q);
-  return sum * A.C.heads;
+  return sum;
 }
 
-// A CTA's share: tiles [begin, end) of `total`, the first of them at `offset` in row `row`.
+// A CTA's share: tiles [begin, end) of all, the first of them at `offset` in row
+// `row`.  Each of `ctas` CTAs has `each` tiles, the first `more` one more.
 struct AttendShare {
-  long long begin, end, total, offset;
-  int row, ctas;     // ctas: those that have work
+  int begin, end, offset, each, more, row, ctas;
 };
 
-__device__ __forceinline__ long long share_begin(long long total, int cta, int ctas) { return total * cta / ctas; }
-__device__ __forceinline__ int share_of(long long total, long long tile, int ctas) {
-  return (int)(((tile + 1) * ctas - 1) / total);
+__device__ __forceinline__ int share_of(const AttendShare& S, int tile) {
+  const int high = S.more * (S.each + 1);
+  return tile < high ? tile / (S.each + 1) : S.more + (tile - high) / S.each;
 }
 
 template <int M, int KT, int THREADS>
 __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
   const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += attend_row_tiles<M, KT>(A, r);
+  for (int r = r0; r < r1; ++r) mine += (long long)attend_head_tiles<M, KT>(A, r) * A.C.heads;
   sums[t] = mine;
   __syncthreads();
-  const int used = (A.C.B + each - 1) / each;
-  long long before = 0, total = 0;
+  const int used = min(A.C.B, THREADS);
+  long long before = 0, all = 0;
 #pragma unroll 8
   for (int i = 0; i < used; ++i) {
     const long long s = sums[i];
     before += i < t ? s : 0;
-    total += s;
+    all += s;
   }
-  const int ctas = (int)min((long long)gridDim.x, total), cta = min((int)blockIdx.x, ctas);
-  const long long begin = total ? share_begin(total, cta, ctas) : 0;
+  // (more than 2^31 tiles, tens of terabytes to read, are refused)
+  const int total = all > 0x7fffffff ? 0 : (int)all;
+  if (all > 0x7fffffff && A.flags && t == 0 && blockIdx.x == 0) atomicOr(&A.flags[0], (uint32_t)SPEC_F_BAD_IDX);
+  const int ctas = min((int)gridDim.x, total), cta = min((int)blockIdx.x, ctas);
+  const int tiles = ctas ? total / ctas : 0, more = total - tiles * ctas, begin = cta * tiles + min(cta, more);
   if (t == 0) {
     out->ctas = ctas;
-    out->total = total;
+    out->each = tiles;
+    out->more = more;
     out->begin = begin;
-    out->end = cta < ctas ? share_begin(total, cta + 1, ctas) : begin;
+    out->end = cta < ctas ? begin + tiles + (cta < more) : begin;
     out->row = 0;
     out->offset = 0;
   }
   __syncthreads();
-  if (begin >= before && begin < before + mine) {
-    long long at = before;
+  if (total && begin >= before && begin < before + mine) {
+    int at = (int)before;
     for (int r = r0; r < r1; ++r) {
-      const long long w = attend_row_tiles<M, KT>(A, r);
+      const int w = attend_head_tiles<M, KT>(A, r) * A.C.heads;
       if (begin < at + w) {
         out->row = r;
         out->offset = begin - at;
@@ -139,16 +156,16 @@ struct AttendWalk {
   AttendRow R;
   int row, head, qt, tiles;      // the item, and its position tiles
   int a, b;                      // this segment's
-  long long at, end;             // the next tile of all, and the share's end
+  int at, end;                   // the next tile of all, and the share's end
   int next_a;
 
   __device__ __forceinline__ AttendWalk(const AttendArgs& args, const AttendShare& S)
       : A(args), row(S.row), head(0), qt(0), tiles(0), a(0), b(0), at(S.begin), end(S.end), next_a(0) {
     if (at >= end) return;
     R = attend_row(A, row);
-    long long off = S.offset;
-    const long long per_head = attend_row_tiles<M, KT>(A, row) / A.C.heads;
-    head = (int)(off / per_head);
+    int off = S.offset;
+    const int per_head = attend_head_tiles<M, KT>(A, row);
+    head = off / per_head;
     off -= head * per_head;
     for (;;) {
       tiles = attend_tiles<M, KT>(A, R, qt);
@@ -156,7 +173,7 @@ struct AttendWalk {
       off -= tiles;
       ++qt;
     }
-    next_a = (int)off;
+    next_a = off;
   }
   // The next segment; false at the end of the share.
   __device__ __forceinline__ bool next() {
@@ -173,14 +190,14 @@ struct AttendWalk {
       tiles = attend_tiles<M, KT>(A, R, qt);
     }
     a = next_a;
-    b = (int)min((long long)tiles, a + (end - at));
+    b = min(tiles, a + (end - at));
     at += b - a;
     next_a = b;
     return true;
   }
   __device__ __forceinline__ bool whole() const { return a == 0 && b == tiles; }
   // The first tile of this item among all.
-  __device__ __forceinline__ long long item_begin() const { return at - b; }
+  __device__ __forceinline__ int item_begin() const { return at - b; }
 };
 
 // ---------------------------------------------------------------------- copies

@@ -107,7 +107,7 @@ struct RowsFetch {
   __device__ __forceinline__ void segment() {
     more = I.next();
     t = I.a;
-    if (more) limit = attend_sees(I.A, I.R, (min((I.qt + 1) * M, I.R.n * I.A.group) - 1) / I.A.group);
+    if (more) limit = attend_sees(I.A, I.R, attend_token(I.A, min((I.qt + 1) * M, I.R.n * I.A.group) - 1));
   }
   __device__ __forceinline__ void look(int warp, int lane) {
     page = -1;
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   __shared__ long long sums[kRowsThreads];
   __shared__ float sm_m[kRowsWarps][M], sm_l[kRowsWarps][M];
   __shared__ int sees[M];
+  __shared__ long long q_at[M], out_at[M];        // where a query row is read and written
   __shared__ int failed, odd, last_part, first_nan;
   __shared__ unsigned q_top;
   unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -220,9 +221,13 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     const int rows = min(M, W.R.n * A.group - W.qt * M);  // query rows of this tile
     if (threadIdx.x == 0) odd = 0, q_top = 0, first_nan = 0x7fffffff;
     if (threadIdx.x < M) {
-      const int g = min(W.qt * M + (int)threadIdx.x, W.R.n * A.group - 1);
-      sees[threadIdx.x] = attend_sees(A, W.R, g / A.group);
+      const int g = min(W.qt * M + (int)threadIdx.x, W.R.n * A.group - 1), token = attend_token(A, g);
+      const int head = W.head * A.group + g - token * A.group;
+      sees[threadIdx.x] = attend_sees(A, W.R, token);
+      q_at[threadIdx.x] = (W.R.first + token) * A.q_token + (long long)head * D;
+      out_at[threadIdx.x] = (long long)(W.R.first + token) * A.hq + head;
     }
+    __syncthreads();
     // Q as the matrix instruction's A fragments, 16 bytes a lane.
     constexpr int each = M * D / 8 / kRowsThreads;
     uint2 qw[each][2];
@@ -236,8 +241,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         const int m = m0 + 8 * h;
         qw[u][h] = make_uint2(0, 0);
         if (m < rows) {
-          const int g = W.qt * M + m, token = g / A.group, head = W.head * A.group + g - token * A.group;
-          const uint16_t* p = A.q + (W.R.first + token) * A.q_token + (long long)head * D;
+          const uint16_t* p = A.q + q_at[m];
           if (E4M3) {
             // a lane's four of k-step ks: those that its 16-byte load of codes brings (see below)
             const int d = D == 128 ? 32 * q + 16 * (ks / 4) + 4 * (ks % 4) : 16 * q + 4 * ks;
@@ -257,7 +261,6 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     float score_scale = A.scale_log2, q_scale = 1.f;
     if (E4M3) {
       top = __reduce_max_sync(0xffffffffu, top);
-      __syncthreads();
       if (lane == 0) atomicMax(&q_top, top);
       __syncthreads();
       // the largest magnitude to 2^13 .. 2^14 (what is 2^-27 of it is still a normal number)
@@ -578,9 +581,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
       __syncthreads();
     }
     const bool whole = W.whole();
-    const long long item = W.item_begin();
-    const int c0 = whole ? 0 : share_of(share.total, item, share.ctas);
-    const int c1 = whole ? 0 : share_of(share.total, item + W.tiles - 1, share.ctas);
+    const int item = W.item_begin();
+    const int c0 = whole ? 0 : share_of(share, item);
+    const int c1 = whole ? 0 : share_of(share, item + W.tiles - 1);
     if (!whole) {
       float* part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       for (int i = threadIdx.x; i < M * D / 4; i += kRowsThreads) {
@@ -635,8 +638,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
             for (int e = 0; e < 8; ++e) x[e] = x[e] * keep + y[e] * add;
           }
         }
-        const int g = W.qt * M + row, token = g / A.group;
-        const long long at = (long long)(W.R.first + token) * A.hq + W.head * A.group + g - token * A.group;
+        const long long at = out_at[row];
         float by = sum == 0.f ? 1.f : 1.f / sum;
         if (E4M3) by *= __uint_as_float((127 - kRowsShift) << 23);
         *reinterpret_cast<uint4*>(A.out + at * D + d) =

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     int n = 0, segment = 0;                      // tiles and items so far
     const int tid = threadIdx.x - ready_warp * 32;
     while (W.next()) {
-      const int fewest = attend_sees(A, W.R, W.qt * M / A.group);
+      const int fewest = attend_sees(A, W.R, attend_token(A, W.qt * M));
       if (tid == 0) odd_at[(segment + 6) & 15] = kNowhere;     // (no warp is six items ahead of another)
       for (int t = W.a; t < W.b; ++t, ++n) {
         const int kst = n % KST, vst = n % VST;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int next_page[4], next_slot[4];            // this lane's positions of the next tile
       uint32_t next_e[4];                        // and their exponents
       while (W.next()) {
-        const int limit = attend_sees(A, W.R, (min((W.qt + 1) * M, W.R.n * A.group) - 1) / A.group);
+        const int limit = attend_sees(A, W.R, attend_token(A, min((W.qt + 1) * M, W.R.n * A.group) - 1));
         auto look = [&](int t) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -428,22 +428,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const AttendRow R = W.R;
       const int item_row = W.row, item_head = W.head, item_qt = W.qt, item_tiles = W.tiles, item_a = W.a, item_b = W.b;
       const bool whole = W.whole();
-      const long long item = W.item_begin();
+      const int item = W.item_begin();
       const int mine = item_qt * M + qt * 128 + row, rows = R.n * A.group;
       const bool real = mine < rows;
-      const int token = min(mine, rows - 1) / A.group, head = item_head * A.group + min(mine, rows - 1) - token * A.group;
-      const int lim = attend_sees(A, R, token), fewest = attend_sees(A, R, min(item_qt * M + qt * 128, rows - 1) / A.group);
+      const int token = attend_token(A, min(mine, rows - 1)), head = item_head * A.group + min(mine, rows - 1) - token * A.group;
+      const int lim = attend_sees(A, R, token), fewest = attend_sees(A, R, attend_token(A, min(item_qt * M + qt * 128, rows - 1)));
       if (!SPLIT || group == 0) {
         // the products with the last Q are done: their results have been waited for
+        const unsigned live = __ballot_sync(0xffffffffu, real);
+        const long long q_row = (R.first + token) * A.q_token + (long long)head * D;
         uint4 q[turns];
 #pragma unroll
         for (int i = 0; i < turns; ++i) {
-          const int g = item_qt * M + qt * 128 + warp % 4 * 32 + i * (32 / across) + lane / across;
+          const int from = i * (32 / across) + lane / across;
+          const long long at = __shfl_sync(0xffffffffu, q_row, from);
           q[i] = make_uint4(0, 0, 0, 0);
-          if (g < rows) {
-            const int tk = g / A.group, hd = item_head * A.group + g - tk * A.group;
-            q[i] = __ldg(reinterpret_cast<const uint4*>(A.q + (R.first + tk) * A.q_token + (long long)hd * D) + lane % across);
-          }
+          if (live >> from & 1) q[i] = __ldg(reinterpret_cast<const uint4*>(A.q + at) + lane % across);
         }
 #pragma unroll
         for (int i = 0; i < turns; ++i) {
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         f1 = exp2_wide(m1 - ref);
         l = stats[128 + row] * f0 + (two ? stats[384 + row] * f1 : 0.f);
       }
-      const int c0 = whole ? 0 : share_of(share.total, item, share.ctas);
-      const int c1 = whole ? 0 : share_of(share.total, item + item_tiles - 1, share.ctas);
+      const int c0 = whole ? 0 : share_of(share, item);
+      const int c1 = whole ? 0 : share_of(share, item + item_tiles - 1);
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
