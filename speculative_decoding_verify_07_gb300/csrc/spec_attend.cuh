@@ -88,7 +88,7 @@ __device__ __forceinline__ int attend_head_tiles(const AttendArgs& A, int r) {
   const AttendRow R = attend_row(A, r);
   const int qts = attend_qtiles<M>(A, R);
   int sum = 0;
-#pragma unroll 1
+#pragma unroll 4
   for (int q = 0; q < qts; ++q) sum += attend_tiles<M, KT>(A, R, q);
   return sum;
 }

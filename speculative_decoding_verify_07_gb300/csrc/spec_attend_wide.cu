@@ -145,7 +145,7 @@ constexpr uint32_t kWideExp = 134;     // the largest exponent byte whose scale,
 struct WideBars {
   unsigned long long k_raw[4], k_full[4], k_empty[4];      // keys: codes copied, ready, read
   unsigned long long v_raw[4], v_full[4], v_empty[4];      // values: copied, ready, read
-  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2];
+  unsigned long long q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
 };
 
 template <int D, bool E4M3, bool SPLIT>
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 128);
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_half[i], 128);
       mbar_init(&bar.p_full[i], 128);
       mbar_init(&bar.o_full[i], 1);
     }
@@ -388,14 +389,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       auto values = [&](int step) {
         const int group = step & 1, at_n = n + step / per, st = at_n % VST;
         mbar_await(&bar.v_full[st], at_n / VST & 1, &failed);
-        mbar_await(&bar.p_full[group], p_phase >> group & 1, &failed);
-        p_phase ^= 1u << group;
-        tmem_after();
-        if (leader) {
-          const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
+        const uint64_t b = wide_desc(smem_u32(v_sm + st * S::tile), S::half_tile);
+        // the first half of the weights is multiplied while the second is computed
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_ts(tmem + 256 + group * D, tmem + group * 128 + k * 8, b + (k * 2048 >> 4), o_instr, step > 1 || k > 0);
+        for (int h = 0; h < 2; ++h) {
+          mbar_await(h ? &bar.p_full[group] : &bar.p_half[group], p_phase >> group & 1, &failed);
+          tmem_after();
+          if (leader) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              mma_ts(tmem + 256 + group * D, tmem + group * 128 + k * 8, b + (k * 2048 >> 4), o_instr, step > 1 || k > 0);
+          }
+        }
+        p_phase ^= 1u << group;
+        if (leader) {
           mma_commit(&bar.o_full[group]);
           if (SPLIT || group == 1) mma_commit(&bar.v_empty[st]);
         }
@@ -460,12 +467,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mbar_await(&bar.s_full[group], done & 1, &failed);
         tmem_after();
         uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
+        tmem_ld32(s_at, s);
+        tmem_ld32(s_at + 32, s + 32);
         const unsigned* mask = there[(n + t - item_a) & 7];
         const bool edge = (t + 1) * KT > fewest || (mask[0] & mask[1] & mask[2] & mask[3]) != ~0u;
         tmem_wait_ld();
+        tmem_ld32(s_at + 64, s + 64);
+        tmem_ld32(s_at + 96, s + 96);
+        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (edge) {
+          tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int left = lim - t * KT - c * 32;
@@ -475,9 +486,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               if (!(seen >> i & 1)) s[c * 32 + i] = 0xff800000u;
           }
         }
-        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 128; i += 8)
+        for (int i = 0; i < 64; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) high[j] = fmaxf(high[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 64; i < 128; i += 8)
 #pragma unroll
           for (int j = 0; j < 4; ++j) high[j] = fmaxf(high[j], fmaxf(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4])));
         float top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
@@ -518,6 +533,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             p[i / 2] = pack_bf16(x.x, x.y);
           }
           tmem_st16(s_at + c * 16, p);
+          if (c == 1) {
+            tmem_wait_st();
+            tmem_before();
+            mbar_arrive(&bar.p_half[group]);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
