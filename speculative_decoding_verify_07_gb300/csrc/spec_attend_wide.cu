@@ -37,7 +37,7 @@ struct WideShape {
   static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
   // what is left of the 227 KB after Q, the alignment and the small arrays, in tiles: keys have the odd one, they are
   // waited for first
-  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 2560 : 1024) - QT * tile) / tile;
+  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 5632 : 1024) - QT * tile) / tile;
   static constexpr int k_stages = (room + 1) / 2 > 4 ? 4 : (room + 1) / 2;
   static constexpr int v_stages = room / 2 > 4 ? 4 : room / 2;
   static constexpr int smem = 1024 + (QT + k_stages + v_stages) * tile;
@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ __align__(8) WideBars bar;
   __shared__ unsigned there[8][4], v_there[8][4];      // which positions of the tile are there, for the last eight tiles
   __shared__ AttendShare share;
-  __shared__ uint8_t exps[2][4][E4M3 ? KT : 1];       // 8-bit cache: a stage's exponents, 0 where nothing is
+  // 8-bit cache: a stage's scales (in both halves, times 2^120; 0 where nothing is), and whether one was cut to fit
+  __shared__ uint32_t scales[2][4][E4M3 ? KT : 1];
+  __shared__ int cut[2][4];
   __shared__ uint32_t tmem_base;
   __shared__ int failed, last_part;
   __shared__ int odd_at[16];     // for the last items: the first position whose value is not finite, where that needs care
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int tid = threadIdx.x - ready_warp * 32;
     while (W.next()) {
       const int fewest = attend_sees(A, W.R, attend_token(A, W.qt * M));
+      const int limit = attend_sees(A, W.R, attend_token(A, min((W.qt + 1) * M, W.R.n * A.group) - 1));
       if (tid == 0) odd_at[(segment + 6) & 15] = kNowhere;     // (no warp is six items ahead of another)
       for (int t = W.a; t < W.b; ++t, ++n) {
         const int kst = n % KST, vst = n % VST;
@@ -214,39 +217,51 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
           for (int v = 0; v < 2; ++v) {
             unsigned char* const tile = v ? v_sm + vst * S::tile : k_sm + kst * S::tile;
-            const uint8_t* const ex = exps[v][v ? vst : kst];
             mbar_await(v ? &bar.v_raw[vst] : &bar.k_raw[kst], (v ? n / VST : n / KST) & 1, &failed);
             // The codes lie in the last 128 D bytes of the stage (in all of it where rows lie apart).  Of 128 dimensions
             // the first 64 go to the other half as they are read; what goes where codes lie is read first.
             unsigned char* const codes = tile + (S::halves - 1) * S::half_tile;
+            const int part = tid % 4, row0 = tid / 4;          // 16 codes of rows row0, row0 + 32, ...
+            uint32_t scale[4];
 #pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i] = scales[v][v ? vst : kst][E4M3 ? row0 + 32 * i : 0];
+            const bool rest = cut[v][v ? vst : kst];
+#pragma unroll 1
             for (int h = 0; h < S::halves; ++h) {
               uint4 w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (i * 32 + tid / 4) * pitch + h * 64 + tid % 4 * 16);
+              for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (row0 + 32 * i) * pitch + h * 64 + part * 16);
               if (h == S::halves - 1) asm volatile("bar.sync 2, 128;" ::: "memory");
-#pragma unroll 1
+#pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int row = i * 32 + tid / 4;
-                const uint32_t e = ex[E4M3 ? row : 0];
-                const uint32_t scale = (e == 0 ? 0u : e > 254 ? 0x7fc0u : (min(e, kWideExp) + 120) << 7) * 0x10001u;
-                uint32_t y[8];
-                const uint4 wi = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-                const uint32_t x[4] = {wi.x, wi.y, wi.z, wi.w};
+                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                unsigned char* const to = tile + h * S::half_tile + (row0 + 32 * i) * 128;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  y[2 * j] = e4m3_bf16(__byte_perm(x[j], 0, 0x1404), scale);
-                  y[2 * j + 1] = e4m3_bf16(__byte_perm(x[j], 0, 0x3424), scale);
+                for (int j = 0; j < 2; ++j) {
+                  uint4 y = make_uint4(e4m3_bf16(__byte_perm(x[2 * j], 0, 0x1404), scale[i]), e4m3_bf16(__byte_perm(x[2 * j], 0, 0x3424), scale[i]),
+                                       e4m3_bf16(__byte_perm(x[2 * j + 1], 0, 0x1404), scale[i]), e4m3_bf16(__byte_perm(x[2 * j + 1], 0, 0x3424), scale[i]));
+                  *reinterpret_cast<uint4*>(to + (((part * 2 + j) ^ (row0 & 7)) << 4)) = y;
                 }
-                if (__any_sync(0xffffffffu, e > kWideExp)) {
-                  const uint32_t rest = (e > kWideExp && e < 255 ? e - kWideExp + 127 : 127u) * 0x00800080u;
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[j]) : "r"(rest));
+              }
+              if (rest) {
+                // a scale over 2^7: what it was cut by
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                  const int pos = t * KT + row0 + 32 * i;
+                  int slot;
+                  const int page = pos < limit ? paged_lookup(A.C, W.row, pos, &slot) : -1;
+                  uint32_t e = 0;
+                  if (page >= 0) e = (v ? A.C.v_exp : A.C.k_exp)[page * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + slot)];
+                  if (e <= kWideExp || e > 254) continue;
+                  const uint32_t more = ((e - kWideExp + 127) << 7) * 0x10001u;
+                  for (int j = 0; j < 2; ++j) {
+                    uint4* p = reinterpret_cast<uint4*>(tile + h * S::half_tile + (row0 + 32 * i) * 128 + (((part * 2 + j) ^ (row0 & 7)) << 4));
+                    uint4 y = *p;
+                    asm("mul.rn.bf16x2 %0, %0, %4;\nmul.rn.bf16x2 %1, %1, %4;\nmul.rn.bf16x2 %2, %2, %4;\nmul.rn.bf16x2 %3, %3, %4;"
+                        : "+r"(y.x), "+r"(y.y), "+r"(y.z), "+r"(y.w) : "r"(more));
+                    *p = y;
+                  }
                 }
-                unsigned char* const to = tile + h * S::half_tile + row * 128;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  *reinterpret_cast<uint4*>(to + (((tid % 4 * 2 + j) ^ (row & 7)) << 4)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
               }
             }
             fence_proxy_async();
@@ -335,8 +350,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int j = 0; j < 4; ++j) {
               // a value of NaN is cleared here and put in at the item's end
               if (v && e[j] > 254) atomicMin(&odd_at[segment & 15], t * KT + 32 * j + lane);
-              exps[v][st][E4M3 ? 32 * j + lane : 0] = (uint8_t)(v && e[j] > 254 ? 0 : e[j]);
+              const uint32_t bits = e[j] == 0 ? 0u : e[j] > 254 ? (v ? 0u : 0x7fc0u) : (min(e[j], kWideExp) + 120) << 7;
+              scales[v][st][E4M3 ? 32 * j + lane : 0] = bits * 0x10001u;
             }
+            const bool over = __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > kWideExp);
+            if (lane == 0) cut[v][st] = over;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(full, bytes);
