@@ -310,6 +310,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int stages = v ? VST : KST, boxes = KT / A.box;
       unsigned char* const sm = v ? v_sm : k_sm;
       const CUtensorMap* map = v ? &vmap : &kmap;
+      unsigned starts[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) starts[j] = attend_starts(A.box, j);
       int n = 0, segment = 0;
       int next_page[4], next_slot[4];            // this lane's positions of the next tile
       uint32_t next_e[4];                        // and their exponents
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             slot[j] = next_slot[j];
             e[j] = page[j] < 0 ? 0 : max(next_e[j], 1u);
             mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
-            copies += __popc(mask[j] & attend_starts(A.box, j));
+            copies += __popc(mask[j] & starts[j]);
           }
           if (t + 1 < W.b) look(t + 1);
           const uint32_t bytes = failed ? 0 : copies * A.box * D * (E4M3 ? 1 : 2);
@@ -346,14 +349,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], (n / stages & 1) ^ 1, &failed);
           if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
           if (E4M3) {
+            const bool over = __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > kWideExp);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              // a value of NaN is cleared here and put in at the item's end
-              if (v && e[j] > 254) atomicMin(&odd_at[segment & 15], t * KT + 32 * j + lane);
-              const uint32_t bits = e[j] == 0 ? 0u : e[j] > 254 ? (v ? 0u : 0x7fc0u) : (min(e[j], kWideExp) + 120) << 7;
+              uint32_t bits = e[j] == 0 ? 0u : (e[j] + 120) << 7;
+              if (over) {
+                // a value of NaN is cleared here and put in at the item's end
+                if (v && e[j] > 254) atomicMin(&odd_at[segment & 15], t * KT + 32 * j + lane);
+                if (e[j] > kWideExp) bits = e[j] < 255 ? (kWideExp + 120) << 7 : v ? 0u : 0x7fc0u;
+              }
               scales[v][st][E4M3 ? 32 * j + lane : 0] = bits * 0x10001u;
             }
-            const bool over = __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > kWideExp);
             if (lane == 0) cut[v][st] = over;
           }
           __syncwarp();
