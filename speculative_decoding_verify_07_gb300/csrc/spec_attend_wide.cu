@@ -37,7 +37,7 @@ struct WideShape {
   static constexpr int tile = halves * half_tile;             // 128 rows of Q, K or V
   // what is left of the 227 KB after Q, the alignment and the small arrays, in tiles: keys have the odd one, they are
   // waited for first
-  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 5632 : 1024) - QT * tile) / tile;
+  static constexpr int room = (227 * 1024 - 1024 - (E4M3 ? 3584 : 1024) - QT * tile) / tile;
   static constexpr int k_stages = (room + 1) / 2 > 4 ? 4 : (room + 1) / 2;
   static constexpr int v_stages = room / 2 > 4 ? 4 : room / 2;
   static constexpr int smem = 1024 + (QT + k_stages + v_stages) * tile;
@@ -130,6 +130,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
+// Whether any thread of the four warps that make tiles ready says so; a barrier among them.
+__device__ __forceinline__ bool ready_any(bool mine) {
+  uint32_t any;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 2, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(any) : "r"((uint32_t)mine) : "memory");
+  return any != 0;
+}
 __device__ __forceinline__ void wide_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the softmax warps
 
 // Two e4m3 codes in the upper bytes of 16-bit halves as bf16, times `scale` (a
@@ -157,9 +164,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ __align__(8) WideBars bar;
   __shared__ unsigned there[8][4], v_there[8][4];      // which positions of the tile are there, for the last eight tiles
   __shared__ AttendShare share;
-  // 8-bit cache: a stage's scales (in both halves, times 2^120; 0 where nothing is), and whether one was cut to fit
-  __shared__ uint32_t scales[2][4][E4M3 ? KT : 1];
-  __shared__ int cut[2][4];
+  __shared__ uint32_t scales[2][2][E4M3 ? KT : 1];    // 8-bit cache: the last two tiles' scales (in both halves, times 2^120)
   __shared__ uint32_t tmem_base;
   __shared__ int failed, last_part;
   __shared__ int odd_at[16];     // for the last items: the first position whose value is not finite, where that needs care
@@ -211,9 +216,45 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int fewest = attend_sees(A, W.R, attend_token(A, W.qt * M));
       const int limit = attend_sees(A, W.R, attend_token(A, min((W.qt + 1) * M, W.R.n * A.group) - 1));
       if (tid == 0) odd_at[(segment + 6) & 15] = kNowhere;     // (no warp is six items ahead of another)
+      // 8-bit cache: this thread's position, its page's entry two tiles ahead and its exponents one tile ahead
+      int entry = -1, slot = 0;
+      uint32_t ke = 0, ve = 0;
+      auto look = [&](int t) {
+        const int pos = t * KT + tid;
+        entry = pos < limit ? paged_entry(A.C, W.row, pos, &slot) : -1;
+      };
+      auto fetch = [&]() {
+        const int page = paged_page(A.C, entry);
+        ke = ve = 0;
+        if (page >= 0) {
+          const long long e = page * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + slot);
+          ke = max((uint32_t)A.C.k_exp[e], 1u);
+          ve = max((uint32_t)A.C.v_exp[e], 1u);
+        }
+      };
+      if (E4M3) {
+        look(W.a);
+        fetch();
+        if (W.a + 1 < W.b) look(W.a + 1);
+      }
       for (int t = W.a; t < W.b; ++t, ++n) {
         const int kst = n % KST, vst = n % VST;
         if (E4M3) {
+          uint32_t bits[2] = {ke == 0 ? 0u : (ke + 120) << 7, ve == 0 ? 0u : (ve + 120) << 7};
+          const bool over = max(ke, ve) > kWideExp;
+          if (over) {
+            // what does not fit is made up for below; a value of NaN is cleared here and put in at the item's end
+            if (ve > 254) atomicMin(&odd_at[segment & 15], t * KT + tid);
+            if (ke > kWideExp) bits[0] = ke < 255 ? (kWideExp + 120) << 7 : 0x7fc0u;
+            if (ve > kWideExp) bits[1] = ve < 255 ? (kWideExp + 120) << 7 : 0u;
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) scales[n & 1][v][E4M3 ? tid : 0] = bits[v] * 0x10001u;
+          if (t + 1 < W.b) {
+            fetch();
+            if (t + 2 < W.b) look(t + 2);
+          }
+          const bool rest = ready_any(over);       // (and every scale is written)
 #pragma unroll 1
           for (int v = 0; v < 2; ++v) {
             unsigned char* const tile = v ? v_sm + vst * S::tile : k_sm + kst * S::tile;
@@ -224,8 +265,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int part = tid % 4, row0 = tid / 4;          // 16 codes of rows row0, row0 + 32, ...
             uint32_t scale[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) scale[i] = scales[v][v ? vst : kst][E4M3 ? row0 + 32 * i : 0];
-            const bool rest = cut[v][v ? vst : kst];
+            for (int i = 0; i < 4; ++i) scale[i] = scales[n & 1][v][E4M3 ? row0 + 32 * i : 0];
 #pragma unroll 1
             for (int h = 0; h < S::halves; ++h) {
               uint4 w[4];
@@ -313,9 +353,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       unsigned starts[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) starts[j] = attend_starts(A.box, j);
-      int n = 0, segment = 0;
+      int n = 0;
       int next_page[4], next_slot[4];            // this lane's positions of the next tile
-      uint32_t next_e[4];                        // and their exponents
       while (W.next()) {
         const int limit = attend_sees(A, W.R, attend_token(A, min((W.qt + 1) * M, W.R.n * A.group) - 1));
         auto look = [&](int t) {
@@ -323,23 +362,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int j = 0; j < 4; ++j) {
             const int pos = t * KT + 32 * j + lane;
             next_slot[j] = 0;
-            next_e[j] = 0;
             next_page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &next_slot[j]) : -1;
             if (next_page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
-            if (E4M3 && next_page[j] >= 0)
-              next_e[j] = (v ? A.C.v_exp : A.C.k_exp)[next_page[j] * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + next_slot[j])];
           }
         };
         look(W.a);
         for (int t = W.a; t < W.b; ++t, ++n) {
           const int st = n % stages;
           int page[4], slot[4];
-          unsigned mask[4], e[4], copies = 0;
+          unsigned mask[4], copies = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             page[j] = next_page[j];
             slot[j] = next_slot[j];
-            e[j] = page[j] < 0 ? 0 : max(next_e[j], 1u);
             mask[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
             copies += __popc(mask[j] & starts[j]);
           }
@@ -348,20 +383,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           unsigned long long* full = v ? &bar.v_raw[st] : E4M3 ? &bar.k_raw[st] : &bar.k_full[st];
           mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], (n / stages & 1) ^ 1, &failed);
           if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
-          if (E4M3) {
-            const bool over = __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > kWideExp);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t bits = e[j] == 0 ? 0u : (e[j] + 120) << 7;
-              if (over) {
-                // a value of NaN is cleared here and put in at the item's end
-                if (v && e[j] > 254) atomicMin(&odd_at[segment & 15], t * KT + 32 * j + lane);
-                if (e[j] > kWideExp) bits = e[j] < 255 ? (kWideExp + 120) << 7 : v ? 0u : 0x7fc0u;
-              }
-              scales[v][st][E4M3 ? 32 * j + lane : 0] = bits * 0x10001u;
-            }
-            if (lane == 0) cut[v][st] = over;
-          }
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
@@ -384,7 +405,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
         }
-        ++segment;
       }
     } else if (warp == mma_warp) {
       // ----------------------------------------------------- matrix products

@@ -82,6 +82,17 @@ __device__ __forceinline__ int paged_lookup(const PagedCache& C, int r, int pos,
   return page >= 0 && page < C.pages ? page : -1;
 }
 
+// The same in two steps, so that the table's entry can be on its way meanwhile:
+// the entry as it stands (-1 beyond the table), and the page that it names or -1.
+__device__ __forceinline__ int paged_entry(const PagedCache& C, int r, int pos, int* slot) {
+  const int i = paged_index(C, pos);
+  *slot = pos - i * C.page_size;
+  return i < C.max_pages ? __ldg(C.table + (long long)r * C.max_pages + i) : -1;
+}
+__device__ __forceinline__ int paged_page(const PagedCache& C, int entry) {
+  return entry >= 0 && entry < C.pages ? entry : -1;
+}
+
 // The row whose new tokens hold `token`, or -1: the last r with cu[r] <= token.
 __device__ __forceinline__ int paged_row(const PagedCache& C, int token) {
   int lo = 0, hi = C.B;   // cu[lo] <= token < cu[hi] once the ends are checked
