@@ -3,9 +3,8 @@
 
 namespace specv {
 
-// cuTensorMapEncodeTiled, looked up once: the library does not link the driver.
-static PFN_attend_encode encoder() {
-  static PFN_attend_encode fn = [] {
+TensorMapEncode tensor_map_encoder() {
+  static TensorMapEncode fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult found;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
@@ -13,13 +12,13 @@ static PFN_attend_encode encoder() {
       cudaGetLastError();
       p = nullptr;
     }
-    return reinterpret_cast<PFN_attend_encode>(p);
+    return reinterpret_cast<TensorMapEncode>(p);
   }();
   return fn;
 }
 
 int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box, bool swizzled) {
-  const PFN_attend_encode encode = encoder();
+  const TensorMapEncode encode = tensor_map_encoder();
   if (!encode) return SPEC_E_CUDA;
   const cuuint64_t es = e4m3 ? 1 : 2, row = C.D * es;
   const cuuint64_t dims[4] = {(cuuint64_t)C.D, (cuuint64_t)C.page_size, (cuuint64_t)C.heads, (cuuint64_t)C.pages};

@@ -1,8 +1,7 @@
 // What the attention kernels share: arguments, the division of the work over
-// CTAs, tensor maps of the cache, and bounded waits.
+// CTAs, and tensor maps of the cache.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -11,6 +10,7 @@
 #include "spec_device.cuh"
 #include "spec_host.h"
 #include "spec_paged.cuh"
+#include "spec_tma.cuh"
 
 namespace specv {
 
@@ -202,48 +202,11 @@ struct AttendWalk {
 
 // ---------------------------------------------------------------------- copies
 
-__device__ __forceinline__ void tma_load_4d(uint32_t smem, const CUtensorMap* map, int x, int y, int z, int w,
-                                            unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // The positions of the j-th 32 of a tile at which boxes of `box` rows begin.
 __device__ __forceinline__ unsigned attend_starts(int box, int j) {
   if (box >= 32) return j * 32 % box == 0 ? 1u : 0u;
   return box == 16 ? 0x10001u : box == 8 ? 0x01010101u : box == 4 ? 0x11111111u : box == 2 ? 0x55555555u : ~0u;
 }
-
-__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// One try that lets the thread sleep for up to a millisecond: threads that poll
-// take issue slots from those that they wait for.
-__device__ __forceinline__ bool mbar_sleep_wait(unsigned long long* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
-  return ok != 0;
-}
-
-// Waits for the phase; sets *failed and returns when it does not come within
-// two seconds, or when another wait of this CTA has given up.
-__device__ __forceinline__ void mbar_await(unsigned long long* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_sleep_wait(bar, parity)) return;
-  const unsigned long long began = global_ns();
-  while (!mbar_sleep_wait(bar, parity)) {
-    if (*failed) return;
-    if (global_ns() - began > 2000000000ull) *failed = 1;
-  }
-}
-
-using PFN_attend_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // A tensor map of one pool: [pages, heads, page_size, head_dim], boxes of up to
 // 128 bytes by `box` rows, in the order they have or swizzled as their width asks.

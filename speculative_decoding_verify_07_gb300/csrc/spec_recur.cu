@@ -6,6 +6,7 @@
 #include "../../include/spec_verify.h"
 #include "spec_host.h"
 #include "spec_paged.cuh"
+#include "spec_tma.cuh"
 
 namespace specv {
 
@@ -191,17 +192,13 @@ __device__ __forceinline__ Word get_word(const Word* p) {
 }
 
 constexpr int kScanWarps = 8;        // at most, one behind the other in time
+constexpr int kScanCh = 64;          // channels of a tile, two a lane
 constexpr int kScanGroupMost = 32;
 constexpr int kScanSpins = 1 << 20;  // about a second of polling
-constexpr int kScanSteps = 8;        // the fewest of scan_steps
 
-// Tokens a warp keeps in registers: a decay in float32 and the rest as loaded,
-// about 96 registers forward and 64 backward.
-template <bool BF16, int VEC, bool BWD>
-constexpr int scan_steps() {
-  if (BWD) return VEC == 4 ? 8 : VEC == 2 ? (BF16 ? 16 : 8) : 16;
-  return VEC == 4 ? 16 : VEC == 2 ? (BF16 ? 32 : 16) : 32;
-}
+// Tokens of a warp: a tile is 16 KB a tensor.
+template <bool BF16>
+constexpr int scan_steps() { return BF16 ? 16 : 8; }
 
 // Waits for N words under the tag and returns their floats; zeros (and
 // *gave_up) where they do not come.
@@ -225,230 +222,250 @@ __device__ __forceinline__ void await_words(const Word* p, unsigned tag, float* 
   *gave_up = true;
 }
 
-// Where a ticket's tile lies.
-struct ScanTile {
-  int tile, row, c, len;
-  bool live, ok;
-  long long from, to;
-};
-
-template <int VEC, bool BWD>
-__device__ __forceinline__ ScanTile scan_tile(const RecurArgs& A, unsigned ticket, int tiles, int blocks, int lane) {
-  ScanTile t;
-  const unsigned per = (unsigned)A.B * (unsigned)blocks;
-  const unsigned nth = ticket / per, rest = ticket - nth * per, row = rest / (unsigned)blocks;
-  t.row = (int)row;
-  t.tile = BWD ? tiles - 1 - (int)nth : (int)nth;
-  t.c = ((int)(rest - row * (unsigned)blocks) * 32 + lane) * VEC;
-  t.live = t.c < A.D;
-  t.ok = recur_row<BWD>(A, t.row, &t.len, &t.from, &t.to);
-  if (!t.ok) t.len = 0;
-  return t;
+// Two neighbouring channels in shared memory.
+template <bool BF16>
+__device__ __forceinline__ float2 lds_pair(uint32_t p) {
+  if (BF16) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(p) : "memory");
+    return make_float2(bf16_lo(w), bf16_hi(w));
+  }
+  float2 x;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(p) : "memory");
+  return x;
 }
 
-// A CTA takes a tile of (32 VEC channels) x (warps * S tokens) of a row.  Tiles
-// go by tickets, all channels of all rows before the next tokens, and a tile
-// waits only for tiles of smaller tickets, whose CTAs have begun.
-template <bool BF16, bool HBF16, int VEC, bool BWD>
-__global__ void __launch_bounds__(kScanWarps * 32, 2) recur_scan_kernel(const RecurArgs A, ScanHeader* W, Word* agg, Word* inc,
-                                                                         int tiles, int blocks, int group) {
-  using In = Channels<BF16, VEC>;
-  using H = Channels<HBF16, VEC>;
-  using Out = Channels<BWD ? BF16 : HBF16, VEC>;
-  constexpr int S = scan_steps<BF16, VEC, BWD>();
-  constexpr int es = BF16 ? 2 : 4, hs = HBF16 ? 2 : 4, os = BWD ? es : hs;
-  __shared__ float sm_a[kScanWarps][VEC][32], sm_b[kScanWarps][VEC][32], sm_in[VEC][32];
-  __shared__ float sm_pa[kScanWarps][VEC][32], sm_pb[kScanWarps][VEC][32];
+// Two neighbouring channels of global memory, the second where `both`; PAIR: as one access.
+template <bool BF16, bool PAIR>
+__device__ __forceinline__ void store_pair(unsigned char* p, float2 x, bool both) {
+  if (PAIR) {
+    if (BF16) __stcs(reinterpret_cast<uint32_t*>(p), pack_bf16(x.x, x.y));
+    else __stcs(reinterpret_cast<float2*>(p), x);
+  } else if (BF16) {
+    __stcs(reinterpret_cast<uint16_t*>(p), (uint16_t)pack_bf16(x.x, 0.f));
+    if (both) __stcs(reinterpret_cast<uint16_t*>(p) + 1, (uint16_t)pack_bf16(x.y, 0.f));
+  } else {
+    __stcs(reinterpret_cast<float*>(p), x.x);
+    if (both) __stcs(reinterpret_cast<float*>(p) + 1, x.y);
+  }
+}
+
+// Fills a warp's rows of a tile from memory of any alignment.
+template <bool BF16>
+__device__ __forceinline__ void fill_rows(unsigned char* to, const unsigned char* p, long long tok_bytes, int rows, bool one, bool both) {
+  constexpr int es = BF16 ? 2 : 4;
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    unsigned char* s = to + i * kScanCh * es;
+    const unsigned char* g = p + i * tok_bytes;
+    if (BF16) {
+      uint16_t a = 0, b = 0;
+      if (one) a = __ldcs(reinterpret_cast<const uint16_t*>(g));
+      if (both) b = __ldcs(reinterpret_cast<const uint16_t*>(g) + 1);
+      *reinterpret_cast<uint32_t*>(s) = (uint32_t)a | (uint32_t)b << 16;
+    } else {
+      float2 x = make_float2(0.f, 0.f);
+      if (one) x.x = __ldcs(reinterpret_cast<const float*>(g));
+      if (both) x.y = __ldcs(reinterpret_cast<const float*>(g) + 1);
+      *reinterpret_cast<float2*>(s) = x;
+    }
+  }
+}
+
+struct ScanMaps {
+  CUtensorMap g, x, h;      // backward: g, dh, h
+};
+
+// A CTA takes a tile of 64 channels x (warps * S tokens) of a row.  Tiles go by
+// tickets, all channels of all rows before the next tokens, and a tile waits only
+// for tiles of smaller tickets, whose CTAs have begun.
+//
+// The tile comes by TMA, past the load queue through which the small loads of
+// the chain have to go.  Its tokens are read twice from shared memory, once to
+// reduce them and once, when the state that enters is known, to walk them; the
+// decay is computed both times, which leaves registers for four CTAs an SM, and
+// their loads and chain steps hide one another.
+template <bool BF16, bool HBF16, bool BWD, bool TMA>
+__global__ void __launch_bounds__(kScanWarps * 32, 4) recur_scan_kernel(const RecurArgs A, const __grid_constant__ ScanMaps maps,
+                                                                         ScanHeader* W, Word* agg, Word* inc, int tiles, int blocks,
+                                                                         int group) {
+  constexpr int S = scan_steps<BF16>();
+  constexpr int es = BF16 ? 2 : 4, hs = HBF16 ? 2 : 4, os = BWD ? es : hs, row_bytes = kScanCh * es, h_row = kScanCh * hs;
+  extern __shared__ __align__(128) unsigned char staged[];       // g, x or dh, and for the gradients h, [token][channel]
+  __shared__ float2 sm_a[kScanWarps][32], sm_b[kScanWarps][32], sm_in[32], sm_pa[kScanWarps][32], sm_pb[kScanWarps][32];
+  __shared__ __align__(8) unsigned long long full;
   __shared__ unsigned sm_ticket, sm_tag;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int span = warps * S;
+  __shared__ int failed;
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32, span = warps * S;
   if (threadIdx.x == 0) {
     sm_ticket = tiles > 1 ? atomicAdd(&W->ticket, 1u) : blockIdx.x;
     sm_tag = *(volatile unsigned*)&W->epoch + 1;
+    failed = 0;
+    if (TMA) {
+      mbar_init(&full, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
   }
   __syncthreads();
-  const unsigned tag = sm_tag;
-  const ScanTile C = scan_tile<VEC, BWD>(A, sm_ticket, tiles, blocks, lane);
-  if (!C.ok && C.tile == 0 && C.c == 0 && warp == 0 && A.flags) atomicOr(&A.flags[C.row], (uint32_t)SPEC_F_BAD_IDX);
-  const int used = (C.len + span - 1) / span;                    // tiles of this row that hold tokens
-  const int order = BWD ? used - 1 - C.tile : C.tile;            // this tile's place among them
-  const int t0 = C.tile * span + warp * S;
-  const bool whole = C.live && t0 + S <= C.len;
-  const long long base = ((long long)C.row * A.T + t0) * A.D + C.c;
+  const unsigned tag = sm_tag, ticket = sm_ticket;
+  const unsigned per = (unsigned)A.B * (unsigned)blocks, nth = ticket / per, rest = ticket - nth * per, row = rest / (unsigned)blocks;
+  const int r = (int)row, tile = BWD ? tiles - 1 - (int)nth : (int)nth, c0 = (int)(rest - row * (unsigned)blocks) * kScanCh;
+  const int c = c0 + 2 * lane;
+  const bool live = c < A.D, both = c + 1 < A.D;
+  int len;
+  long long from, to;
+  const bool ok = recur_row<BWD>(A, r, &len, &from, &to);
+  if (!ok) len = 0;
+  if (!ok && tile == 0 && c == 0 && warp == 0 && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_BAD_IDX);
+  const int used = (len + span - 1) / span;                    // tiles of this row that hold tokens
+  const int order = BWD ? used - 1 - tile : tile;              // this tile's place among them
+  const int t0 = tile * span + warp * S;
+  const long long base = ((long long)r * A.T + t0) * A.D + c;
   unsigned char* const out_p = A.h + base * os;
   unsigned char* const dg_p = BWD ? A.dg + base * es : nullptr;
   const long long out_tok = (long long)A.D * os, dg_tok = (long long)A.D * es;
 
-  if (C.tile >= used) {
+  if (tile >= used) {
     // nothing but zeros here; a row without tokens hands its state on
-    if (C.live) {
-      float zero[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) zero[v] = 0.f;
+    if (live) {
       for (int i = 0; i < S && t0 + i < A.T; ++i) {
-        Out::store(out_p + i * out_tok, zero);
-        if (BWD) In::store(dg_p + i * dg_tok, zero);
+        store_pair<BWD ? BF16 : HBF16, TMA>(out_p + i * out_tok, make_float2(0.f, 0.f), both);
+        if (BWD) store_pair<BF16, TMA>(dg_p + i * dg_tok, make_float2(0.f, 0.f), both);
       }
-      if (C.tile == 0 && warp == 0 && C.to >= 0)
-        for (int v = 0; v < VEC; ++v)
-          A.last[C.to + C.c + v] = BWD ? (A.d_last && C.ok ? A.d_last[(long long)C.row * A.D + C.c + v] : 0.f)
-                                       : (C.from >= 0 ? A.state[C.from + C.c + v] : 0.f);
+      if (tile == 0 && warp == 0 && to >= 0)
+        for (int v = 0; v < 1 + both; ++v)
+          A.last[to + c + v] = BWD ? (A.d_last && ok ? A.d_last[(long long)r * A.D + c + v] : 0.f) : (from >= 0 ? A.state[from + c + v] : 0.f);
     }
   } else {
-    In g[S], x[S];
-    const long long g_tok = A.g_tok * es, x_tok = (BWD ? (long long)A.D : A.x_tok) * es;
-    const unsigned char* gp = A.g + (C.row * A.g_row + C.c) * es + t0 * g_tok;
-    const unsigned char* xp = A.x + (BWD ? base * es : (C.row * A.x_row + C.c) * es + t0 * x_tok);
-    if (whole) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        g[i].load(gp + i * g_tok);
-        x[i].load(xp + i * x_tok);
+    unsigned char* const sm_x = staged + span * row_bytes;
+    unsigned char* const sm_h = sm_x + span * row_bytes;
+    if (TMA) {
+      if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(&full, span * (2 * row_bytes + (BWD ? h_row : 0)));
+        tma_load_3d(smem_u32(staged), &maps.g, c0, tile * span, r, &full);
+        tma_load_3d(smem_u32(sm_x), &maps.x, c0, tile * span, r, &full);
+        if (BWD) tma_load_3d(smem_u32(sm_h), &maps.h, c0, tile * span - 1, r, &full);     // the states before
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        g[i].zero();
-        x[i].zero();
-        if (C.live && t0 + i < C.len) {
-          g[i].load(gp + i * g_tok);
-          x[i].load(xp + i * x_tok);
-        }
+      const long long g_tok = A.g_tok * es, x_tok = (BWD ? (long long)A.D : A.x_tok) * es, h_tok = (long long)A.D * hs;
+      const int rows = max(0, min(S, len - t0));
+      fill_rows<BF16>(staged + (warp * S * kScanCh + 2 * lane) * es, A.g + (r * A.g_row + c) * es + t0 * g_tok, g_tok, rows, live, both);
+      fill_rows<BF16>(sm_x + (warp * S * kScanCh + 2 * lane) * es, A.x + (BWD ? base * es : (r * A.x_row + c) * es + t0 * x_tok), x_tok, rows, live, both);
+      if (BWD) {
+        const int skip = t0 == 0;      // (before the first token there is the state)
+        fill_rows<HBF16>(sm_h + ((warp * S + skip) * kScanCh + 2 * lane) * hs, A.hin + (base + (long long)(skip - 1) * A.D) * hs, h_tok, max(0, rows - skip), live, both);
       }
     }
-    // this warp's steps as one: s -> pa s + pb (a token beyond the row has g = x = 0: s -> s)
-    float a[S][VEC], pa[VEC], pb[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) pa[v] = 1.f, pb[v] = 0.f;
+    const bool whole = t0 + S <= len;
+    const uint32_t at_g = smem_u32(staged) + (warp * S * kScanCh + 2 * lane) * es, at_x = smem_u32(sm_x) + (warp * S * kScanCh + 2 * lane) * es;
+    const uint32_t at_h = smem_u32(sm_h) + (warp * S * kScanCh + 2 * lane) * hs;
+    if (TMA) mbar_await(&full, 0, &failed);
+    // this warp's steps as one: s -> pa s + pb (a token beyond the row: s -> s)
+    float2 pa = make_float2(1.f, 1.f), pb = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int n = BWD ? S - 1 - i : i;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        a[n][v] = decay(g[n].get(v));
-        pb[v] = BWD ? a[n][v] * (x[n].get(v) + pb[v]) : fmaf(a[n][v], pb[v], x[n].get(v));
-        pa[v] *= a[n][v];
+      const float2 g = lds_pair<BF16>(at_g + n * row_bytes), x = lds_pair<BF16>(at_x + n * row_bytes);
+      if (whole || t0 + n < len) {
+        const float a0 = decay(g.x), a1 = decay(g.y);
+        pb = BWD ? make_float2(a0 * (x.x + pb.x), a1 * (x.y + pb.y)) : make_float2(fmaf(a0, pb.x, x.x), fmaf(a1, pb.y, x.y));
+        pa.x *= a0;
+        pa.y *= a1;
       }
     }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) sm_a[warp][v][lane] = pa[v], sm_b[warp][v][lane] = pb[v];
+    sm_a[warp][lane] = pa;
+    sm_b[warp][lane] = pb;
     __syncthreads();
     const int ahead = order % group;                             // tiles of this group that come first
     const bool ends = ahead == group - 1, hands_on = order < used - 1;
     const bool publishes = warp == (BWD ? 0 : warps - 1);        // the last in order
-    const long long mine = ((long long)C.tile * A.B + C.row) * A.D + C.c;
-    const long long back = (BWD ? 1LL : -1LL) * A.B * A.D;       // to the tile before in order
-    float ta[VEC], tb[VEC];                                      // the whole tile, in the warp that publishes it
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      // what comes before this warp in the tile
-      float fa = 1.f, fb = 0.f;
-      for (int w = 0; w < (BWD ? warps - 1 - warp : warp); ++w) {
-        const int n = BWD ? warps - 1 - w : w;
-        const float wa = sm_a[n][v][lane];
-        fb = fmaf(wa, fb, sm_b[n][v][lane]);
-        fa *= wa;
-      }
-      ta[v] = fa * pa[v];
-      tb[v] = fmaf(pa[v], fb, pb[v]);
-      if (publishes && C.live && hands_on && !ends) {
-        put_word(agg + (mine + v) * 2, tagged(ta[v], tag));
-        put_word(agg + (mine + v) * 2 + 1, tagged(tb[v], tag));
-      }
-      pa[v] = fa;
-      pb[v] = fb;
+    const long long mine = ((long long)tile * A.B + r) * (blocks * kScanCh) + c;
+    const long long back = (BWD ? 1LL : -1LL) * A.B * (blocks * kScanCh);       // to the tile before in order
+    // what comes before this warp in the tile, and in the warp that publishes it the whole tile
+    float2 fa = make_float2(1.f, 1.f), fb = make_float2(0.f, 0.f);
+    for (int w = 0; w < (BWD ? warps - 1 - warp : warp); ++w) {
+      const int n = BWD ? warps - 1 - w : w;
+      const float2 wa = sm_a[n][lane], wb = sm_b[n][lane];
+      fb = make_float2(fmaf(wa.x, fb.x, wb.x), fmaf(wa.y, fb.y, wb.y));
+      fa = make_float2(fa.x * wa.x, fa.y * wa.y);
     }
-    H hb[BWD ? S : 1];
-    if (BWD) {
-      const unsigned char* hp = A.hin + (base - A.D) * hs;
-      const long long h_tok = (long long)A.D * hs;
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        hb[BWD ? i : 0].zero();
-        if (whole ? i > 0 || t0 > 0 : C.live && t0 + i > 0 && t0 + i < C.len) hb[BWD ? i : 0].load(hp + i * h_tok);
-      }
+    const float2 ta = make_float2(fa.x * pa.x, fa.y * pa.y), tb = make_float2(fmaf(pa.x, fb.x, pb.x), fmaf(pa.y, fb.y, pb.y));
+    if (publishes && hands_on && !ends) {
+      put_word(agg + mine * 2, tagged(ta.x, tag));
+      put_word(agg + mine * 2 + 1, tagged(tb.x, tag));
+      put_word(agg + mine * 2 + 2, tagged(ta.y, tag));
+      put_word(agg + mine * 2 + 3, tagged(tb.y, tag));
     }
     // The state that enters is that behind the group before, through the tiles of this group that come first: each
     // warp fetches some of these and joins them.  Always the same products in the same order.
     bool gave_up = false;
     if (ahead > 0) {
       const int share = (ahead + warps - 1) / warps, far = min(ahead, (warp + 1) * share);
-      float ca[VEC], cb[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) ca[v] = 1.f, cb[v] = 0.f;
-      for (int k = far; k > warp * share && C.live; --k) {
-        float w[2 * VEC];
-        await_words<2 * VEC>(agg + (mine + back * k) * 2, tag, w, &gave_up);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          cb[v] = fmaf(w[2 * v], cb[v], w[2 * v + 1]);
-          ca[v] *= w[2 * v];
-        }
+      float2 ca = make_float2(1.f, 1.f), cb = make_float2(0.f, 0.f);
+      for (int k = far; k > warp * share; --k) {
+        float w[4];
+        await_words<4>(agg + (mine + back * k) * 2, tag, w, &gave_up);
+        cb = make_float2(fmaf(w[0], cb.x, w[1]), fmaf(w[2], cb.y, w[3]));
+        ca = make_float2(ca.x * w[0], ca.y * w[2]);
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) sm_pa[warp][v][lane] = ca[v], sm_pb[warp][v][lane] = cb[v];
+      sm_pa[warp][lane] = ca;
+      sm_pb[warp][lane] = cb;
       __syncthreads();
     }
     if (publishes) {
-      float s[VEC], ca[VEC], cb[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        ca[v] = 1.f, cb[v] = 0.f, s[v] = 0.f;
-        for (int w = warps - 1; w >= 0 && ahead > 0; --w) {
-          cb[v] = fmaf(sm_pa[w][v][lane], cb[v], sm_pb[w][v][lane]);
-          ca[v] *= sm_pa[w][v][lane];
-        }
+      float2 ca = make_float2(1.f, 1.f), cb = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+      for (int w = warps - 1; w >= 0 && ahead > 0; --w) {
+        const float2 wa = sm_pa[w][lane], wb = sm_pb[w][lane];
+        cb = make_float2(fmaf(wa.x, cb.x, wb.x), fmaf(wa.y, cb.y, wb.y));
+        ca = make_float2(ca.x * wa.x, ca.y * wa.y);
       }
-      if (C.live) {
-        if (order != ahead) {
-          await_words<VEC>(inc + mine + back * (ahead + 1), tag, s, &gave_up);
-        } else {
-#pragma unroll
-          for (int v = 0; v < VEC; ++v)
-            s[v] = BWD ? (A.d_last ? A.d_last[(long long)C.row * A.D + C.c + v] : 0.f)
-                       : C.from >= 0 ? A.state[C.from + C.c + v] : 0.f;
-        }
+      if (order != ahead) {
+        float w[2];
+        await_words<2>(inc + mine + back * (ahead + 1), tag, w, &gave_up);
+        s = make_float2(w[0], w[1]);
+      } else if (live) {
+        const float* p = BWD ? (A.d_last ? A.d_last + (long long)r * A.D : nullptr) : from >= 0 ? A.state + from : nullptr;
+        if (p) s = make_float2(p[c], both ? p[c + 1] : 0.f);
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        s[v] = fmaf(ca[v], s[v], cb[v]);
-        if (C.live && hands_on && ends) put_word(inc + mine + v, tagged(fmaf(ta[v], s[v], tb[v]), tag));
-        sm_in[v][lane] = s[v];
+      s = make_float2(fmaf(ca.x, s.x, cb.x), fmaf(ca.y, s.y, cb.y));
+      if (hands_on && ends) {
+        put_word(inc + mine, tagged(fmaf(ta.x, s.x, tb.x), tag));
+        put_word(inc + mine + 1, tagged(fmaf(ta.y, s.y, tb.y), tag));
       }
+      sm_in[lane] = s;
     }
-    if (gave_up && A.flags) atomicOr(&A.flags[C.row], (uint32_t)SPEC_F_TIMEOUT);
+    if ((gave_up || failed) && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_TIMEOUT);
     __syncthreads();
-    float s[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) s[v] = fmaf(pa[v], sm_in[v][lane], pb[v]);
+    float2 s = sm_in[lane], first = make_float2(0.f, 0.f);
+    s = make_float2(fmaf(fa.x, s.x, fb.x), fmaf(fa.y, s.y, fb.y));
+    if (BWD && t0 == 0 && from >= 0 && live) first = make_float2(A.state[from + c], both ? A.state[from + c + 1] : 0.f);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int n = BWD ? S - 1 - i : i;
-      float out[VEC], dg[VEC];
-      x[n].again();
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
+      const int n = BWD ? S - 1 - i : i, t = t0 + n;
+      const float2 g = lds_pair<BF16>(at_g + n * row_bytes), x = lds_pair<BF16>(at_x + n * row_bytes);
+      float2 out = make_float2(0.f, 0.f), dg = out;
+      if (whole || t < len) {
+        const float a0 = decay(g.x), a1 = decay(g.y);
         if (BWD) {
-          out[v] = x[n].get(v) + s[v];
-          s[v] = a[n][v] * out[v];
-          float before = hb[BWD ? n : 0].get(v);
-          if (n == 0 && t0 == 0) before = C.from >= 0 && C.live ? A.state[C.from + C.c + v] : 0.f;
-          dg[v] = s[v] * before;
+          float2 before = lds_pair<HBF16>(at_h + n * h_row);
+          if (n == 0 && t0 == 0) before = first;
+          out = make_float2(x.x + s.x, x.y + s.y);
+          s = make_float2(a0 * out.x, a1 * out.y);
+          dg = make_float2(s.x * before.x, s.y * before.y);
         } else {
-          s[v] = fmaf(a[n][v], s[v], x[n].get(v));
-          out[v] = s[v];
+          out = s = make_float2(fmaf(a0, s.x, x.x), fmaf(a1, s.y, x.y));
         }
-        if (!whole && t0 + n >= C.len) out[v] = dg[v] = 0.f;
       }
-      if (whole || (C.live && t0 + n < A.T)) {
-        Out::store(out_p + n * out_tok, out);
-        if (BWD) In::store(dg_p + n * dg_tok, dg);
+      if (live && (whole || t < A.T)) {
+        store_pair<BWD ? BF16 : HBF16, TMA>(out_p + n * out_tok, out, both);
+        if (BWD) store_pair<BF16, TMA>(dg_p + n * dg_tok, dg, both);
       }
     }
-    const bool ends_row = BWD ? C.tile == 0 && warp == 0 : C.tile == used - 1 && warp == warps - 1;
-    if (C.live && ends_row && C.to >= 0)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) A.last[C.to + C.c + v] = s[v];
+    const bool ends_row = BWD ? tile == 0 && warp == 0 : tile == used - 1 && warp == warps - 1;
+    if (live && ends_row && to >= 0) {
+      A.last[to + c] = s.x;
+      if (both) A.last[to + c + 1] = s.y;
+    }
   }
   if (tiles > 1 && threadIdx.x == 0 && atomicAdd(&W->done, 1u) == gridDim.x - 1) {
     W->ticket = 0;
@@ -471,27 +488,63 @@ static ScanShape scan_shape(int T, int steps) {
   return {warps, (T + warps * steps - 1) / (warps * steps)};
 }
 
+static int scan_blocks(int D) { return (D + kScanCh - 1) / kScanCh; }
+
+// Records of the finer of the two tilings.
 static size_t scan_records(int B, int T, int D) {
   if (T <= kStepTokens) return 0;
-  return (size_t)scan_shape(T, kScanSteps).tiles * B * D;
+  return (size_t)scan_shape(T, scan_steps<false>()).tiles * B * scan_blocks(D) * kScanCh;
+}
+
+// A tensor map of [B, T, D] with channels dense, boxes of 64 channels by `tokens`; false where TMA cannot read it.
+static bool scan_map(CUtensorMap* map, const void* p, bool bf16, const RecurArgs& A, long long tok, long long row, int tokens) {
+  const TensorMapEncode encode = tensor_map_encoder();
+  const cuuint64_t es = bf16 ? 2 : 4;
+  if (A.B == 1) row = tok * A.T;
+  if (!encode || (uintptr_t)p % 16 || tok <= 0 || row <= 0 || tok * es % 16 || row * es % 16) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)A.D, (cuuint64_t)A.T, (cuuint64_t)A.B}, strides[2] = {tok * es, row * es};
+  const cuuint32_t box[3] = {kScanCh, (cuuint32_t)tokens, 1}, ones[3] = {1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(p), dims, strides,
+                box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, bool HBF16, bool BWD, bool TMA>
+static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape& S, void* workspace, cudaStream_t st) {
+  const int blocks = scan_blocks(A.D), span = S.warps * scan_steps<BF16>();
+  const long long grid = (long long)S.tiles * A.B * blocks;
+  if (grid > 0x7fffffffLL) return SPEC_E_DIM;
+  ScanHeader* W = static_cast<ScanHeader*>(workspace);
+  Word* agg = reinterpret_cast<Word*>(W + 1);
+  Word* inc = agg + 2LL * S.tiles * A.B * blocks * kScanCh;
+  const int smem = span * kScanCh * ((BF16 ? 4 : 8) + (BWD ? (HBF16 ? 2 : 4) : 0));
+  const auto kernel = recur_scan_kernel<BF16, HBF16, BWD, TMA>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_E_CUDA;
+  }
+  // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.
+  const int group = grid <= 4 * 152 ? kScanGroupMost : 16;
+  kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
+}
+
+template <bool BF16, bool HBF16, bool BWD>
+static int launch_long(const RecurArgs& A, void* workspace, cudaStream_t st) {
+  const ScanShape S = scan_shape(A.T, scan_steps<BF16>());
+  const int span = S.warps * scan_steps<BF16>();
+  const long long dense = (long long)A.T * A.D;
+  ScanMaps maps;
+  const bool tma = A.D % 8 == 0 && paged_aligned(A.h, 8) && paged_aligned(A.dg, 8) && scan_map(&maps.g, A.g, BF16, A, A.g_tok, A.g_row, span) &&
+                   scan_map(&maps.x, A.x, BF16, A, BWD ? A.D : A.x_tok, BWD ? dense : A.x_row, span) &&
+                   (!BWD || scan_map(&maps.h, A.hin, HBF16, A, A.D, dense, span));
+  return tma ? launch_scan<BF16, HBF16, BWD, true>(A, maps, S, workspace, st) : launch_scan<BF16, HBF16, BWD, false>(A, maps, S, workspace, st);
 }
 
 template <bool BF16, bool HBF16, int VEC, bool BWD>
-static int launch_recur(const RecurArgs& A, void* workspace, cudaStream_t st) {
-  if (A.T <= kStepTokens) {
-    const dim3 grid((A.D + kStepThreads * VEC - 1) / (kStepThreads * VEC), A.B);
-    recur_step_kernel<BF16, HBF16, VEC, BWD><<<grid, kStepThreads, 0, st>>>(A);
-  } else {
-    const ScanShape S = scan_shape(A.T, scan_steps<BF16, VEC, BWD>());
-    const int blocks = (A.D + 32 * VEC - 1) / (32 * VEC);
-    const long long work = (long long)S.tiles * A.B * blocks;
-    if (work > 0x7fffffffLL) return SPEC_E_DIM;
-    ScanHeader* W = static_cast<ScanHeader*>(workspace);
-    Word* agg = reinterpret_cast<Word*>(W + 1);
-    Word* inc = agg + 2LL * S.tiles * A.B * A.D;
-    const int group = work <= 2 * 152 ? kScanGroupMost : 16;
-    recur_scan_kernel<BF16, HBF16, VEC, BWD><<<(unsigned)work, S.warps * 32, 0, st>>>(A, W, agg, inc, S.tiles, blocks, group);
-  }
+static int launch_steps(const RecurArgs& A, cudaStream_t st) {
+  const dim3 grid((A.D + kStepThreads * VEC - 1) / (kStepThreads * VEC), A.B);
+  recur_step_kernel<BF16, HBF16, VEC, BWD><<<grid, kStepThreads, 0, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
@@ -503,22 +556,20 @@ static bool recur_aligned(const RecurArgs& A, int vec, size_t es, size_t hs) {
 }
 
 template <bool BF16, bool HBF16, bool BWD>
-static int launch_vec(const RecurArgs& A, void* workspace, cudaStream_t st) {
-  // 8 bytes a lane of g, less where a warp's width would leave half of its lanes idle
+static int launch_recur(const RecurArgs& A, void* workspace, cudaStream_t st) {
+  if (A.T > kStepTokens) return launch_long<BF16, HBF16, BWD>(A, workspace, st);
+  // 8 bytes a lane of g where they are aligned
   constexpr int most = BF16 ? 4 : 2;
-  if (A.D > 16 * most && recur_aligned(A, most, BF16 ? 2 : 4, HBF16 ? 2 : 4))
-    return launch_recur<BF16, HBF16, most, BWD>(A, workspace, st);
-  if (BF16 && A.D > 32 && recur_aligned(A, 2, 2, HBF16 ? 2 : 4))
-    return launch_recur<BF16, HBF16, 2, BWD>(A, workspace, st);
-  return launch_recur<BF16, HBF16, 1, BWD>(A, workspace, st);
+  if (recur_aligned(A, most, BF16 ? 2 : 4, HBF16 ? 2 : 4)) return launch_steps<BF16, HBF16, most, BWD>(A, st);
+  return launch_steps<BF16, HBF16, 1, BWD>(A, st);
 }
 
 template <bool BWD>
 static int recur_launch(const RecurArgs& A, int dtype, int h_dtype, void* workspace, cudaStream_t st) {
   const bool hb = h_dtype == SPEC_BF16;
   if (dtype == SPEC_BF16)
-    return hb ? launch_vec<true, true, BWD>(A, workspace, st) : launch_vec<true, false, BWD>(A, workspace, st);
-  return hb ? launch_vec<false, true, BWD>(A, workspace, st) : launch_vec<false, false, BWD>(A, workspace, st);
+    return hb ? launch_recur<true, true, BWD>(A, workspace, st) : launch_recur<true, false, BWD>(A, workspace, st);
+  return hb ? launch_recur<false, true, BWD>(A, workspace, st) : launch_recur<false, false, BWD>(A, workspace, st);
 }
 
 static bool recur_dims(int B, int T, int D) { return B >= 0 && B <= 65535 && T >= 0 && D >= 1 && D <= (1 << 26); }
