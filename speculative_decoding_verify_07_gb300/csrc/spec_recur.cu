@@ -103,6 +103,39 @@ __device__ __forceinline__ float decay(float g) {
   return fabsf(g) < 0.03125f ? near : a;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both_of(float x) { return make_float2(x, x); }
+
+// decay() of two channels.
+__device__ __forceinline__ float2 decay2(float2 g) {
+  const float2 y = mul2(g, both_of(1.4426950408889634f));
+  float2 a;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(y.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(y.y));
+  const float2 near = fma2(fma2(fma2(g, both_of(1.f / 6.f), both_of(0.5f)), g, both_of(1.f)), g, both_of(1.f));
+  return make_float2(fabsf(g.x) < 0.03125f ? near.x : a.x, fabsf(g.y) < 0.03125f ? near.y : a.y);
+}
+
 // ---------------------------------------------------------------- few tokens
 
 constexpr int kStepThreads = 256;
@@ -286,7 +319,7 @@ struct ScanMaps {
 // decay is computed both times, which leaves registers for four CTAs an SM, and
 // their loads and chain steps hide one another.
 template <bool BF16, bool HBF16, bool BWD, bool TMA>
-__global__ void __launch_bounds__(kScanWarps * 32, 4) recur_scan_kernel(const RecurArgs A, const __grid_constant__ ScanMaps maps,
+__global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_scan_kernel(const RecurArgs A, const __grid_constant__ ScanMaps maps,
                                                                          ScanHeader* W, Word* agg, Word* inc, int tiles, int blocks,
                                                                          int group) {
   constexpr int S = scan_steps<BF16>();
@@ -361,17 +394,19 @@ __global__ void __launch_bounds__(kScanWarps * 32, 4) recur_scan_kernel(const Re
     const uint32_t at_h = smem_u32(sm_h) + (warp * S * kScanCh + 2 * lane) * hs;
     if (TMA) mbar_await(&full, 0, &failed);
     // this warp's steps as one: s -> pa s + pb (a token beyond the row: s -> s)
-    float2 pa = make_float2(1.f, 1.f), pb = make_float2(0.f, 0.f);
+    float2 pa = both_of(1.f), pb = both_of(0.f);
+    auto reduce = [&](int n) {
+      const float2 a = decay2(lds_pair<BF16>(at_g + n * row_bytes)), x = lds_pair<BF16>(at_x + n * row_bytes);
+      pb = BWD ? mul2(a, add2(x, pb)) : fma2(a, pb, x);
+      pa = mul2(pa, a);
+    };
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int n = BWD ? S - 1 - i : i;
-      const float2 g = lds_pair<BF16>(at_g + n * row_bytes), x = lds_pair<BF16>(at_x + n * row_bytes);
-      if (whole || t0 + n < len) {
-        const float a0 = decay(g.x), a1 = decay(g.y);
-        pb = BWD ? make_float2(a0 * (x.x + pb.x), a1 * (x.y + pb.y)) : make_float2(fmaf(a0, pb.x, x.x), fmaf(a1, pb.y, x.y));
-        pa.x *= a0;
-        pa.y *= a1;
-      }
+      for (int i = 0; i < S; ++i) reduce(BWD ? S - 1 - i : i);
+    } else {
+      const int rows = max(0, min(S, len - t0));
+#pragma unroll 1
+      for (int i = 0; i < rows; ++i) reduce(BWD ? rows - 1 - i : i);
     }
     sm_a[warp][lane] = pa;
     sm_b[warp][lane] = pb;
@@ -439,26 +474,32 @@ __global__ void __launch_bounds__(kScanWarps * 32, 4) recur_scan_kernel(const Re
     float2 s = sm_in[lane], first = make_float2(0.f, 0.f);
     s = make_float2(fmaf(fa.x, s.x, fb.x), fmaf(fa.y, s.y, fb.y));
     if (BWD && t0 == 0 && from >= 0 && live) first = make_float2(A.state[from + c], both ? A.state[from + c + 1] : 0.f);
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int n = BWD ? S - 1 - i : i, t = t0 + n;
-      const float2 g = lds_pair<BF16>(at_g + n * row_bytes), x = lds_pair<BF16>(at_x + n * row_bytes);
-      float2 out = make_float2(0.f, 0.f), dg = out;
-      if (whole || t < len) {
-        const float a0 = decay(g.x), a1 = decay(g.y);
+    auto walk = [&](int n, bool inside) {
+      float2 out = both_of(0.f), dg = out;
+      if (inside) {
+        const float2 a = decay2(lds_pair<BF16>(at_g + n * row_bytes)), x = lds_pair<BF16>(at_x + n * row_bytes);
         if (BWD) {
           float2 before = lds_pair<HBF16>(at_h + n * h_row);
           if (n == 0 && t0 == 0) before = first;
-          out = make_float2(x.x + s.x, x.y + s.y);
-          s = make_float2(a0 * out.x, a1 * out.y);
-          dg = make_float2(s.x * before.x, s.y * before.y);
+          out = add2(x, s);
+          s = mul2(a, out);
+          dg = mul2(s, before);
         } else {
-          out = s = make_float2(fmaf(a0, s.x, x.x), fmaf(a1, s.y, x.y));
+          out = s = fma2(a, s, x);
         }
       }
-      if (live && (whole || t < A.T)) {
-        store_pair<BWD ? BF16 : HBF16, TMA>(out_p + n * out_tok, out, both);
-        if (BWD) store_pair<BF16, TMA>(dg_p + n * dg_tok, dg, both);
+      store_pair<BWD ? BF16 : HBF16, TMA>(out_p + n * out_tok, out, both);
+      if (BWD) store_pair<BF16, TMA>(dg_p + n * dg_tok, dg, both);
+    };
+    if (whole && live) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) walk(BWD ? S - 1 - i : i, true);
+    } else if (live) {
+      const int rows = min(S, A.T - t0);
+#pragma unroll 1
+      for (int i = 0; i < rows; ++i) {
+        const int n = BWD ? rows - 1 - i : i;
+        walk(n, t0 + n < len);
       }
     }
     const bool ends_row = BWD ? tile == 0 && warp == 0 : tile == used - 1 && warp == warps - 1;
@@ -524,7 +565,7 @@ static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape
     return SPEC_E_CUDA;
   }
   // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.
-  const int group = grid <= 4 * 152 ? kScanGroupMost : 16;
+  const int group = grid <= (TMA && !BWD ? 5 : 4) * 152 ? kScanGroupMost : 16;
   kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
