@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -43,12 +44,9 @@ SPEC_MAX_V = 524288
 SPEC_MAX_K = 16
 
 
-class CacheView(ctypes.Structure):
-    """spec_cache_t of include/spec_forward.h."""
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_exp", "v_exp", "page_table", "cu_tokens",
-                                                "kv_len")]
-                + [(n, ctypes.c_int64) for n in ("page_stride", "exp_stride")]
-                + [(n, ctypes.c_int32) for n in ("dtype", "B", "max_pages", "pages", "heads", "page_size", "head_dim")])
+# spec_cache_t of include/spec_forward.h, as bytes: k_pages, v_pages, k_exp, v_exp, page_table, cu_tokens, kv_len;
+# page_stride, exp_stride; dtype, B, max_pages, pages, heads, page_size, head_dim.
+CACHE_T = struct.Struct("@7Q2q7i")
 
 
 class SpecError(RuntimeError):
@@ -82,7 +80,7 @@ def _load():
     lib.spec_draft_workspace_size.restype = sz
     lib.spec_draft_sample.argtypes = [vp, i32, vp, u64, u32, u32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.spec_draft_sample.restype = i32
-    i64, cache = ctypes.c_int64, ctypes.POINTER(CacheView)
+    i64, cache = ctypes.c_int64, ctypes.c_char_p
     lib.spec_cache_write.argtypes = [vp, vp, i32, i64, i32, cache, vp, vp]
     lib.spec_cache_write.restype = i32
     lib.spec_cache_read.argtypes = [vp, vp, i32, cache, vp, vp]
@@ -481,10 +479,12 @@ def philox4x32_10(ctr: torch.Tensor, seed: int, stream=None) -> torch.Tensor:
     return out
 
 
-# The forward's sequence mixers (include/spec_forward.h).
+# The forward's sequence mixers (include/spec_forward.h).  A step makes several of
+# these calls a layer, so their checks read each attribute of a tensor once.
 
 _POOL_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
 _IO_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _io_dtype(t, name):
@@ -494,8 +494,16 @@ def _io_dtype(t, name):
     return dt
 
 
+def _expect(t, name, dtype, shape, dev):
+    """_check for a call's small tensors; the message is made by _check."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check(t, name, dtype, shape, dev)
+
+
 def _page_stride(a, b, names, per_page):
     """Elements from page to page of two pools whose pages are dense inside."""
+    if a.is_contiguous() and b.is_contiguous():
+        return per_page
     strides = []
     for t, name in zip((a, b), names):
         inner = 1
@@ -511,38 +519,42 @@ def _page_stride(a, b, names, per_page):
     return strides[0]
 
 
-def _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp):
-    """spec_cache_t of a batch's tensors, checked.  The struct holds raw
-    pointers: the tensors outlive the call that it is made for."""
+def _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags):
+    """(spec_cache_t, B, heads, head_dim) of a batch's tensors, checked.  The
+    bytes hold raw pointers: the tensors outlive the call that they are made for."""
     dt = _POOL_DTYPES.get(k_pages.dtype)
     if dt is None:
         raise TypeError("the cache must be bfloat16 or float8_e4m3fn")
-    if k_pages.dim() != 4:
+    shape, dev = k_pages.shape, k_pages.device
+    if len(shape) != 4:
         raise ValueError("k_pages must be [pages, heads, page_size, head_dim]")
-    pages, heads, page_size, dim = k_pages.shape
-    dev = k_pages.device
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != dev:
+    pages, heads, page_size, dim = shape
+    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype or v_pages.device != dev:
         raise ValueError("v_pages must be like k_pages")
-    if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1 or page_table.dim() != 2:
+    if cu_tokens.dim() != 1 or page_table.dim() != 2:
         raise ValueError("cu_tokens must be [B + 1] and page_table [B, max_pages]")
     B, max_pages = page_table.shape
-    _check(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
-    _check(kv_len, "kv_len", torch.int32, (B,), dev)
-    _check(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    exp_stride = 0
+    i32 = torch.int32
+    _expect(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    _expect(kv_len, "kv_len", i32, (B,), dev)
+    _expect(page_table, "page_table", i32, (B, max_pages), dev)
+    if flags is not None:
+        _expect(flags, "flags", i32, (B,), dev)
+    ke = ve = exp_stride = 0
     if dt == SPEC_E4M3:
         for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
             if t is None:
                 raise ValueError(f"an e4m3 cache needs {name}")
-            if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != (pages, heads, page_size):
+            if t.dtype is not torch.uint8 or t.device != dev or t.shape != (pages, heads, page_size):
                 raise ValueError(f"{name} must be uint8 [pages, heads, page_size] on {dev}")
         exp_stride = _page_stride(k_exp, v_exp, ("k_exp", "v_exp"), heads * page_size)
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("a bfloat16 cache has no exponents")
-    return CacheView(k_pages.data_ptr(), v_pages.data_ptr(), None if k_exp is None else k_exp.data_ptr(),
-                     None if v_exp is None else v_exp.data_ptr(), page_table.data_ptr(), cu_tokens.data_ptr(),
-                     kv_len.data_ptr(), _page_stride(k_pages, v_pages, ("k_pages", "v_pages"), heads * page_size * dim),
-                     exp_stride, dt, B, max_pages, pages, heads, page_size, dim)
+    page_stride = _page_stride(k_pages, v_pages, ("k_pages", "v_pages"), heads * page_size * dim)
+    view = CACHE_T.pack(k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, page_table.data_ptr(), cu_tokens.data_ptr(),
+                        kv_len.data_ptr(), page_stride, exp_stride, dt, B, max_pages, pages, heads, page_size, dim)
+    return view, B, heads, dim
 
 
 def _token_stride(t, name):
@@ -550,18 +562,32 @@ def _token_stride(t, name):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [N, heads, head_dim]")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    token, head, one = t.stride()
+    if (d > 1 and one != 1) or (h > 1 and head != d):
         raise ValueError(f"{name} must be dense within a token")
-    return t.stride(0) if n > 1 else h * d
+    return token if n > 1 else h * d
 
 
-def _flags_ok(flags, B, dev):
-    if flags is not None:
-        _check(flags, "flags", torch.int32, (B,), dev)
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _queue(stream, dev):
+    """The raw stream that a call goes to: the given one, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev.index) if dev.type == "cuda" else None
+
+
+def _empty(shape, dtype, dev, stream):
+    """What a call allocates for itself is allocated on the stream that it runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _on(stream):
-    """What a call allocates for itself is allocated (and cleared) on the stream that it runs on."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
@@ -580,15 +606,14 @@ def spec_cache_write(k, v, cu_tokens, kv_len, page_table, k_pages, v_pages, k_ex
     v_pages [pages, heads, page_size, head_dim] bfloat16 or float8_e4m3fn, the
     latter with k_exp, v_exp [pages, heads, page_size] uint8; flags [B] int32.
     """
-    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
-    dt, stride, shape = _io_dtype(k, "k"), _token_stride(k, "k"), (k.shape[0], view.heads, view.head_dim)
-    if tuple(k.shape) != shape or k.device != k_pages.device:
-        raise ValueError(f"k must be {shape} on {k_pages.device}")
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or _token_stride(v, "v") != stride:
+    view, _, heads, dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
+    dt, stride, shape, dev = _io_dtype(k, "k"), _token_stride(k, "k"), k.shape, k.device
+    if shape[1] != heads or shape[2] != dim or dev != k_pages.device:
+        raise ValueError(f"k must be [N, {heads}, {dim}] on {k_pages.device}")
+    if v.shape != shape or v.dtype != k.dtype or v.device != dev or (v.stride() != k.stride() and _token_stride(v, "v") != stride):
         raise ValueError("v must be like k")
-    _flags_ok(flags, view.B, k.device)
-    _done(LIB.spec_cache_write(k.data_ptr(), v.data_ptr(), dt, stride, shape[0], view, _ptr(flags), _stream(stream)),
-          "spec_cache_write")
+    rc = LIB.spec_cache_write(k.data_ptr(), v.data_ptr(), dt, stride, shape[0], view, _at(flags), _queue(stream, dev))
+    _done(rc, "spec_cache_write")
 
 
 def spec_cache_read(tokens, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, k=None, v=None,
@@ -596,17 +621,18 @@ def spec_cache_read(tokens, cu_tokens, kv_len, page_table, k_pages, v_pages, k_e
     """Read `tokens` = cu_tokens[B] packed tokens back as bfloat16 (see
     spec_cache_read in spec_forward.h); returns (k, v), each [tokens, heads,
     head_dim]."""
-    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
-    shape, dev = (int(tokens), view.heads, view.head_dim), k_pages.device
-    with _on(stream):
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _check(k, "k", torch.bfloat16, shape, dev)
-    _check(v, "v", torch.bfloat16, shape, dev)
-    _flags_ok(flags, view.B, dev)
-    _done(LIB.spec_cache_read(k.data_ptr(), v.data_ptr(), shape[0], view, _ptr(flags), _stream(stream)), "spec_cache_read")
+    view, _, heads, dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
+    shape, dev = (int(tokens), heads, dim), k_pages.device
+    if k is None:
+        k = _empty(shape, torch.bfloat16, dev, stream)
+    else:
+        _expect(k, "k", torch.bfloat16, shape, dev)
+    if v is None:
+        v = _empty(shape, torch.bfloat16, dev, stream)
+    else:
+        _expect(v, "v", torch.bfloat16, shape, dev)
+    rc = LIB.spec_cache_read(k.data_ptr(), v.data_ptr(), shape[0], view, _at(flags), _queue(stream, dev))
+    _done(rc, "spec_cache_read")
     return k, v
 
 
@@ -630,27 +656,29 @@ def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, 
     tokens of a row.  Returns (out [N, heads * group, head_dim] bfloat16,
     lse [N, heads * group] float32).
     """
-    view = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp)
+    view, _, heads, head_dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
     stride, dev = _token_stride(q, "q"), k_pages.device
-    N, hq, dim = q.shape
-    if q.dtype != torch.bfloat16:
+    shape = q.shape
+    N, hq, dim = shape
+    if q.dtype is not torch.bfloat16:
         raise TypeError("q must be bfloat16")
-    if dim != view.head_dim or hq % view.heads or q.device != dev:
-        raise ValueError(f"q must be [N, a multiple of {view.heads}, {view.head_dim}] on {dev}")
-    group = hq // view.heads
-    with _on(stream):
-        if out is None:
-            out = torch.empty((N, hq, dim), dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty((N, hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = new_attend_workspace(view.heads, group, dim, dev)
-    _check(out, "out", torch.bfloat16, (N, hq, dim), dev)
-    _check(lse, "lse", torch.float32, (N, hq), dev)
-    _flags_ok(flags, view.B, dev)
-    _done(LIB.spec_attend(q.data_ptr(), stride, N, group, dim ** -0.5 if scale is None else scale, int(max_tokens), view,
-                          out.data_ptr(), lse.data_ptr(), _ptr(flags), workspace.data_ptr(), workspace.numel(),
-                          _stream(stream)), "spec_attend")
+    if dim != head_dim or hq % heads or q.device != dev:
+        raise ValueError(f"q must be [N, a multiple of {heads}, {head_dim}] on {dev}")
+    if out is None:
+        out = _empty(shape, torch.bfloat16, dev, stream)
+    else:
+        _expect(out, "out", torch.bfloat16, (N, hq, dim), dev)
+    if lse is None:
+        lse = _empty((N, hq), torch.float32, dev, stream)
+    else:
+        _expect(lse, "lse", torch.float32, (N, hq), dev)
+    if workspace is None:
+        with _on(stream):
+            workspace = new_attend_workspace(heads, hq // heads, dim, dev)
+    rc = LIB.spec_attend(q.data_ptr(), stride, N, hq // heads, dim ** -0.5 if scale is None else scale, max_tokens, view,
+                         out.data_ptr(), lse.data_ptr(), _at(flags), workspace.data_ptr(), workspace.numel(),
+                         _queue(stream, dev))
+    _done(rc, "spec_attend")
     return out, lse
 
 
@@ -664,24 +692,25 @@ def new_recur_workspace(B: int, T: int, D: int, device) -> torch.Tensor:
 
 
 def _recur_strides(t, name, shape, dtype, dev):
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} {shape} on {dev}")
-    if shape[2] > 1 and t.stride(2) != 1:
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}")
+    row, tok, one = t.stride()
+    if shape[2] > 1 and one != 1:
         raise ValueError(f"{name} must have dense channels")
-    return t.stride(0), t.stride(1)
+    return row, tok
 
 
-def _recur_state(state, slot, lens, B, D, dev):
+def _recur_rows(state, slot, lens, flags, B, D, dev):
+    """The per-row arguments, checked; the number of states."""
     slots = 0
     if state is not None:
         if state.dim() != 2:
             raise ValueError("state must be [slots, D]")
         slots = state.shape[0]
-        _check(state, "state", torch.float32, (slots, D), dev)
-    if slot is not None:
-        _check(slot, "slot", torch.int32, (B,), dev)
-    if lens is not None:
-        _check(lens, "lens", torch.int32, (B,), dev)
+        _expect(state, "state", torch.float32, (slots, D), dev)
+    for t, name in ((slot, "slot"), (lens, "lens"), (flags, "flags")):
+        if t is not None:
+            _expect(t, name, torch.int32, (B,), dev)
     return slots
 
 
@@ -696,26 +725,30 @@ def spec_recur(g, x, state=None, slot=None, lens=None, *, h=None, h_dtype=torch.
     """
     if g.dim() != 3:
         raise ValueError("g must be [B, T, D]")
-    B, T, D = shape = tuple(g.shape)
-    dev, dt = g.device, _io_dtype(g, "g")
+    shape, dev, dt = g.shape, g.device, _io_dtype(g, "g")
+    B, T, D = shape
     g_row, g_tok = _recur_strides(g, "g", shape, g.dtype, dev)
     x_row, x_tok = _recur_strides(x, "x", shape, g.dtype, dev)
-    slots = _recur_state(state, slot, lens, B, D, dev)
-    with _on(stream):
-        if h is None:
-            h = torch.empty(shape, dtype=h_dtype, device=dev)
-        if last is None:
-            last = torch.empty((B, D), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = new_recur_workspace(B, T, D, dev)
-    _check(h, "h", h.dtype, shape, dev)
-    _check(last, "last", torch.float32, (last.shape[0], D), dev)
+    slots = _recur_rows(state, slot, lens, flags, B, D, dev)
+    if h is None:
+        h = _empty(shape, h_dtype, dev, stream)
+    else:
+        _expect(h, "h", h.dtype, shape, dev)
+    if last is None:
+        last = _empty((B, D), torch.float32, dev, stream)
+        last_slots = B
+    else:
+        last_slots = last.shape[0]
+        _expect(last, "last", torch.float32, (last_slots, D), dev)
     if last_slot is not None:
-        _check(last_slot, "last_slot", torch.int32, (B,), dev)
-    _flags_ok(flags, B, dev)
-    _done(LIB.spec_recur(g.data_ptr(), g_row, g_tok, x.data_ptr(), x_row, x_tok, dt, _ptr(state), _ptr(slot), slots,
-                         _ptr(lens), B, T, D, h.data_ptr(), _io_dtype(h, "h"), last.data_ptr(), _ptr(last_slot),
-                         last.shape[0], _ptr(flags), workspace.data_ptr(), workspace.numel(), _stream(stream)), "spec_recur")
+        _expect(last_slot, "last_slot", torch.int32, (B,), dev)
+    if workspace is None:
+        with _on(stream):
+            workspace = new_recur_workspace(B, T, D, dev)
+    rc = LIB.spec_recur(g.data_ptr(), g_row, g_tok, x.data_ptr(), x_row, x_tok, dt, _at(state), _at(slot), slots, _at(lens),
+                        B, T, D, h.data_ptr(), _io_dtype(h, "h"), last.data_ptr(), _at(last_slot), last_slots, _at(flags),
+                        workspace.data_ptr(), workspace.numel(), _queue(stream, dev))
+    _done(rc, "spec_recur")
     return h, last
 
 
@@ -726,29 +759,31 @@ def spec_recur_backward(g, h, dh, state=None, slot=None, lens=None, d_last=None,
     dtype, d_last [B, D] float32 or None.  Returns (dg, dx, d_state)."""
     if g.dim() != 3:
         raise ValueError("g must be [B, T, D]")
-    B, T, D = shape = tuple(g.shape)
-    dev, dt = g.device, _io_dtype(g, "g")
+    shape, dev, dt = g.shape, g.device, _io_dtype(g, "g")
+    B, T, D = shape
     g_row, g_tok = _recur_strides(g, "g", shape, g.dtype, dev)
-    _check(dh, "dh", g.dtype, shape, dev)
-    _check(h, "h", h.dtype, shape, dev)
-    slots = _recur_state(state, slot, lens, B, D, dev)
+    _expect(dh, "dh", g.dtype, shape, dev)
+    _expect(h, "h", h.dtype, shape, dev)
+    slots = _recur_rows(state, slot, lens, flags, B, D, dev)
     if d_last is not None:
-        _check(d_last, "d_last", torch.float32, (B, D), dev)
-    with _on(stream):
-        if dg is None:
-            dg = torch.empty(shape, dtype=g.dtype, device=dev)
-        if dx is None:
-            dx = torch.empty(shape, dtype=g.dtype, device=dev)
-        if d_state is None:
-            d_state = torch.empty((B, D), dtype=torch.float32, device=dev)
-        if workspace is None:
+        _expect(d_last, "d_last", torch.float32, (B, D), dev)
+    if dg is None:
+        dg = _empty(shape, g.dtype, dev, stream)
+    else:
+        _expect(dg, "dg", g.dtype, shape, dev)
+    if dx is None:
+        dx = _empty(shape, g.dtype, dev, stream)
+    else:
+        _expect(dx, "dx", g.dtype, shape, dev)
+    if d_state is None:
+        d_state = _empty((B, D), torch.float32, dev, stream)
+    else:
+        _expect(d_state, "d_state", torch.float32, (B, D), dev)
+    if workspace is None:
+        with _on(stream):
             workspace = new_recur_workspace(B, T, D, dev)
-    _check(dg, "dg", g.dtype, shape, dev)
-    _check(dx, "dx", g.dtype, shape, dev)
-    _check(d_state, "d_state", torch.float32, (B, D), dev)
-    _flags_ok(flags, B, dev)
-    _done(LIB.spec_recur_backward(g.data_ptr(), g_row, g_tok, h.data_ptr(), _io_dtype(h, "h"), dh.data_ptr(), _ptr(d_last),
-                                  dt, _ptr(state), _ptr(slot), slots, _ptr(lens), B, T, D, dg.data_ptr(), dx.data_ptr(),
-                                  d_state.data_ptr(), _ptr(flags), workspace.data_ptr(), workspace.numel(),
-                                  _stream(stream)), "spec_recur_backward")
+    rc = LIB.spec_recur_backward(g.data_ptr(), g_row, g_tok, h.data_ptr(), _io_dtype(h, "h"), dh.data_ptr(), _at(d_last), dt,
+                                 _at(state), _at(slot), slots, _at(lens), B, T, D, dg.data_ptr(), dx.data_ptr(),
+                                 d_state.data_ptr(), _at(flags), workspace.data_ptr(), workspace.numel(), _queue(stream, dev))
+    _done(rc, "spec_recur_backward")
     return dg, dx, d_state

@@ -658,10 +658,8 @@ static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
   using S = RowsShape<D, E4M3, MT>;
   static_assert(S::stages >= 2, "a ring needs two stages");
   const auto kernel = attend_rows_kernel<D, E4M3, MT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SPEC_E_CUDA;
-  }
+  static std::atomic<unsigned long long> allowed;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
   kernel<<<S::ctas * 152, kRowsThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }

@@ -747,10 +747,8 @@ static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
   using S = WideShape<D, E4M3, SPLIT>;
   static_assert(S::v_stages >= 2, "a ring needs two stages");
   const auto kernel = attend_wide_kernel<D, E4M3, SPLIT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SPEC_E_CUDA;
-  }
+  static std::atomic<unsigned long long> allowed;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
   kernel<<<152, kWideThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }

@@ -558,12 +558,11 @@ static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape
   ScanHeader* W = static_cast<ScanHeader*>(workspace);
   Word* agg = reinterpret_cast<Word*>(W + 1);
   Word* inc = agg + 2LL * S.tiles * A.B * blocks * kScanCh;
-  const int smem = span * kScanCh * ((BF16 ? 4 : 8) + (BWD ? (HBF16 ? 2 : 4) : 0));
+  constexpr int token_bytes = kScanCh * ((BF16 ? 4 : 8) + (BWD ? (HBF16 ? 2 : 4) : 0));
+  const int smem = span * token_bytes;
   const auto kernel = recur_scan_kernel<BF16, HBF16, BWD, TMA>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SPEC_E_CUDA;
-  }
+  static std::atomic<unsigned long long> allowed;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), kScanWarps * scan_steps<BF16>() * token_bytes, &allowed)) return SPEC_E_CUDA;
   // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.
   const int group = grid <= (TMA && !BWD ? 5 : 4) * 152 ? kScanGroupMost : 16;
   kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);

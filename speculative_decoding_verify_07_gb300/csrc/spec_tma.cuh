@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spec_device.cuh"
 
 namespace specv {
@@ -12,6 +14,20 @@ namespace specv {
 using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                      const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                      CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Lets a kernel have `bytes` of shared memory, once a device; `done` is the kernel's own.
+inline bool allow_shared(const void* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done->load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done->fetch_or(bit);
+  return true;
+}
 
 // cuTensorMapEncodeTiled, looked up once (the library does not link the driver); null where there is none.
 TensorMapEncode tensor_map_encoder();

@@ -1,5 +1,4 @@
 """Refusals of the forward's entry points, which need no GPU: arguments are checked before CUDA is touched."""
-import ctypes
 import os
 import re
 
@@ -30,8 +29,8 @@ def view(sv, **kw):
     a = dict(k=P, v=P, ke=None, ve=None, table=P, cu=P, kv=P, pstride=0, estride=0, pool=1, B=2, max_pages=3, pages=5,
              heads=2, ps=16, dim=64)
     a.update(kw)
-    return sv.CacheView(a["k"], a["v"], a["ke"], a["ve"], a["table"], a["cu"], a["kv"], a["pstride"], a["estride"],
-                        a["pool"], a["B"], a["max_pages"], a["pages"], a["heads"], a["ps"], a["dim"])
+    return sv.CACHE_T.pack(*(a[n] or 0 for n in ("k", "v", "ke", "ve", "table", "cu", "kv")), a["pstride"], a["estride"],
+                           a["pool"], a["B"], a["max_pages"], a["pages"], a["heads"], a["ps"], a["dim"])
 
 
 CACHE = [
