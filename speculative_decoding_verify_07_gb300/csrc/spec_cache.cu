@@ -10,10 +10,11 @@
 // range), and what is read back is exact in bf16.  One exponent byte a
 // vector costs 1/128 of an 8-bit cache.
 //
-// Both kernels are bound by memory (3 bytes an element for bf16 to e4m3).
-// A CTA takes a run of (token, key or value, head, lane) items in the order
-// of the packed array; the tokens' places in the cache are looked up once a
-// CTA, into shared memory, while the loads of the items are in flight.
+// Both kernels are bound by memory (3 bytes an element for bf16 to e4m3).  A
+// token's vectors, key and value of every head, take 2 * heads * D / 8 lanes; a
+// thread keeps its place among them and takes U tokens, all of whose loads are
+// begun before the first is used.  The tokens' places in the cache are looked up
+// once a CTA, into shared memory, while the loads are in flight.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,20 +30,19 @@ struct CacheIO {
   PagedCache C;
   unsigned char* kv[2];      // packed keys and values
   long long token_bytes;     // from one token to the next
-  long long items;           // N * 2 * heads * (D / 8)
   int N;
+  int lanes;                 // of a token: 2 * heads * (D / 8)
+  int across, at_once;       // of these, in a CTA; and tokens that it takes at a time
   uint32_t* flags;
 };
 
-// Where the run of items starting at `first` finds its tokens: the byte offset
-// of each token's page and slot, in shared memory; -1 where there is none.
+// Where a token is in the cache.
 struct TokenPlace {
   long long page;   // page index, or -1
   int slot;
   int row;
 };
 
-// `bad`: flag the row of a token without a place.
 __device__ __forceinline__ TokenPlace find_place(const CacheIO& A, int token) {
   TokenPlace t;
   t.page = -1;
@@ -56,60 +56,67 @@ __device__ __forceinline__ TokenPlace find_place(const CacheIO& A, int token) {
   return t;
 }
 
-struct Item {
+// A thread's place among a token's lanes, and its first token.
+struct Place {
   int token, head, kv, lane;
+  bool live;
 };
 
-template <int LPV>
-__device__ __forceinline__ Item item_of(const CacheIO& A, long long i) {
-  Item t;
-  t.lane = (int)(i % LPV);
-  const unsigned vec = (unsigned)(i / LPV);
-  const unsigned per = 2u * (unsigned)A.C.heads;
-  t.token = (int)(vec / per);
-  const unsigned rest = vec - (unsigned)t.token * per;
-  t.kv = rest >= (unsigned)A.C.heads;
-  t.head = (int)(rest - (t.kv ? (unsigned)A.C.heads : 0u));
-  return t;
-}
-
-// The tokens of a CTA's run, at most one more than its items' share.
 template <int LPV, int U>
-__device__ __forceinline__ void run_places(const CacheIO& A, TokenPlace* places, int* first_token) {
-  const long long first = (long long)blockIdx.x * (kCacheThreads * U);
-  const long long last = min(first + kCacheThreads * U, A.items) - 1;
-  const long long per = 2LL * A.C.heads * LPV;
-  const int t0 = (int)(first / per), t1 = (int)(last / per);
-  for (int t = t0 + threadIdx.x; t <= t1; t += kCacheThreads) places[t - t0] = find_place(A, t);
-  *first_token = t0;
+__device__ __forceinline__ Place thread_place(const CacheIO& A, TokenPlace* places) {
+  const int first = blockIdx.x * U * A.at_once, count = min(U * A.at_once, A.N - first);
+  for (int t = threadIdx.x; t < count; t += kCacheThreads) places[t] = find_place(A, first + t);
+  Place p;
+  const int turn = threadIdx.x / A.across, w = blockIdx.y * kCacheThreads + threadIdx.x - turn * A.across;
+  p.live = turn < A.at_once && w < A.lanes;
+  p.token = first + turn;
+  p.lane = w % LPV;
+  const int vec = w / LPV;
+  p.kv = vec >= A.C.heads;
+  p.head = vec - (p.kv ? A.C.heads : 0);
+  return p;
 }
 
 template <bool F32, bool E4M3, int LPV, int U>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheIO A) {
-  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV) + 2];
-  const long long first = (long long)blockIdx.x * (kCacheThreads * U) + threadIdx.x;
+  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV)];
+  const Place P = thread_place<LPV, U>(A, places);
+  const unsigned char* from = A.kv[P.kv] + P.token * A.token_bytes + ((long long)P.head * LPV + P.lane) * (F32 ? 32 : 16);
+  const long long step = A.at_once * A.token_bytes;
   uint4 raw[U][F32 ? 2 : 1];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long i = first + u * kCacheThreads;
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int w = 0; w < (F32 ? 2 : 1); ++w) raw[u][w] = make_uint4(0, 0, 0, 0);
-    if (i < A.items) {
-      const Item t = item_of<LPV>(A, i);
-      const uint4* p = reinterpret_cast<const uint4*>(A.kv[t.kv] + t.token * A.token_bytes +
-                                                      ((long long)t.head * LPV + t.lane) * (F32 ? 32 : 16));
-#pragma unroll
-      for (int w = 0; w < (F32 ? 2 : 1); ++w) raw[u][w] = __ldcs(p + w);
+    for (int w = 0; w < (F32 ? 2 : 1); ++w) {
+      raw[u][w] = make_uint4(0, 0, 0, 0);
+      if (P.live && P.token + u * A.at_once < A.N) raw[u][w] = __ldcs(reinterpret_cast<const uint4*>(from + u * step) + w);
     }
-  }
-  int t0;
-  run_places<LPV, U>(A, places, &t0);
   __syncthreads();
+  const int turn = P.token - blockIdx.x * U * A.at_once;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long i = first + u * kCacheThreads;
-    const bool live = i < A.items;
-    const Item t = item_of<LPV>(A, live ? i : 0);
+    // the largest magnitude as bits: NaN above infinity above every number
+    uint32_t amax;
+    if (F32) {
+      const uint4 a = raw[u][0], b = raw[u][F32 ? 1 : 0];
+      constexpr uint32_t m = 0x7fffffffu;
+      amax = max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)), max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
+#pragma unroll
+      for (int o = LPV / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    } else {
+      const uint4 a = raw[u][0];
+      constexpr uint32_t m = 0x7fff7fffu;
+      uint32_t two = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+#pragma unroll
+      for (int o = LPV / 2; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+      amax = max(two << 16, two & 0xffff0000u);
+    }
+    if (!P.live || P.token + u * A.at_once >= A.N) continue;
+    const TokenPlace at = places[turn + u * A.at_once];
+    if (P.lane == 0 && amax >= 0x7f800000u && A.flags && at.row >= 0) atomicOr(&A.flags[at.row], (uint32_t)SPEC_F_NAN);
+    if (at.page < 0) continue;
+    const long long vec = (long long)P.head * A.C.page_size + at.slot;
+    unsigned char* const pool = (P.kv ? A.C.v : A.C.k) + at.page * A.C.page_bytes;
     float x[8];
     if (F32) {
       const uint4 a = raw[u][0], b = raw[u][F32 ? 1 : 0];
@@ -120,77 +127,58 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheI
       x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
       x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
     }
-    uint32_t amax = 0;   // as bits: NaN above infinity above every number
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = LPV / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (!live) continue;
-    const TokenPlace at = places[t.token - t0];
-    if (t.lane == 0 && amax >= 0x7f800000u && A.flags && at.row >= 0) atomicOr(&A.flags[at.row], (uint32_t)SPEC_F_NAN);
-    if (at.page < 0) continue;
-    const long long vec = (long long)t.head * A.C.page_size + at.slot;
-    unsigned char* pool = t.kv ? A.C.v : A.C.k;
     if (!E4M3) {
       uint4 w = raw[u][0];
       if (F32)
         w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-      *reinterpret_cast<uint4*>(pool + at.page * A.C.page_bytes + (vec * LPV + t.lane) * 16) = w;
+      *reinterpret_cast<uint4*>(pool + (vec * LPV + P.lane) * 16) = w;
     } else {
       // amax = 1.f * 2^E; 448 = 1.75 * 2^8
-      int s = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u);
-      s = max(s, -126);
+      const int s = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u), -126);
       const bool bad = amax >= 0x7f800000u;
-      const float inv = bad ? 0.f : __uint_as_float((uint32_t)(127 - s) << 23);
-      uint32_t lo, hi;
+      const float inv = __uint_as_float((uint32_t)(127 - s) << 23);
       uint16_t h[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = bad ? 0.f : x[2 * e] * inv, b = bad ? 0.f : x[2 * e + 1] * inv;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[e]) : "f"(b), "f"(a));
-      }
-      lo = (uint32_t)h[0] | (uint32_t)h[1] << 16;
-      hi = (uint32_t)h[2] | (uint32_t)h[3] << 16;
-      *reinterpret_cast<uint2*>(pool + at.page * A.C.page_bytes + (vec * LPV + t.lane) * 8) = make_uint2(lo, hi);
-      if (t.lane == 0) (t.kv ? A.C.v_exp : A.C.k_exp)[at.page * A.C.exp_bytes + vec] = (uint8_t)(bad ? 255 : s + 127);
+      for (int e = 0; e < 4; ++e)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[e]) : "f"(x[2 * e + 1] * inv), "f"(x[2 * e] * inv));
+      const uint2 codes = make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+      *reinterpret_cast<uint2*>(pool + (vec * LPV + P.lane) * 8) = bad ? make_uint2(0, 0) : codes;
+      if (P.lane == 0) (P.kv ? A.C.v_exp : A.C.k_exp)[at.page * A.C.exp_bytes + vec] = (uint8_t)(bad ? 255 : s + 127);
     }
   }
 }
 
 template <bool E4M3, int LPV, int U>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheIO A) {
-  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV) + 2];
-  int t0;
-  run_places<LPV, U>(A, places, &t0);
+  __shared__ TokenPlace places[kCacheThreads * U / (2 * LPV)];
+  const Place P = thread_place<LPV, U>(A, places);
   __syncthreads();
-  const long long first = (long long)blockIdx.x * (kCacheThreads * U) + threadIdx.x;
+  const int turn = P.token - blockIdx.x * U * A.at_once;
   uint4 raw[U];
   uint32_t e[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long i = first + u * kCacheThreads;
     raw[u] = make_uint4(0, 0, 0, 0);
     e[u] = 127;
-    if (i >= A.items) continue;
-    const Item t = item_of<LPV>(A, i);
-    const TokenPlace at = places[t.token - t0];
+    if (!P.live || P.token + u * A.at_once >= A.N) continue;
+    const TokenPlace at = places[turn + u * A.at_once];
     if (at.page < 0) continue;
-    const long long vec = (long long)t.head * A.C.page_size + at.slot;
-    const unsigned char* p = (t.kv ? A.C.v : A.C.k) + at.page * A.C.page_bytes;
+    const long long vec = (long long)P.head * A.C.page_size + at.slot;
+    const unsigned char* p = (P.kv ? A.C.v : A.C.k) + at.page * A.C.page_bytes;
     if (E4M3) {
-      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p + (vec * LPV + t.lane) * 8));
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p + (vec * LPV + P.lane) * 8));
       raw[u].x = w.x;
       raw[u].y = w.y;
-      e[u] = __ldg((t.kv ? A.C.v_exp : A.C.k_exp) + at.page * A.C.exp_bytes + vec);
+      e[u] = __ldg((P.kv ? A.C.v_exp : A.C.k_exp) + at.page * A.C.exp_bytes + vec);
     } else {
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(p + (vec * LPV + t.lane) * 16));
+      raw[u] = __ldcs(reinterpret_cast<const uint4*>(p + (vec * LPV + P.lane) * 16));
     }
   }
+  unsigned char* const to = A.kv[P.kv] + P.token * A.token_bytes + ((long long)P.head * LPV + P.lane) * 16;
+  const long long step = A.at_once * A.token_bytes;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long i = first + u * kCacheThreads;
-    if (i >= A.items) continue;
-    const Item t = item_of<LPV>(A, i);
+    if (!P.live || P.token + u * A.at_once >= A.N) continue;
     uint4 w = raw[u];
     if (E4M3) {
       const float s = exp_value(e[u]);
@@ -198,17 +186,13 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheIO
       w = make_uint4(pack_bf16(a.x * s, a.y * s), pack_bf16(a.z * s, a.w * s), pack_bf16(b.x * s, b.y * s),
                      pack_bf16(b.z * s, b.w * s));
     }
-    __stcs(reinterpret_cast<uint4*>(A.kv[t.kv] + t.token * A.token_bytes + ((long long)t.head * LPV + t.lane) * 16), w);
+    __stcs(reinterpret_cast<uint4*>(to + u * step), w);
   }
 }
 
-// Items a thread: four keep four independent loads in flight; one where four
-// would leave SMs without a CTA (fewer than two CTAs each).
-static bool many_items(long long items) { return items >= 2LL * 152 * kCacheThreads * 4; }
-
 template <int LPV, int U>
 static void launch_write(const CacheIO& A, bool f32, bool e4m3, cudaStream_t st) {
-  const unsigned grid = (unsigned)((A.items + kCacheThreads * U - 1) / (kCacheThreads * U));
+  const dim3 grid((A.N + U * A.at_once - 1) / (U * A.at_once), (A.lanes + kCacheThreads - 1) / kCacheThreads);
   if (f32) {
     if (e4m3) cache_write_kernel<true, true, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
     else cache_write_kernel<true, false, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
@@ -220,7 +204,7 @@ static void launch_write(const CacheIO& A, bool f32, bool e4m3, cudaStream_t st)
 
 template <int LPV, int U>
 static void launch_read(const CacheIO& A, bool e4m3, cudaStream_t st) {
-  const unsigned grid = (unsigned)((A.items + kCacheThreads * U - 1) / (kCacheThreads * U));
+  const dim3 grid((A.N + U * A.at_once - 1) / (U * A.at_once), (A.lanes + kCacheThreads - 1) / kCacheThreads);
   if (e4m3) cache_read_kernel<true, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
   else cache_read_kernel<false, LPV, U><<<grid, kCacheThreads, 0, st>>>(A);
 }
@@ -241,8 +225,9 @@ static int cache_launch(bool write, void* k, void* v, int dtype, long long token
   if (!paged_aligned(k, 16) || !paged_aligned(v, 16) || A.token_bytes % 16 || (flags && !paged_aligned(flags, 4)))
     return SPEC_E_ALIGN;
   const int lpv = A.C.D / 8;
-  A.items = (long long)N * 2 * A.C.heads * lpv;
-  if (A.items / lpv > 0x7fffffffLL) return SPEC_E_DIM;
+  A.lanes = 2 * A.C.heads * lpv;
+  A.across = A.lanes < kCacheThreads ? A.lanes : kCacheThreads;
+  A.at_once = kCacheThreads / A.across;
   const int arc = check_arch();
   if (arc != SPEC_OK) return arc;
   A.kv[0] = static_cast<unsigned char*>(k);
@@ -250,7 +235,9 @@ static int cache_launch(bool write, void* k, void* v, int dtype, long long token
   A.N = N;
   A.flags = flags;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-  const bool e4m3 = cache->dtype == SPEC_E4M3, f32 = dtype == SPEC_F32, many = many_items(A.items);
+  const bool e4m3 = cache->dtype == SPEC_E4M3, f32 = dtype == SPEC_F32;
+  // Four tokens a thread keep four loads in flight; one where four would leave SMs without two CTAs.
+  const bool many = (long long)N * A.lanes >= 2LL * 152 * kCacheThreads * 4;
   if (write) {
     if (lpv == 16) many ? launch_write<16, 4>(A, f32, e4m3, st) : launch_write<16, 1>(A, f32, e4m3, st);
     else many ? launch_write<8, 4>(A, f32, e4m3, st) : launch_write<8, 1>(A, f32, e4m3, st);
