@@ -565,6 +565,8 @@ def _token_stride(t, name):
     token, head, one = t.stride()
     if (d > 1 and one != 1) or (h > 1 and head != d):
         raise ValueError(f"{name} must be dense within a token")
+    if n > 1 and token < h * d:
+        raise ValueError(f"{name} has overlapping tokens")
     return token if n > 1 else h * d
 
 
