@@ -18,7 +18,11 @@
 // so the products are fp16: the queries are brought into its range by a power
 // of two for the tile, and the values' scales 2^e go into the exponent,
 //   t_j = log2(weight_j) + e_j,   p_j = 2^(t_j - max t),   sum += p_j 2^-e_j,
-// so that the weights of large terms keep all 11 bits whatever the scales.
+// so that the weights of large terms keep all 11 bits whatever the scales.  A
+// position whose scale lies far below another's (a value of zero has the smallest
+// of all) would lose its weight that way, p_j being no number any more: where a
+// tile has exponent bytes out of the ordinary range, its weights are summed by
+// 2^((t_j - e_j - max t) / 2) squared instead, which is in range for all scales.
 #include "spec_attend.cuh"
 
 namespace specv {
@@ -28,6 +32,7 @@ constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr float kRowsSlack = 8.f;
 constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
 constexpr unsigned kRowsTop = 221;   // so the largest exponent byte whose 2^-e is a normal number; above it is NaN
+constexpr unsigned kRowsLow = 64, kRowsHigh = 144;   // the ordinary range: within 2^80 a weight of 2^-46 stays a normal number
 
 template <int D, bool E4M3, int MT>
 struct RowsShape {
@@ -80,6 +85,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
   return v;
+}
+
+// x 2^y where 2^y may be out of range, x being far from 1.
+__device__ __forceinline__ float times_exp2(float x, float y) {
+  const float half = exp2_fast(0.5f * y);
+  return x * half * half;
 }
 
 // Two pairs of e4m3 codes as fp16.
@@ -137,7 +148,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   constexpr int M = S::M, KT = S::KT, NK = S::NK, NS = NK / 16;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) unsigned long long full[kRowsWarps][S::stages];
-  __shared__ unsigned there[kRowsWarps][S::stages][2];                   // bits: positions of the stage that are there; NaN values
+  // bits: positions of the stage that are there; whether values are NaN (1), scales above (2) or below (4) the ordinary
+  __shared__ unsigned there[kRowsWarps][S::stages][2];
   __shared__ __align__(8) float scales[kRowsWarps][S::stages][E4M3 ? 3 : 1][E4M3 ? NK : 1];   // keys' 2^e, values' e and 2^-e
   __shared__ AttendShare share;
   __shared__ long long sums[kRowsThreads];
@@ -169,7 +181,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   auto bring = [&](int stage) {
     if (!F.more) return;
     const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
-    const unsigned nans = E4M3 ? __ballot_sync(0xffffffffu, F.ve > kRowsTop) : 0;
+    unsigned found = 0;
+    if (E4M3) found = __reduce_or_sync(0xffffffffu, F.ve > kRowsTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
     unsigned char* const to = ring + stage * S::stage;
     const unsigned bytes = failed ? 0 : __popc(mask & starts & all) * (box * 2 * S::row_bytes);
     if (E4M3) {
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     }
     if (lane == 0) {
       there[warp][stage][0] = mask;
-      there[warp][stage][1] = nans;
+      there[warp][stage][1] = found;
       mbar_arrive_expect_tx(&full[warp][stage], bytes);
     }
     __syncwarp();
@@ -294,12 +307,19 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
       }
     }
 
+    bool high_scales = false;                             // among this warp's positions so far
     for (int t = W.a; t < W.b; ++t) {
       mbar_await(&full[warp][stage], phase, &failed);
       unsigned char* const k_sm = ring + stage * S::stage;
       const uint32_t ks_base = smem_u32(k_sm), vs_base = ks_base + S::kv_tile;
       const unsigned mask = there[warp][stage][0];
-      if (E4M3 && there[warp][stage][1]) odd = 1;
+      bool far_scales = false;
+      if (E4M3) {
+        const unsigned found = there[warp][stage][1];
+        if (found & 1) odd = 1;
+        high_scales = high_scales || (found & 2);
+        far_scales = high_scales || (found & 4);
+      }
       const int key0 = t * KT + warp * NK;                // this warp's first position
       const bool edge = key0 + NK > fewest || mask != all;
       if (edge) {
@@ -430,15 +450,30 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
           for (int h = 0; h < 2; ++h) {
             high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 1));
             high[h] = fmaxf(high[h], __shfl_xor_sync(0xffffffffu, high[h], 2));
-            const float to = fmaxf(m[i][h], high[h]);
-            const float keep = to == -INFINITY ? 1.f : exp2_fast(m[i][h] - to);
+            const float was = m[i][h], to = fmaxf(was, high[h]);
+            const float keep = to == -INFINITY ? 1.f : exp2_fast(was - to);
             m[i][h] = to;
-            l[i][h] *= keep;
+            l[i][h] = E4M3 ? times_exp2(l[i][h], to == -INFINITY ? 0.f : was - to) : l[i][h] * keep;
 #pragma unroll
             for (int d = 0; d < D / 8; ++d) o[i][d][2 * h] *= keep, o[i][d][2 * h + 1] *= keep;
           }
         }
         const float from[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
+        if (E4M3 && __builtin_expect(far_scales, 0)) {
+#pragma unroll
+          for (int z = 0; z < NS; ++z)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float2 e = *reinterpret_cast<const float2*>(&scales[warp][stage][E4M3 ? 1 : 0][E4M3 ? 16 * z + 8 * n + 2 * q4 : 0]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float a = exp2_fast(0.5f * (s[z][i][n][2 * h] - e.x - from[h]) - kRowsShift / 2);
+                const float b = exp2_fast(0.5f * (s[z][i][n][2 * h + 1] - e.y - from[h]) - kRowsShift / 2);
+                l[i][h] = fmaf(b, b, fmaf(a, a, l[i][h]));
+              }
+              if (i == 0) inv[z][n][0] = inv[z][n][1] = 0.f;
+            }
+        }
 #pragma unroll
         for (int z = 0; z < NS; ++z)
 #pragma unroll
@@ -596,7 +631,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][threadIdx.x]);
 #pragma unroll
         for (int w = 0; w < kRowsWarps; ++w)
-          sum += sm_l[w][threadIdx.x] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][threadIdx.x] - top));
+          sum += times_exp2(sm_l[w][threadIdx.x], top == -INFINITY ? 0.f : sm_m[w][threadIdx.x] - top);
         __stcg(part + M * D + threadIdx.x, top);
         __stcg(part + M * D + M + threadIdx.x, sum);
       }
@@ -620,7 +655,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
 #pragma unroll
           for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
 #pragma unroll
-          for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w][row] * (top == -INFINITY ? 1.f : exp2_fast(sm_m[w][row] - top));
+          for (int w = 0; w < kRowsWarps; ++w) sum += times_exp2(sm_l[w][row], top == -INFINITY ? 0.f : sm_m[w][row] - top);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = o_sm[row * S::pitch + d + e];
         } else {
@@ -631,8 +666,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
             const float4 b = __ldcg(reinterpret_cast<const float4*>(part + row * D + d + 4));
             const float to = fmaxf(top, pm);
             const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(pm - to);
+            if (to != -INFINITY) sum = times_exp2(sum, top - to) + times_exp2(pl, pm - to);
             top = to;
-            sum = sum * keep + pl * add;
             const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = x[e] * keep + y[e] * add;
