@@ -84,10 +84,10 @@ __device__ __forceinline__ int attend_qtiles(const AttendArgs& A, const AttendRo
 
 // The tiles of one head of a row.
 template <int M, int KT>
-__device__ __forceinline__ int attend_head_tiles(const AttendArgs& A, int r) {
+__device__ __forceinline__ long long attend_head_tiles(const AttendArgs& A, int r) {
   const AttendRow R = attend_row(A, r);
   const int qts = attend_qtiles<M>(A, R);
-  int sum = 0;
+  long long sum = 0;
 #pragma unroll 4
   for (int q = 0; q < qts; ++q) sum += attend_tiles<M, KT>(A, R, q);
   return sum;
@@ -108,7 +108,7 @@ template <int M, int KT, int THREADS>
 __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
   const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += (long long)attend_head_tiles<M, KT>(A, r) * A.C.heads;
+  for (int r = r0; r < r1; ++r) mine += attend_head_tiles<M, KT>(A, r) * A.C.heads;
   sums[t] = mine;
   __syncthreads();
   const int used = min(A.C.B, THREADS);
@@ -137,7 +137,7 @@ __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* o
   if (total && begin >= before && begin < before + mine) {
     int at = (int)before;
     for (int r = r0; r < r1; ++r) {
-      const int w = attend_head_tiles<M, KT>(A, r) * A.C.heads;
+      const int w = (int)attend_head_tiles<M, KT>(A, r) * A.C.heads;
       if (begin < at + w) {
         out->row = r;
         out->offset = begin - at;
@@ -164,7 +164,7 @@ struct AttendWalk {
     if (at >= end) return;
     R = attend_row(A, row);
     int off = S.offset;
-    const int per_head = attend_head_tiles<M, KT>(A, row);
+    const int per_head = (int)attend_head_tiles<M, KT>(A, row);
     head = off / per_head;
     off -= head * per_head;
     for (;;) {

@@ -46,10 +46,6 @@ struct Channels {
   static constexpr int kBytes = VEC * (BF16 ? 2 : 4);
   uint32_t w[kBytes < 4 ? 1 : kBytes / 4];
 
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (uint32_t& x : w) x = 0;
-  }
   __device__ __forceinline__ void load(const unsigned char* p) {
     if (kBytes == 16) {
       const uint4 x = __ldcs(reinterpret_cast<const uint4*>(p));
@@ -62,11 +58,6 @@ struct Channels {
     } else {
       w[0] = __ldcs(reinterpret_cast<const uint16_t*>(p));
     }
-  }
-  // Forgets what was unpacked, so that it is unpacked again and not kept beside the words.
-  __device__ __forceinline__ void again() {
-#pragma unroll
-    for (uint32_t& x : w) asm volatile("" : "+r"(x));
   }
   __device__ __forceinline__ float get(int v) const {
     if (!BF16) return __uint_as_float(w[v]);
