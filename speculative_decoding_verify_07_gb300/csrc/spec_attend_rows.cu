@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   __shared__ __align__(8) float scales[kRowsWarps][S::stages][E4M3 ? 3 : 1][E4M3 ? NK : 1];   // keys' 2^e, values' e and 2^-e
   __shared__ AttendShare share;
   __shared__ long long sums[kRowsThreads];
-  __shared__ float sm_m[kRowsWarps][M], sm_l[kRowsWarps][M];
+  __shared__ float sm_m[kRowsWarps][M], sm_l[kRowsWarps][M], tops[kRowsThreads / M][M];
   __shared__ int sees[M];
   __shared__ long long q_at[M], out_at[M];        // where a query row is read and written
   __shared__ int failed, odd, last_part, first_nan;
@@ -645,32 +645,47 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
       }
       __syncthreads();
     }
+    // The parts' maxima first, then what they add up to: no part's loads wait for the part before.
+    constexpr int ways = kRowsThreads / M;
+    if (whole ? threadIdx.x < M : last_part) {
+      const int row = threadIdx.x % M;
+      float top = -INFINITY;
+      if (whole) {
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
+      } else {
+#pragma unroll 4
+        for (int c = c0 + threadIdx.x / M; c <= c1; c += ways)
+          top = fmaxf(top, __ldcg(A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats + M * D + row));
+      }
+      tops[threadIdx.x / M][row] = top;
+    }
+    __syncthreads();
     if (whole || last_part) {
       for (int i = threadIdx.x; i < rows * (D / 8); i += kRowsThreads) {
         const int row = i / (D / 8), d = i % (D / 8) * 8;
-        float x[8], top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        float x[8], top = tops[0][row], sum = 0.f;
         if (whole) {
-#pragma unroll
-          for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
 #pragma unroll
           for (int w = 0; w < kRowsWarps; ++w) sum += times_exp2(sm_l[w][row], top == -INFINITY ? 0.f : sm_m[w][row] - top);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = o_sm[row * S::pitch + d + e];
         } else {
+#pragma unroll
+          for (int w = 1; w < ways; ++w) top = fmaxf(top, tops[w][row]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
             const float* part = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats;
             const float pm = __ldcg(part + M * D + row), pl = __ldcg(part + M * D + M + row);
             const float4 a = __ldcg(reinterpret_cast<const float4*>(part + row * D + d));
             const float4 b = __ldcg(reinterpret_cast<const float4*>(part + row * D + d + 4));
-            const float to = fmaxf(top, pm);
-            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(pm - to);
-            if (to != -INFINITY) sum = times_exp2(sum, top - to) + times_exp2(pl, pm - to);
-            top = to;
+            const float far = top == -INFINITY ? 0.f : pm - top, add = exp2_fast(far);
+            sum += times_exp2(pl, far);
             const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * keep + y[e] * add;
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e], add, x[e]);
           }
         }
         const long long at = out_at[row];
