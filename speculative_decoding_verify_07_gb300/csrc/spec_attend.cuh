@@ -93,18 +93,27 @@ __device__ __forceinline__ long long attend_head_tiles(const AttendArgs& A, int 
   return sum;
 }
 
-// A CTA's share: tiles [begin, end) of all, the first of them at `offset` in row
-// `row`.  Each of `ctas` CTAs has `each` tiles, the first `more` one more.
+// A CTA's share: tiles [begin, end) of all, of which the first is tile `a` of the
+// item (row, head, qt).  Share c begins where an even division would have it begin,
+// bound(c), unless that lies inside an item of at most WHOLE tiles or within
+// `slack` tiles of the end of a longer one: then at the nearer end of the item,
+// since writing and joining the parts of an item takes as long as some tiles.  (A
+// share may be empty then.)  With WHOLE = 6 in the wide kernel, whose end of an
+// item is the longer one, 5x484 tokens over short contexts take 25 us and not 38,
+// ragged chunks 134 us and not 147; the few-rows kernel lost 2 % of its long
+// contexts by it and has WHOLE = 0.
 struct AttendShare {
-  int begin, end, offset, each, more, row, ctas;
+  int begin, end, row, head, qt, tiles, a;
+  int each, more, slack;             // every share has `each` tiles, the first `more` one more
 };
 
+// The last share whose bound is not behind a tile.
 __device__ __forceinline__ int share_of(const AttendShare& S, int tile) {
   const int high = S.more * (S.each + 1);
   return tile < high ? tile / (S.each + 1) : S.more + (tile - high) / S.each;
 }
 
-template <int M, int KT, int THREADS>
+template <int M, int KT, int THREADS, int WHOLE>
 __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
   const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
   long long mine = 0;
@@ -123,34 +132,63 @@ __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* o
   const int total = all > 0x7fffffff ? 0 : (int)all;
   if (all > 0x7fffffff && A.flags && t == 0 && blockIdx.x == 0) atomicOr(&A.flags[0], (uint32_t)SPEC_F_BAD_IDX);
   const int ctas = min((int)gridDim.x, total), cta = min((int)blockIdx.x, ctas);
-  const int tiles = ctas ? total / ctas : 0, more = total - tiles * ctas, begin = cta * tiles + min(cta, more);
+  const int tiles_each = ctas ? total / ctas : 0, more = total - tiles_each * ctas;
+  const int slack = min(WHOLE / 2, tiles_each / 32);      // (1/16 more work for a share that takes in both its ends)
+  const int begin = cta * tiles_each + min(cta, more), end = cta < ctas ? begin + tiles_each + (cta < more) : begin;
   if (t == 0) {
-    out->ctas = ctas;
-    out->each = tiles;
+    out->each = tiles_each;
     out->more = more;
+    out->slack = slack;
     out->begin = begin;
-    out->end = cta < ctas ? begin + tiles + (cta < more) : begin;
-    out->row = 0;
-    out->offset = 0;
+    out->end = end;
   }
   __syncthreads();
-  if (total && begin >= before && begin < before + mine) {
-    int at = (int)before;
-    for (int r = r0; r < r1; ++r) {
-      const int w = (int)attend_head_tiles<M, KT>(A, r) * A.C.heads;
-      if (begin < at + w) {
-        out->row = r;
-        out->offset = begin - at;
-        break;
-      }
-      at += w;
+#pragma unroll 1
+  for (int e = 0; e < (WHOLE ? 2 : 1); ++e) {
+    const int x = e ? end : begin;
+    if (begin == end || x < before || x >= before + mine) continue;
+    int a = x - (int)before, row = r0, per_head;
+    for (;; ++row) {
+      per_head = (int)attend_head_tiles<M, KT>(A, row);
+      if (a < per_head * A.C.heads) break;
+      a -= per_head * A.C.heads;
+    }
+    const AttendRow R = attend_row(A, row);
+    const int head = a / per_head;
+    a -= head * per_head;
+    int qt = 0, tiles;
+    for (;; ++qt) {
+      tiles = attend_tiles<M, KT>(A, R, qt);
+      if (a < tiles) break;
+      a -= tiles;
+    }
+    const int near = tiles <= WHOLE ? tiles : slack;
+    const int move = a <= tiles - a ? (a <= near ? -a : 0) : (tiles - a <= near ? tiles - a : 0);
+    if (e) {
+      out->end = x + move;
+    } else {
+      out->begin = x + move;
+      out->row = row;
+      out->head = head;
+      out->qt = qt;
+      out->tiles = tiles;
+      out->a = a + move;
     }
   }
   __syncthreads();
 }
 
-// Walks a CTA's share, one segment (a run of position tiles of one item) after another.
-template <int M, int KT>
+// The CTAs that have parts of an item that no CTA has whole: all from *c0 to *c1.
+__device__ __forceinline__ void share_parts(const AttendShare& S, int item, int tiles, int* c0, int* c1) {
+  *c0 = share_of(S, item + S.slack);
+  *c1 = share_of(S, item + tiles - S.slack - 1);
+}
+
+// Walks a CTA's share, one segment (a run of position tiles of one item) after
+// another.  COUNT: the first item's tiles are counted again and not read from the
+// share, which gives the wide kernel the better code (2x2048 tokens in 413 us and
+// not 421) and the other the worse (32x5, group 8: 227 us and not 214).
+template <int M, int KT, bool COUNT>
 struct AttendWalk {
   const AttendArgs& A;
   AttendRow R;
@@ -160,20 +198,10 @@ struct AttendWalk {
   int next_a;
 
   __device__ __forceinline__ AttendWalk(const AttendArgs& args, const AttendShare& S)
-      : A(args), row(S.row), head(0), qt(0), tiles(0), a(0), b(0), at(S.begin), end(S.end), next_a(0) {
+      : A(args), row(S.row), head(S.head), qt(S.qt), tiles(COUNT ? 0 : S.tiles), a(0), b(0), at(S.begin), end(S.end), next_a(S.a) {
     if (at >= end) return;
     R = attend_row(A, row);
-    int off = S.offset;
-    const int per_head = (int)attend_head_tiles<M, KT>(A, row);
-    head = off / per_head;
-    off -= head * per_head;
-    for (;;) {
-      tiles = attend_tiles<M, KT>(A, R, qt);
-      if (off < tiles) break;
-      off -= tiles;
-      ++qt;
-    }
-    next_a = off;
+    if (COUNT) tiles = attend_tiles<M, KT>(A, R, qt);
   }
   // The next segment; false at the end of the share.
   __device__ __forceinline__ bool next() {

@@ -108,7 +108,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // their copies begin.
 template <int M, int NK, bool E4M3>
 struct RowsFetch {
-  AttendWalk<M, NK * kRowsWarps> I;
+  AttendWalk<M, NK * kRowsWarps, false> I;
   int t, limit;          // the tile, and the positions that its item sees
   bool more;
   int page, slot;        // of position `lane` (NK of them)
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     for (int i = 0; i < kRowsWarps * S::stages; ++i) mbar_init(&full[0][0] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  attend_share<M, KT, kRowsThreads>(A, &share, sums);
+  attend_share<M, KT, kRowsThreads, 0>(A, &share, sums);
 
   RowsFetch<M, NK, E4M3> F(A, share);
   F.look(warp, lane);
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     if (!F.more) return;
     const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
     unsigned found = 0;
-    if (E4M3) found = __reduce_or_sync(0xffffffffu, F.ve > kRowsTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
+    if (E4M3 && __any_sync(0xffffffffu, F.page >= 0 && F.ve - kRowsLow > kRowsHigh - kRowsLow))
+      found = __reduce_or_sync(0xffffffffu, F.ve > kRowsTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
     unsigned char* const to = ring + stage * S::stage;
     const unsigned bytes = failed ? 0 : __popc(mask & starts & all) * (box * 2 * S::row_bytes);
     if (E4M3) {
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   int stage = 0;
   uint32_t phase = 0;
   const int q4 = lane % 4, r8 = lane / 4;
-  AttendWalk<M, KT> W(A, share);
+  AttendWalk<M, KT, false> W(A, share);
   while (W.next()) {
     const int rows = min(M, W.R.n * A.group - W.qt * M);  // query rows of this tile
     if (threadIdx.x == 0) odd = 0, q_top = 0, first_nan = 0x7fffffff;
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     }
     const bool whole = W.whole();
     const int item = W.item_begin();
-    const int c0 = whole ? 0 : share_of(share, item);
-    const int c1 = whole ? 0 : share_of(share, item + W.tiles - 1);
+    int c0 = 0, c1 = 0;
+    if (!whole) share_parts(share, item, W.tiles, &c0, &c1);
     if (!whole) {
       float* part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       for (int i = threadIdx.x; i < M * D / 4; i += kRowsThreads) {

@@ -27,6 +27,7 @@ namespace specv {
 constexpr int kWideKT = 128;
 constexpr int kNowhere = 0x7fffffff;
 constexpr float kWideSlack = 8.f;
+constexpr int kWideWhole = 6;       // items of so few tiles stay in one CTA
 
 template <int D, bool E4M3, bool SPLIT>
 struct WideShape {
@@ -201,11 +202,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tmem_before();
   }
-  attend_share<M, KT, kWideThreads>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
+  attend_share<M, KT, kWideThreads, kWideWhole>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
   fence_proxy_async();
   tmem_after();
   const uint32_t tmem = tmem_base;
-  AttendWalk<M, KT> W(A, share);
+  AttendWalk<M, KT, true> W(A, share);
 
   if (warp >= ready_warp && warp < mma_warp) {
     // --------------------------------------------- keys and values made ready
@@ -613,8 +614,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         f1 = exp2_wide(m1 - ref);
         l = stats[128 + row] * f0 + (two ? stats[384 + row] * f1 : 0.f);
       }
-      const int c0 = whole ? 0 : share_of(share, item);
-      const int c1 = whole ? 0 : share_of(share, item + item_tiles - 1);
+      int c0 = 0, c1 = 0;
+      if (!whole) share_parts(share, item, item_tiles, &c0, &c1);
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
