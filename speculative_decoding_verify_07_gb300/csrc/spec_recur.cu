@@ -274,24 +274,34 @@ __device__ __forceinline__ void store_pair(unsigned char* p, float2 x, bool both
   }
 }
 
-// Fills a warp's rows of a tile from memory of any alignment.
+// Fills a warp's rows of a tile from memory that TMA cannot read: by 4-byte copies
+// that need no registers on the way, or, where 16-bit rows do not begin at 4-byte
+// boundaries, element by element.  `p` is the first row's channel c0 of the tile,
+// `left` the channels from there to D.
 template <bool BF16>
-__device__ __forceinline__ void fill_rows(unsigned char* to, const unsigned char* p, long long tok_bytes, int rows, bool one, bool both) {
-  constexpr int es = BF16 ? 2 : 4;
+__device__ __forceinline__ void fill_rows(unsigned char* to, const unsigned char* p, long long tok_bytes, int rows, int left) {
+  constexpr int es = BF16 ? 2 : 4, row_bytes = kScanCh * es;
+  const int lane = threadIdx.x % 32;
+  if (!BF16 || (((uintptr_t)p | tok_bytes) & 3) == 0) {
 #pragma unroll 4
-  for (int i = 0; i < rows; ++i) {
-    unsigned char* s = to + i * kScanCh * es;
-    const unsigned char* g = p + i * tok_bytes;
-    if (BF16) {
-      uint16_t a = 0, b = 0;
-      if (one) a = __ldcs(reinterpret_cast<const uint16_t*>(g));
-      if (both) b = __ldcs(reinterpret_cast<const uint16_t*>(g) + 1);
-      *reinterpret_cast<uint32_t*>(s) = (uint32_t)a | (uint32_t)b << 16;
-    } else {
-      float2 x = make_float2(0.f, 0.f);
-      if (one) x.x = __ldcs(reinterpret_cast<const float*>(g));
-      if (both) x.y = __ldcs(reinterpret_cast<const float*>(g) + 1);
-      *reinterpret_cast<float2*>(s) = x;
+    for (int i = 0; i < rows; ++i)
+#pragma unroll
+      for (int w = 0; w < row_bytes / 128; ++w) {
+        const int c = (w * 32 + lane) * (4 / es);
+        const unsigned char* g = p + i * tok_bytes;
+        const int bytes = min(max(left - c, 0) * es, 4);          // (the rest of the word becomes zero)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to + i * row_bytes + w * 128 + lane * 4)),
+                     "l"(bytes ? g + c * es : g), "r"(bytes) : "memory");
+      }
+  } else {
+    const int c = 2 * lane;
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+      const uint16_t* g = reinterpret_cast<const uint16_t*>(p + i * tok_bytes) + c;
+      uint16_t x = 0, y = 0;
+      if (c < left) x = __ldcs(g);
+      if (c + 1 < left) y = __ldcs(g + 1);
+      *reinterpret_cast<uint32_t*>(to + i * row_bytes + lane * 4) = (uint32_t)x | (uint32_t)y << 16;
     }
   }
 }
@@ -372,13 +382,16 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
       }
     } else {
       const long long g_tok = A.g_tok * es, x_tok = (BWD ? (long long)A.D : A.x_tok) * es, h_tok = (long long)A.D * hs;
-      const int rows = max(0, min(S, len - t0));
-      fill_rows<BF16>(staged + (warp * S * kScanCh + 2 * lane) * es, A.g + (r * A.g_row + c) * es + t0 * g_tok, g_tok, rows, live, both);
-      fill_rows<BF16>(sm_x + (warp * S * kScanCh + 2 * lane) * es, A.x + (BWD ? base * es : (r * A.x_row + c) * es + t0 * x_tok), x_tok, rows, live, both);
+      const int rows = max(0, min(S, len - t0)), left = A.D - c0;
+      const long long first = base - 2 * lane;                   // of channel c0
+      fill_rows<BF16>(staged + warp * S * row_bytes, A.g + (r * A.g_row + c0) * es + t0 * g_tok, g_tok, rows, left);
+      fill_rows<BF16>(sm_x + warp * S * row_bytes, A.x + (BWD ? first * es : (r * A.x_row + c0) * es + t0 * x_tok), x_tok, rows, left);
       if (BWD) {
         const int skip = t0 == 0;      // (before the first token there is the state)
-        fill_rows<HBF16>(sm_h + ((warp * S + skip) * kScanCh + 2 * lane) * hs, A.hin + (base + (long long)(skip - 1) * A.D) * hs, h_tok, max(0, rows - skip), live, both);
+        fill_rows<HBF16>(sm_h + (warp * S + skip) * h_row, A.hin + (first + (long long)(skip - 1) * A.D) * hs, h_tok, max(0, rows - skip), left);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
     }
     const bool whole = t0 + S <= len;
     const uint32_t at_g = smem_u32(staged) + (warp * S * kScanCh + 2 * lane) * es, at_x = smem_u32(sm_x) + (warp * S * kScanCh + 2 * lane) * es;
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
 
 // ---------------------------------------------------------------- launches
 
-constexpr int kStepTokens = 32;     // up to here a thread walks its channels' tokens
+constexpr int kStepTokens = 12;     // up to here a thread walks its channels' tokens
 
 struct ScanShape {
   int warps, tiles;
