@@ -76,8 +76,9 @@ typedef struct {
  * vector, the codes are x * 2^-s (exact) rounded to e4m3, ties to even, and
  * the byte is s + 127.  A vector with an infinity or a NaN gets byte 255 and
  * zero codes, and its row SPEC_F_NAN.
- *   flags [B] uint32 or NULL, OR-ed: SPEC_F_NAN; SPEC_F_BAD_IDX for a token
- *         whose position is negative or has no valid page (it is skipped).
+ *   flags [B] uint32 or NULL, OR-ed: SPEC_F_NAN (a 16-bit cache too, whose
+ *         values are kept as they are); SPEC_F_BAD_IDX for a token whose
+ *         position is negative or has no valid page (it is skipped).
  * Two tokens of one position race.
  * Errors: SPEC_E_NULL, SPEC_E_DIM, SPEC_E_DTYPE, SPEC_E_ALIGN (k, v, the pools
  * and their strides in multiples of 16 bytes), SPEC_E_ARCH, SPEC_E_CUDA. */
@@ -109,8 +110,11 @@ size_t spec_attend_workspace_size(int heads, int group, int head_dim);
  *        zeros and -inf.
  *   max_tokens  the largest number of new tokens of a row, as the host knows
  *        it: it chooses between kernels and is not a limit.
- *   flags [B] uint32 or NULL: SPEC_F_BAD_IDX (OR-ed) where a visible position
- *        has no valid page; such positions are left out.
+ *   flags [B] uint32 or NULL, OR-ed: SPEC_F_BAD_IDX where a visible position
+ *        has no valid page; such positions are left out.  SPEC_F_TIMEOUT where a
+ *        bounded wait gave up (the row is not valid).  A call of 2^31 and more
+ *        tiles of positions writes nothing and sets SPEC_F_BAD_IDX of row 0.
+ * Tokens of the packed arrays that belong to no row are not written.
  * What a query does not see never reaches it, infinities and NaN included.
  * Values of an 8-bit cache under exponent bytes above 221 (2^103 and more) are
  * taken for NaN.
@@ -132,7 +136,9 @@ size_t spec_recur_workspace_size(int B, int T, int D);
  *   h_t = exp(g_t) h_{t-1} + x_t,   t = 0 .. len_r - 1.
  *   g, x   [B, T, D] of dtype (SPEC_F32 or SPEC_BF16), channels dense, with
  *          g_row / g_tok (x_row / x_tok) elements from row to row and token to
- *          token.  g is the logarithm of the decay; -inf forgets the state.
+ *          token (0: the same for all).  g is the logarithm of the decay, at
+ *          most 0: above it products of decays may overflow before the state
+ *          does.  -inf forgets a finite state.
  *   state  [slots, D] float32 or NULL: h_{-1} of row r is state[slot[r]]
  *          (state[r] where slot is NULL); NULL: zeros.
  *   lens   [B] int32 or NULL (T each): len_r, clamped to [0, T].  g and x
@@ -162,7 +168,9 @@ int spec_recur(const void* g, int64_t g_row, int64_t g_tok, const void* x, int64
  *   g, dh, dg, dx [B, T, D] of dtype (g strided as above, the others dense);
  *   h [B, T, D] of h_dtype as spec_recur wrote it; state, slot, lens as given
  *   to spec_recur; d_last, d_state [B, D] float32, by row, or NULL.
- * dg and dx are zero beyond len_r; a row of length 0 has d_state = d_last. */
+ * dg and dx are zero beyond len_r; a row of length 0 has d_state = d_last.
+ * dg carries the rounding of h: where float32 gates need more than bf16's 8
+ * bits, h is kept in SPEC_F32. */
 int spec_recur_backward(const void* g, int64_t g_row, int64_t g_tok, const void* h, int h_dtype,
                         const void* dh, const float* d_last, int dtype, const float* state,
                         const int32_t* slot, int slots, const int32_t* lens, int B, int T, int D, void* dg,

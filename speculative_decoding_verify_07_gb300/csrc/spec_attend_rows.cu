@@ -23,6 +23,12 @@
 // of all) would lose its weight that way, p_j being no number any more: where a
 // tile has exponent bytes out of the ordinary range, its weights are summed by
 // 2^((t_j - e_j - max t) / 2) squared instead, which is in range for all scales.
+//
+// Measured, 8 heads of 128, group 4, 64 rows of 3 tokens: over 8000 positions in
+// bf16 5700 GB/s (85 % of the copy bandwidth), over up to 12000 in e4m3 4400 GB/s
+// (66 %: issue slots and the warp-level products share the time with the loads);
+// one token over 333 positions 12 us, a chain of latencies (share, page table,
+// copy, products, join).
 #include "spec_attend.cuh"
 
 namespace specv {
@@ -717,6 +723,7 @@ static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
 
 template <int D, bool E4M3>
 static int launch_rows_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
+  // 16 rows where they suffice: 64x1 tokens of group 8 at 8000 103 us, with 32 rows 122; 64x3 189 and 222
   return rows <= 16 ? launch_rows<D, E4M3, 1>(A, maps, st) : launch_rows<D, E4M3, 2>(A, maps, st);
 }
 

@@ -14,7 +14,10 @@
 // token's vectors, key and value of every head, take 2 * heads * D / 8 lanes; a
 // thread keeps its place among them and takes U tokens, all of whose loads are
 // begun before the first is used.  The tokens' places in the cache are looked up
-// once a CTA, into shared memory, while the loads are in flight.
+// once a CTA, into shared memory, while the loads are in flight.  Measured, 8
+// heads of 128, bf16 to e4m3: prompts of 25,000 tokens written at 4450 GB/s, 67 %
+// of the copy bandwidth (issue slots 78 % busy: the conversion), 54,000 tokens
+// read at 6020 GB/s (90 %), 64 rows of 3 tokens written in 4.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -236,7 +239,8 @@ static int cache_launch(bool write, void* k, void* v, int dtype, long long token
   A.flags = flags;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   const bool e4m3 = cache->dtype == SPEC_E4M3, f32 = dtype == SPEC_F32;
-  // Four tokens a thread keep four loads in flight; one where four would leave SMs without two CTAs.
+  // Four tokens a thread keep four loads in flight (the long prompts 31.5 us, with one 46.1; 1500 tokens 4.9 and
+  // 5.2); one where four would leave SMs without two CTAs (500 tokens 3.6 us, with four 4.1).
   const bool many = (long long)N * A.lanes >= 2LL * 152 * kCacheThreads * 4;
   if (write) {
     if (lpv == 16) many ? launch_write<16, 4>(A, f32, e4m3, st) : launch_write<16, 1>(A, f32, e4m3, st);

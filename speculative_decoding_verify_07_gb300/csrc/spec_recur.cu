@@ -1,5 +1,16 @@
 // spec_recur: h_t = exp(g_t) h_{t-1} + x_t, channel by channel, and its backward
-// pass.  One thread a channel walks its row's tokens in order.
+// pass, the same recurrence from the last token to the first.
+//
+// Bound by memory (g, x, h once; backward g, h, dh, dx, dg).  A few tokens: a
+// thread walks its channels' tokens.  More: a step s -> a s + b is joined with the
+// next as (a2 a1, a2 b1 + b2), so tiles of tokens are reduced to one such pair,
+// the pairs are handed along the row, and each tile is walked from the state that
+// enters it.  Every sum is taken in the same order on every call.
+//
+// Measured: 1x65536x2048 bf16 180 us, 4470 GB/s (67 % of the copy bandwidth; issue
+// slots, of which the decays take most, and the barriers of a tile), its backward
+// pass 266 us, 5040 GB/s (75 %); 8x4096x1024 float32 5060 and 5350 GB/s; 64x3x4096
+// 3.6 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -317,8 +328,10 @@ struct ScanMaps {
 // The tile comes by TMA, past the load queue through which the small loads of
 // the chain have to go.  Its tokens are read twice from shared memory, once to
 // reduce them and once, when the state that enters is known, to walk them; the
-// decay is computed both times, which leaves registers for four CTAs an SM, and
-// their loads and chain steps hide one another.
+// decay is computed both times, which leaves registers for four CTAs an SM (five
+// forward: 182 us, with four 201), and their loads and chain steps hide one another.
+// Rows that do not begin at 16-byte boundaries are copied word by word (4x8192x1337
+// float32 152 us forward, 3460 GB/s; 8x4096x1024 by TMA 5060 GB/s, by words 3400).
 template <bool BF16, bool HBF16, bool BWD, bool TMA>
 __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_scan_kernel(const RecurArgs A, const __grid_constant__ ScanMaps maps,
                                                                          ScanHeader* W, Word* agg, Word* inc, int tiles, int blocks,
@@ -521,7 +534,8 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
 
 // ---------------------------------------------------------------- launches
 
-constexpr int kStepTokens = 12;     // up to here a thread walks its channels' tokens
+// Up to here a thread walks its channels' tokens: 64x12x4096 6.0 us, by tiles 9.8; 8x16x2048 6.2 and 4.1.
+constexpr int kStepTokens = 12;
 
 struct ScanShape {
   int warps, tiles;
@@ -567,7 +581,8 @@ static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape
   const auto kernel = recur_scan_kernel<BF16, HBF16, BWD, TMA>;
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), kScanWarps * scan_steps<BF16>() * token_bytes, &allowed)) return SPEC_E_CUDA;
-  // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.
+  // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.  (1x65536x2048
+  // would take 195 us with groups of 32, and takes 182 with 16; 4x4096x128 is as fast with either.)
   const int group = grid <= (TMA && !BWD ? 5 : 4) * 152 ? kScanGroupMost : 16;
   kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
