@@ -1,5 +1,5 @@
-// Attention of a few query rows (up to 32: tokens times the group) over a long
-// cache: verify and decode steps.
+// Attention of a few query rows (tokens times the group, in tiles of 16 or 32) over
+// a long cache: verify and decode steps.
 //
 // Bound by the cache's bytes: for M rows a position of one head costs
 // 4 * M * D operations for 4 D bytes (2 D in 8 bits), 16 to 64 a byte, which
