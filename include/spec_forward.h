@@ -167,7 +167,8 @@ int spec_recur(const void* g, int64_t g_row, int64_t g_tok, const void* x, int64
  *   dx_t = l_t,   dg_t = exp(g_t) l_t h_{t-1},   d_state = exp(g_0) l_0.
  *   g, dh, dg, dx [B, T, D] of dtype (g strided as above, the others dense);
  *   h [B, T, D] of h_dtype as spec_recur wrote it; state, slot, lens as given
- *   to spec_recur; d_last, d_state [B, D] float32, by row, or NULL.
+ *   to spec_recur; d_last, d_state [B, D] float32, by row, or NULL (d_state may
+ *   be d_last).
  * dg and dx are zero beyond len_r; a row of length 0 has d_state = d_last.
  * dg carries the rounding of h: where float32 gates need more than bf16's 8
  * bits, h is kept in SPEC_F32. */

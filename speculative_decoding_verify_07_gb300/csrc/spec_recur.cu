@@ -442,13 +442,21 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
       fa = make_float2(fa.x * wa.x, fa.y * wa.y);
     }
     const float2 ta = make_float2(fa.x * pa.x, fa.y * pa.y), tb = make_float2(fmaf(pa.x, fb.x, pb.x), fmaf(pa.y, fb.y, pb.y));
-    if (publishes && hands_on && !ends) {
-      put_word(agg + mine * 2, tagged(ta.x, tag));
-      put_word(agg + mine * 2 + 1, tagged(tb.x, tag));
-      put_word(agg + mine * 2 + 2, tagged(ta.y, tag));
-      put_word(agg + mine * 2 + 3, tagged(tb.y, tag));
+    // The state that enters the row is read by its first tile alone, which hands on what is behind it: `last` may be the
+    // same memory, and the tile that writes it has waited, through the tiles between, for words made of that read.
+    float2 s = make_float2(0.f, 0.f);
+    if (publishes && order == 0 && live) {
+      const float* p = BWD ? (A.d_last ? A.d_last + (long long)r * A.D : nullptr) : from >= 0 ? A.state + from : nullptr;
+      if (p) s = make_float2(p[c], both ? p[c + 1] : 0.f);
     }
-    // The state that enters is that behind the group before, through the tiles of this group that come first: each
+    if (publishes && hands_on && !ends) {
+      const bool start = order == 0;
+      put_word(agg + mine * 2, tagged(start ? 0.f : ta.x, tag));
+      put_word(agg + mine * 2 + 1, tagged(start ? fmaf(ta.x, s.x, tb.x) : tb.x, tag));
+      put_word(agg + mine * 2 + 2, tagged(start ? 0.f : ta.y, tag));
+      put_word(agg + mine * 2 + 3, tagged(start ? fmaf(ta.y, s.y, tb.y) : tb.y, tag));
+    }
+    // The state that enters the tile is that behind the group before, through the tiles of this group that come first: each
     // warp fetches some of these and joins them.  Always the same products in the same order.
     bool gave_up = false;
     if (ahead > 0) {
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
       __syncthreads();
     }
     if (publishes) {
-      float2 ca = make_float2(1.f, 1.f), cb = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+      float2 ca = make_float2(1.f, 1.f), cb = make_float2(0.f, 0.f);
       for (int w = warps - 1; w >= 0 && ahead > 0; --w) {
         const float2 wa = sm_pa[w][lane], wb = sm_pb[w][lane];
         cb = make_float2(fmaf(wa.x, cb.x, wb.x), fmaf(wa.y, cb.y, wb.y));
@@ -474,12 +482,10 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
       if (order != ahead) {
         float w[2];
         await_words<2>(inc + mine + back * (ahead + 1), tag, w, &gave_up);
-        s = make_float2(w[0], w[1]);
-      } else if (live) {
-        const float* p = BWD ? (A.d_last ? A.d_last + (long long)r * A.D : nullptr) : from >= 0 ? A.state + from : nullptr;
-        if (p) s = make_float2(p[c], both ? p[c + 1] : 0.f);
+        s = make_float2(fmaf(ca.x, w[0], cb.x), fmaf(ca.y, w[1], cb.y));
+      } else if (ahead > 0) {
+        s = cb;                                                  // the first tile's pair holds the state
       }
-      s = make_float2(fmaf(ca.x, s.x, cb.x), fmaf(ca.y, s.y, cb.y));
       if (hands_on && ends) {
         put_word(inc + mine, tagged(fmaf(ta.x, s.x, tb.x), tag));
         put_word(inc + mine + 1, tagged(fmaf(ta.y, s.y, tb.y), tag));
@@ -488,8 +494,9 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
     }
     if ((gave_up || failed) && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_TIMEOUT);
     __syncthreads();
-    float2 s = sm_in[lane], first = make_float2(0.f, 0.f);
-    s = make_float2(fmaf(fa.x, s.x, fb.x), fmaf(fa.y, s.y, fb.y));
+    const float2 in = sm_in[lane];
+    float2 first = make_float2(0.f, 0.f);
+    s = make_float2(fmaf(fa.x, in.x, fb.x), fmaf(fa.y, in.y, fb.y));
     if (BWD && t0 == 0 && from >= 0 && live) first = make_float2(A.state[from + c], both ? A.state[from + c + 1] : 0.f);
     auto walk = [&](int n, bool inside) {
       float2 out = both_of(0.f), dg = out;

@@ -1,0 +1,58 @@
+"""What spec_forward.h promises beside the values: states updated in place, flags, answers that no hint and no
+neighbour changes."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = [torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+def scan_inputs(B, T, D, dtype, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    # what a row begins with is still seen at its end: decays of 1 / T a token
+    g = (-torch.rand((B, T, D), device="cuda", generator=gen) / T).to(dtype)
+    x, dh = (torch.randn((B, T, D), device="cuda", generator=gen).to(dtype) for _ in range(2))
+    return g, x, dh, 100 * torch.randn((B + 3, D), device="cuda", generator=gen)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tiles", [2, 16, 17, 40])
+@pytest.mark.parametrize("B,D", [(3, 71), (4, 136), (6, 1024)])
+def test_recur_in_place_is_the_call_out_of_place(B, D, tiles, dtype):
+    """`last` over `state`: every tile of a long row sees the state that was there before the call."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    T = tiles * (128 if dtype == torch.bfloat16 else 64) - 3
+    g, x, _, state = scan_inputs(B, T, D, dtype, tiles + B)
+    slot = torch.randperm(B + 3, device="cuda")[:B].to(torch.int32)
+    ws = sv.new_recur_workspace(B, T, D, "cuda")
+    h, last = sv.spec_recur(g, x, state, slot, h_dtype=dtype, workspace=ws)
+    want = state.clone()
+    want[slot.long()] = last
+    got = torch.empty_like(h)
+    for _ in range(25):
+        cache = state.clone()
+        sv.spec_recur(g, x, cache, slot, h=got, last=cache, last_slot=slot, workspace=ws)
+        assert torch.equal(got, h) and torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tiles", [1, 2, 17, 40])
+def test_recur_backward_in_place_is_the_call_out_of_place(tiles, dtype):
+    """`d_state` over `d_last`."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, D, T = 5, 520, tiles * (128 if dtype == torch.bfloat16 else 64) - 3
+    g, x, dh, state = scan_inputs(B, T, D, dtype, tiles)
+    h, _ = sv.spec_recur(g, x, state[:B])
+    want = sv.spec_recur_backward(g, h, dh, state[:B], d_last=state[3:])
+    for _ in range(25):
+        both = state[3:].clone()
+        got = sv.spec_recur_backward(g, h, dh, state[:B], d_last=both, d_state=both)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
