@@ -68,7 +68,7 @@ def _row_cache(r, n, table, k_values, v_values):
     """The row's first n positions, dense: keys, values [n, heads, D], and which positions have a page."""
     pages, _, page_size, _ = k_values.shape
     i, slot = np.divmod(np.arange(n), page_size)
-    page = np.where(i < table.shape[1], table[r, np.minimum(i, table.shape[1] - 1)], -1)
+    page = np.append(table[r], -1)[np.minimum(i, table.shape[1])]
     there = (page >= 0) & (page < pages)
     page = np.where(there, page, 0)
     return k_values[page, :, slot], v_values[page, :, slot], there

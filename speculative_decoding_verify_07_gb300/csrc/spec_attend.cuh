@@ -117,7 +117,12 @@ template <int M, int KT, int THREADS, int WHOLE>
 __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
   const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += attend_head_tiles<M, KT>(A, r) * A.C.heads;
+  for (int r = r0; r < r1; ++r) {
+    mine += attend_head_tiles<M, KT>(A, r) * A.C.heads;
+    // (no tile is counted, and so nothing looked up, for positions beyond the page table: they have no page)
+    const AttendRow R = attend_row(A, r);
+    if (R.n > 0 && R.kv > A.C.max_pages * A.C.page_size && blockIdx.x == 0 && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_BAD_IDX);
+  }
   sums[t] = mine;
   __syncthreads();
   const int used = min(A.C.B, THREADS);

@@ -4,6 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import forward as of
+from tests.test_gpu_forward import Batch, check_attend
+
 pytestmark = pytest.mark.gpu
 
 DT = [torch.bfloat16, torch.float32]
@@ -56,3 +59,12 @@ def test_recur_backward_in_place_is_the_call_out_of_place(tiles, dtype):
         both = state[3:].clone()
         got = sv.spec_recur_backward(g, h, dh, state[:B], d_last=both, d_state=both)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [2, 150])          # either kernel
+@pytest.mark.parametrize("wide", [9, 4, 1, 0])     # pages of the table: row 0 ends in page 10, row 1 in page 3
+def test_attend_flags_a_cache_longer_than_its_page_table(wide, new, pool):
+    b = Batch([new, 1, 0], [11 * 16 - 3, 3 * 16 + 5, 160], page=16, pool=pool, seed=41)
+    b.table = np.ascontiguousarray(b.table[:, :wide])
+    check_attend(b, 4, expect_flags=np.array([of.F_BAD_IDX, of.F_BAD_IDX if wide < 4 else 0, 0], np.uint32))
