@@ -29,6 +29,9 @@ struct AttendArgs {
   float* parts;          // workspace: per CTA, two partial results
 };
 
+// 8-bit cache: values under a larger exponent byte are taken for NaN, by either kernel.
+constexpr unsigned kAttendTop = 221;
+
 // Workspace: a counter a CTA, then the partial results.
 constexpr int kAttendCtas = 512;       // no launch has more
 constexpr size_t kAttendCounters = kAttendCtas * sizeof(unsigned);

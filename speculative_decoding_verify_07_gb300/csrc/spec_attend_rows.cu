@@ -37,7 +37,7 @@ constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr float kRowsSlack = 8.f;
 constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
-constexpr unsigned kRowsTop = 221;   // so the largest exponent byte whose 2^-e is a normal number; above it is NaN
+static_assert(254 - (int)kAttendTop - kRowsShift >= 1, "so 2^-e of the largest scale is a normal number");
 constexpr unsigned kRowsLow = 64, kRowsHigh = 144;   // the ordinary range: within 2^80 a weight of 2^-46 stays a normal number
 
 template <int D, bool E4M3, int MT>
@@ -189,13 +189,13 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
     unsigned found = 0;
     if (E4M3 && __any_sync(0xffffffffu, F.page >= 0 && F.ve - kRowsLow > kRowsHigh - kRowsLow))
-      found = __reduce_or_sync(0xffffffffu, F.ve > kRowsTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
+      found = __reduce_or_sync(0xffffffffu, F.ve > kAttendTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
     unsigned char* const to = ring + stage * S::stage;
     const unsigned bytes = failed ? 0 : __popc(mask & starts & all) * (box * 2 * S::row_bytes);
     if (E4M3) {
       float* s = &scales[warp][stage][0][0] + lane;
       s[0] = exp_value(F.ke);
-      const int e = F.ve > kRowsTop ? 127 : max((int)F.ve, 1);
+      const int e = F.ve > kAttendTop ? 127 : max((int)F.ve, 1);
       s[NK * (E4M3 ? 1 : 0)] = (float)(e - 127);
       s[2 * NK * (E4M3 ? 1 : 0)] = __uint_as_float((uint32_t)(254 - e - kRowsShift) << 23);
     }
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         for (int k = W.a * KT + threadIdx.x; k < k1; k += kRowsThreads) {
           int slot;
           const int page = paged_lookup(A.C, W.row, k, &slot);
-          if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > kRowsTop) atomicMin(&first_nan, k);
+          if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > kAttendTop) atomicMin(&first_nan, k);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < M * D; i += kRowsThreads)

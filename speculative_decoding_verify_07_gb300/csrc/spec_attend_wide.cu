@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const bool over = max(ke, ve) > kWideExp;
           if (over) {
             // what does not fit is made up for below; a value of NaN is cleared here and put in at the item's end
-            if (ve > 254) atomicMin(&odd_at[segment & 15], t * KT + tid);
+            if (ve > kAttendTop) atomicMin(&odd_at[segment & 15], t * KT + tid);
             if (ke > kWideExp) bits[0] = ke < 255 ? (kWideExp + 120) << 7 : 0x7fc0u;
-            if (ve > kWideExp) bits[1] = ve < 255 ? (kWideExp + 120) << 7 : 0u;
+            if (ve > kWideExp) bits[1] = ve <= kAttendTop ? (kWideExp + 120) << 7 : 0u;
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v) scales[n & 1][v][E4M3 ? tid : 0] = bits[v] * 0x10001u;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                   const int page = pos < limit ? paged_lookup(A.C, W.row, pos, &slot) : -1;
                   uint32_t e = 0;
                   if (page >= 0) e = (v ? A.C.v_exp : A.C.k_exp)[page * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + slot)];
-                  if (e <= kWideExp || e > 254) continue;
+                  if (e <= kWideExp || e > (v ? kAttendTop : 254u)) continue;
                   const uint32_t more = ((e - kWideExp + 127) << 7) * 0x10001u;
                   for (int j = 0; j < 2; ++j) {
                     uint4* p = reinterpret_cast<uint4*>(tile + h * S::half_tile + (row0 + 32 * i) * 128 + (((part * 2 + j) ^ (row0 & 7)) << 4));

@@ -68,3 +68,17 @@ def test_attend_flags_a_cache_longer_than_its_page_table(wide, new, pool):
     b = Batch([new, 1, 0], [11 * 16 - 3, 3 * 16 + 5, 160], page=16, pool=pool, seed=41)
     b.table = np.ascontiguousarray(b.table[:, :wide])
     check_attend(b, 4, expect_flags=np.array([of.F_BAD_IDX, of.F_BAD_IDX if wide < 4 else 0, 0], np.uint32))
+
+
+@pytest.mark.parametrize("byte", [221, 222, 246, 254, 255])
+@pytest.mark.parametrize("new,most", [(3, 3), (3, 4096), (140, 140), (140, 1)])     # either kernel, either hint
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_takes_the_largest_scales_for_nan_in_either_kernel(dim, new, most, byte):
+    b = Batch([new, 1], [new + 70, 40], page=16, pool="e4m3", dim=dim, seed=42)
+    at = 70 + new // 2
+    page, slot = b.table[0, at // 16], at % 16
+    b.exps[1, page, :, slot] = byte
+    codes = b.v.view(torch.uint8)[page, :, slot].cpu().numpy()
+    b.values[1][page, :, slot] = of.cache_values(codes, np.full(b.heads, byte)) if byte <= 221 else np.nan
+    out, _ = check_attend(b, 4, max_tokens=most)
+    assert out[new // 2:new].isnan().all() == (byte > 221) and torch.isfinite(out[:new // 2]).all()
