@@ -589,8 +589,9 @@ static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), kScanWarps * scan_steps<BF16>() * token_bytes, &allowed)) return SPEC_E_CUDA;
   // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.  (1x65536x2048
-  // would take 195 us with groups of 32, and takes 182 with 16; 4x4096x128 is as fast with either.)
-  const int group = grid <= (TMA && !BWD ? 5 : 4) * 152 ? kScanGroupMost : 16;
+  // would take 195 us with groups of 32, and takes 182 with 16; 4x4096x128 is as fast with either.)  The groups decide
+  // the order of the products, so they go by the sizes alone, not by how the rows are aligned.
+  const int group = grid <= 4 * 152 ? kScanGroupMost : 16;
   kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }

@@ -82,3 +82,22 @@ def test_attend_takes_the_largest_scales_for_nan_in_either_kernel(dim, new, most
     b.values[1][page, :, slot] = of.cache_values(codes, np.full(b.heads, byte)) if byte <= 221 else np.nan
     out, _ = check_attend(b, 4, max_tokens=most)
     assert out[new // 2:new].isnan().all() == (byte > 221) and torch.isfinite(out[:new // 2]).all()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tiles", [38, 42, 50])      # 608, 672 and 800 in all: as many CTAs as run at once, and more
+def test_recur_alignment_changes_no_bits_of_long_rows(tiles, dtype):
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, D, T = 1, 1024, tiles * (128 if dtype == torch.bfloat16 else 64)
+    g, x, dh, state = scan_inputs(B, T, D, dtype, tiles)
+
+    def shifted(t):          # begins between 16-byte boundaries
+        odd = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        odd[1:] = t.flatten()
+        return odd[1:].view(t.shape)
+
+    h, last = sv.spec_recur(g, x, state[:1])
+    h2, last2 = sv.spec_recur(shifted(g), shifted(x), state[:1])
+    assert torch.equal(h2, h) and torch.equal(last2, last)
+    for a, b in zip(sv.spec_recur_backward(shifted(g), h, dh, state[:1]), sv.spec_recur_backward(g, h, dh, state[:1])):
+        assert torch.equal(a, b)
