@@ -484,7 +484,8 @@ def philox4x32_10(ctr: torch.Tensor, seed: int, stream=None) -> torch.Tensor:
 
 _POOL_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
 _IO_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The device's current stream without the Stream object around it, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _io_dtype(t, name):
