@@ -576,10 +576,18 @@ def _at(t):
 
 
 def _queue(stream, dev):
-    """The raw stream that a call goes to: the given one, or the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(dev.index) if dev.type == "cuda" else None
+    """The raw stream that a call goes to: the given one, or the device's current
+    one.  Kernels read what they are given, so tensors elsewhere are refused."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not on {dev}")
+    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _space(workspace, dev):
+    """(address, bytes) of a given workspace."""
+    if workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous uint8 on {dev}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def _empty(shape, dtype, dev, stream):
@@ -679,8 +687,7 @@ def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, 
         with _on(stream):
             workspace = new_attend_workspace(heads, hq // heads, dim, dev)
     rc = LIB.spec_attend(q.data_ptr(), stride, N, hq // heads, dim ** -0.5 if scale is None else scale, max_tokens, view,
-                         out.data_ptr(), lse.data_ptr(), _at(flags), workspace.data_ptr(), workspace.numel(),
-                         _queue(stream, dev))
+                         out.data_ptr(), lse.data_ptr(), _at(flags), *_space(workspace, dev), _queue(stream, dev))
     _done(rc, "spec_attend")
     return out, lse
 
@@ -750,7 +757,7 @@ def spec_recur(g, x, state=None, slot=None, lens=None, *, h=None, h_dtype=torch.
             workspace = new_recur_workspace(B, T, D, dev)
     rc = LIB.spec_recur(g.data_ptr(), g_row, g_tok, x.data_ptr(), x_row, x_tok, dt, _at(state), _at(slot), slots, _at(lens),
                         B, T, D, h.data_ptr(), _io_dtype(h, "h"), last.data_ptr(), _at(last_slot), last_slots, _at(flags),
-                        workspace.data_ptr(), workspace.numel(), _queue(stream, dev))
+                        *_space(workspace, dev), _queue(stream, dev))
     _done(rc, "spec_recur")
     return h, last
 
@@ -787,6 +794,6 @@ def spec_recur_backward(g, h, dh, state=None, slot=None, lens=None, d_last=None,
             workspace = new_recur_workspace(B, T, D, dev)
     rc = LIB.spec_recur_backward(g.data_ptr(), g_row, g_tok, h.data_ptr(), _io_dtype(h, "h"), dh.data_ptr(), _at(d_last), dt,
                                  _at(state), _at(slot), slots, _at(lens), B, T, D, dg.data_ptr(), dx.data_ptr(),
-                                 d_state.data_ptr(), _at(flags), workspace.data_ptr(), workspace.numel(), _queue(stream, dev))
+                                 d_state.data_ptr(), _at(flags), *_space(workspace, dev), _queue(stream, dev))
     _done(rc, "spec_recur_backward")
     return dg, dx, d_state

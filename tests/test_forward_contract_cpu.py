@@ -27,3 +27,28 @@ def test_the_binding_imports_under_a_torch_without_cuda(sv):
             "assert sv.row_block(7, 2, 1) == (4, 7) and sv.recur_workspace_size(1, 1, 1) > 0\n")
     run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert run.returncode == 0, run.stderr
+
+
+def calls(sv):
+    """Each call on well-formed arguments that lie on the host, with what else it is given."""
+    kv = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
+    cu, ln, table = torch.tensor([0, 1, 2], dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32)
+    q, new, g = torch.zeros((2, 8, 64), dtype=torch.bfloat16), torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.zeros((2, 3, 8))
+    cache = (cu, ln, table, kv, kv.clone())
+    return (lambda **kw: sv.spec_attend(q, *cache, max_tokens=1, **kw), lambda **kw: sv.spec_recur(g, g, **kw),
+            lambda **kw: sv.spec_recur_backward(g, g, g, **kw), lambda **kw: sv.spec_cache_write(new, new, *cache, **kw),
+            lambda **kw: sv.spec_cache_read(2, *cache, **kw))
+
+
+def test_tensors_on_the_host_are_refused(sv):
+    for call in calls(sv):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+
+
+@pytest.mark.parametrize("unfit", [lambda n: torch.zeros(n // 4, dtype=torch.int32), lambda n: torch.zeros(2 * n, dtype=torch.uint8)[::2],
+                                   lambda n: torch.zeros(1, dtype=torch.uint8).expand(n), lambda n: torch.zeros(n, dtype=torch.uint8, device="meta")])
+def test_unfit_workspaces_are_refused(sv, unfit):
+    for call in calls(sv)[:3]:
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=unfit(1 << 26))
