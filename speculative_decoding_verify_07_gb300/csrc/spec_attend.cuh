@@ -54,7 +54,7 @@ __device__ __forceinline__ AttendRow attend_row(const AttendArgs& A, int r) {
   AttendRow R;
   R.first = __ldg(A.C.cu + r);
   R.n = __ldg(A.C.cu + r + 1) - R.first;
-  R.kv = __ldg(A.C.kv_len + r);
+  R.kv = paged_kv_len(A.C, r);
   if (R.first < 0 || R.n < 0 || R.n > A.N - R.first) R.n = 0;
   return R;
 }

@@ -53,7 +53,7 @@ __device__ __forceinline__ TokenPlace find_place(const CacheIO& A, int token) {
   t.row = paged_row(A.C, token);
   if (t.row < 0) return t;
   const int end = __ldg(A.C.cu + t.row + 1);
-  const int pos = __ldg(A.C.kv_len + t.row) - (end - token);
+  const int pos = paged_kv_len(A.C, t.row) - (end - token);
   if (pos >= 0) t.page = paged_lookup(A.C, t.row, pos, &t.slot);
   if (t.page < 0 && A.flags) atomicOr(&A.flags[t.row], (uint32_t)SPEC_F_BAD_IDX);
   return t;

@@ -73,6 +73,10 @@ __device__ __forceinline__ int paged_index(const PagedCache& C, int pos) {
   return C.page_shift >= 0 ? pos >> C.page_shift : pos / C.page_size;
 }
 
+// What row r has cached.  A negative number places no token, as zero does, and
+// taking tokens from the lowest would pass 32 bits.
+__device__ __forceinline__ int paged_kv_len(const PagedCache& C, int r) { return max(__ldg(C.kv_len + r), 0); }
+
 // The page of position pos >= 0 of row r, or -1 where there is none.
 __device__ __forceinline__ int paged_lookup(const PagedCache& C, int r, int pos, int* slot) {
   const int i = paged_index(C, pos);

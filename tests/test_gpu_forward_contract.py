@@ -101,3 +101,18 @@ def test_recur_alignment_changes_no_bits_of_long_rows(tiles, dtype):
     assert torch.equal(h2, h) and torch.equal(last2, last)
     for a, b in zip(sv.spec_recur_backward(shifted(g), h, dh, state[:1]), sv.spec_recur_backward(g, h, dh, state[:1])):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kv_len", [0, -1, -2 ** 31, -2 ** 31 + 2])
+@pytest.mark.parametrize("new", [3, 150])
+def test_rows_of_negative_length_hold_nothing(new, kv_len):
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    b = Batch([new, 2], [new + 40, 30], page=16, seed=43)
+    b.kv_len[0] = kv_len
+    check_attend(b, 4, expect_flags=np.zeros(2, np.uint32))
+    before = b.k.clone()
+    flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = torch.ones((b.N, b.heads, b.dim), dtype=torch.bfloat16, device="cuda")
+    sv.spec_cache_write(x, x, *b.args(), flags=flags)
+    assert flags.tolist() == [of.F_BAD_IDX, 0]
+    assert (b.k != before).flatten(1).any(1).sum() == 1          # row 1's two tokens, positions 28 and 29
