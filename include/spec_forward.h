@@ -27,9 +27,10 @@ extern "C" {
  * codes under one exponent byte a (token, head). */
 #define SPEC_E4M3 2
 
-/* Limits of the paged cache. */
+/* Limits: of the paged cache, and of a row's positions or tokens. */
 #define SPEC_MAX_PAGE 4096
 #define SPEC_MAX_GROUP 64
+#define SPEC_MAX_LENGTH 0x7fffff00
 
 /* A batch's view of a paged cache (a host struct of device pointers).
  *
@@ -48,7 +49,8 @@ extern "C" {
  *   page_table [B, max_pages] int32.  Only the entries of positions below
  *     kv_len[r] are read; one outside [0, pages) sets SPEC_F_BAD_IDX.
  *   cu_tokens [B + 1] int32 not decreasing from 0 to at most N; kv_len [B].
- * head_dim is 64 or 128; page_size any number up to SPEC_MAX_PAGE. */
+ * head_dim is 64 or 128; page_size any number up to SPEC_MAX_PAGE, and
+ * max_pages * page_size at most SPEC_MAX_LENGTH. */
 typedef struct {
   void* k_pages;
   void* v_pages;

@@ -31,7 +31,8 @@ inline int paged_check(const spec_cache_t* c, int N, PagedCache* out) {
   if (N < 0 || c->B < 0 || c->max_pages < 0 || c->pages < 0 || c->heads < 1 || c->heads > 65535) return SPEC_E_DIM;
   if (c->page_size < 1 || c->page_size > SPEC_MAX_PAGE) return SPEC_E_DIM;
   if (c->head_dim != 64 && c->head_dim != 128) return SPEC_E_DIM;
-  if ((long long)c->max_pages * c->page_size > 0x7fffffffLL) return SPEC_E_DIM;
+  // (the ends of the tiles that positions are counted in are held in 32 bits too)
+  if ((long long)c->max_pages * c->page_size > SPEC_MAX_LENGTH) return SPEC_E_DIM;
   if (c->dtype != SPEC_BF16 && c->dtype != SPEC_E4M3) return SPEC_E_DTYPE;
   const bool e4m3 = c->dtype == SPEC_E4M3;
   const int es = e4m3 ? 1 : 2;

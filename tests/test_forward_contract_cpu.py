@@ -52,3 +52,17 @@ def test_unfit_workspaces_are_refused(sv, unfit):
     for call in calls(sv)[:3]:
         with pytest.raises(ValueError, match="workspace"):
             call(workspace=unfit(1 << 26))
+
+
+P, DIM, REACHED = 4096, -2, (-6, -7)      # a fake, aligned address: never dereferenced; without a GPU a valid call ends there
+MOST = 0x7FFFFF00
+
+
+@pytest.mark.parametrize("max_pages,page,ok", [(2 ** 31 - 1, 1, False), (MOST + 1, 1, False), (MOST, 1, True),
+                                               (2 ** 31 // 24, 24, False), (MOST // 24, 24, True)])
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would run")
+def test_positions_stay_within_32_bits(sv, max_pages, page, ok):
+    view = sv.CACHE_T.pack(P, P, 0, 0, P, P, P, 0, 0, 1, 1, max_pages, 5, 2, page, 64)
+    codes = (sv.LIB.spec_attend(P, 0, 1, 4, 0.1, 1, view, P, P, None, P, 1 << 40, None),
+             sv.LIB.spec_cache_write(P, P, 1, 0, 1, view, None, None), sv.LIB.spec_cache_read(P, P, 1, view, None, None))
+    assert all(c in REACHED if ok else c == DIM for c in codes), codes
