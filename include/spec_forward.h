@@ -136,6 +136,7 @@ size_t spec_recur_workspace_size(int B, int T, int D);
 
 /* spec_recur - gated linear recurrence, channel by channel:
  *   h_t = exp(g_t) h_{t-1} + x_t,   t = 0 .. len_r - 1.
+ * B is at most 65535, T SPEC_MAX_LENGTH, D 2^26.
  *   g, x   [B, T, D] of dtype (SPEC_F32 or SPEC_BF16), channels dense, with
  *          g_row / g_tok (x_row / x_tok) elements from row to row and token to
  *          token (0: the same for all).  g is the logarithm of the decay, at

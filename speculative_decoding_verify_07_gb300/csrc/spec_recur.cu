@@ -639,7 +639,7 @@ static int recur_launch(const RecurArgs& A, int dtype, int h_dtype, void* worksp
   return hb ? launch_recur<false, true, BWD>(A, workspace, st) : launch_recur<false, false, BWD>(A, workspace, st);
 }
 
-static bool recur_dims(int B, int T, int D) { return B >= 0 && B <= 65535 && T >= 0 && D >= 1 && D <= (1 << 26); }
+static bool recur_dims(int B, int T, int D) { return B >= 0 && B <= 65535 && T >= 0 && T <= SPEC_MAX_LENGTH && D >= 1 && D <= (1 << 26); }
 
 // The checks both passes share.
 static int recur_check(int dtype, int h_dtype, int B, int T, int D, int slots, int last_slots, const int32_t* slot,

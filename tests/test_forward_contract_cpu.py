@@ -66,3 +66,14 @@ def test_positions_stay_within_32_bits(sv, max_pages, page, ok):
     codes = (sv.LIB.spec_attend(P, 0, 1, 4, 0.1, 1, view, P, P, None, P, 1 << 40, None),
              sv.LIB.spec_cache_write(P, P, 1, 0, 1, view, None, None), sv.LIB.spec_cache_read(P, P, 1, view, None, None))
     assert all(c in REACHED if ok else c == DIM for c in codes), codes
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would run")
+@pytest.mark.parametrize("T,ok", [(2 ** 31 - 1, False), (MOST + 1, False), (MOST, True)])
+def test_a_rows_tokens_stay_within_32_bits(sv, T, ok):
+    size = sv.LIB.spec_recur_workspace_size(1, T, 1)
+    # three words of eight bytes for each of 64 channels of a tile of 64 tokens, behind a header of 256 bytes
+    assert size == (256 + 3 * 8 * 64 * (T // 64) if ok else 0)
+    codes = (sv.LIB.spec_recur(P, 0, 1, P, 0, 1, 1, None, None, 0, None, 1, T, 1, P, 1, None, None, 0, None, P, 1 << 50, None),
+             sv.LIB.spec_recur_backward(P, 0, 1, P, 1, P, None, 1, None, None, 0, None, 1, T, 1, P, P, None, None, P, 1 << 50, None))
+    assert all(c in REACHED if ok else c == DIM for c in codes), codes
