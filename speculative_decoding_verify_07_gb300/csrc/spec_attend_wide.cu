@@ -33,6 +33,7 @@ namespace specv {
 constexpr int kWideKT = 128;
 constexpr int kNowhere = 0x7fffffff;
 constexpr float kWideSlack = 8.f;
+constexpr int kWideLarge = 30;       // scores of 2^30 and more are taken for one of that size (see below)
 constexpr int kWideWhole = 6;       // items of so few tiles stay in one CTA
 
 template <int D, bool E4M3, bool SPLIT>
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         fence_proxy_async();
         mbar_arrive(&bar.q_full[SPLIT ? 0 : group]);
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, by = scale, from = 0.f;     // weights are 2^(by * product + from)
       const int began = done;
       for (int t = item_a + (SPLIT ? group : 0); t < item_b; t += SPLIT ? 2 : 1, ++done) {
         mbar_await(&bar.s_full[group], done & 1, &failed);
@@ -552,6 +553,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (top > m + kWideSlack) {
           keep = exp2_wide(m - top);
           m = top;
+          // The multiply-add of the weights leaves what m lost by rounding, 2^6 at 2^30 and soon more than an exponent.
+          // From there on a score that is smaller at all is smaller by 2^6: brought to that size by a power of two, the
+          // largest keep the weight and all others lose it, as they should.
+          const int over = max((int)(__float_as_uint(m) >> 23 & 255) - (127 + kWideLarge), 0);
+          const float cut = __uint_as_float((uint32_t)(127 - over) << 23);
+          by = scale * cut;
+          from = -m * cut;
         }
         if (__any_sync(0xffffffffu, keep != 1.f)) {
           l *= keep;
@@ -569,8 +577,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
         }
-        const float from = m == -INFINITY ? 0.f : -m;
-        const float2 scale2 = make_float2(scale, scale), from2 = make_float2(from, from);
+        const float2 scale2 = make_float2(by, by), from2 = make_float2(from, from);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

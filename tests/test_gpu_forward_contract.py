@@ -116,3 +116,15 @@ def test_rows_of_negative_length_hold_nothing(new, kv_len):
     sv.spec_cache_write(x, x, *b.args(), flags=flags)
     assert flags.tolist() == [of.F_BAD_IDX, 0]
     assert (b.k != before).flatten(1).any(1).sum() == 1          # row 1's two tokens, positions 28 and 29
+
+
+# tiles of 16 and 32 query rows in the few-rows kernel, and of 128
+@pytest.mark.parametrize("new,group,pool", [(3, 4, "bf16"), (1, 2, "bf16"), (9, 5, "bf16"), (40, 4, "bf16"), (40, 4, "e4m3")])
+@pytest.mark.parametrize("high,low", [(100, -100), (60, 0), (40, -20)])
+def test_attend_a_query_is_not_measured_by_its_neighbours(high, low, new, group, pool):
+    """Queries of one row and head group that are far apart in size, as an unused token's may be: each keeps its bits."""
+    b = Batch([new, 2], [new + 200, 130], page=16, pool=pool, dim=128, seed=44)
+    size = np.full((b.N, b.heads * group, 1), 2.0)
+    size[::2, ::group] = 2.0 ** high
+    size[::3, group - 1::group] = 2.0 ** low
+    check_attend(b, group, q_size=size)
