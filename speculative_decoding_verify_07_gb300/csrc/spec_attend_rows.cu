@@ -15,8 +15,8 @@
 // times a row instead of at every tile.
 //
 // 8-bit codes become fp16 in registers by the conversion instruction (exact),
-// so the products are fp16: the queries are brought into its range by a power
-// of two for the tile, and the values' scales 2^e go into the exponent,
+// so the products are fp16: each query is brought into its range by a power
+// of two of its own, and the values' scales 2^e go into the exponent,
 //   t_j = log2(weight_j) + e_j,   p_j = 2^(t_j - max t),   sum += p_j 2^-e_j,
 // so that the weights of large terms keep all 11 bits whatever the scales.  A
 // position whose scale lies far below another's (a value of zero has the smallest
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   __shared__ int sees[M];
   __shared__ long long q_at[M], out_at[M];        // where a query row is read and written
   __shared__ int failed, odd, last_part, first_nan;
-  __shared__ unsigned q_top;
+  // 8-bit cache: a query row's largest magnitude
+  __shared__ unsigned q_top[E4M3 ? M : 1];
   unsigned char* const base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   unsigned char* const q_sm = base + S::stages * kRowsWarps * S::stage;
   float* const o_sm = reinterpret_cast<float*>(q_sm + S::q_bytes);
@@ -239,8 +240,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   AttendWalk<M, KT, false> W(A, share);
   while (W.next()) {
     const int rows = min(M, W.R.n * A.group - W.qt * M);  // query rows of this tile
-    if (threadIdx.x == 0) odd = 0, q_top = 0, first_nan = 0x7fffffff;
+    if (threadIdx.x == 0) odd = 0, first_nan = 0x7fffffff;
     if (threadIdx.x < M) {
+      if (E4M3) q_top[threadIdx.x] = 0;
       const int g = min(W.qt * M + (int)threadIdx.x, W.R.n * A.group - 1), token = attend_token(A, g);
       const int head = W.head * A.group + g - token * A.group;
       sees[threadIdx.x] = attend_sees(A, W.R, token);
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     // Q as the matrix instruction's A fragments, 16 bytes a lane.
     constexpr int each = M * D / 8 / kRowsThreads;
     uint2 qw[each][2];
-    uint32_t top = 0;
+    uint32_t top[MT][2] = {};                             // (load u is of rows 16 i + r8 and those 8 on, with i = u / (D / 64))
 #pragma unroll
     for (int u = 0; u < each; ++u) {
       const int i = u * kRowsThreads + threadIdx.x;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t x = (e < 2 ? qw[u][h].x : qw[u][h].y) >> (e % 2 * 16) & 0x7fffu;
-              top = max(top, x < 0x7f80u ? x : 0u);
+              top[u / (D / 64)][h] = max(top[u / (D / 64)][h], x < 0x7f80u ? x : 0u);
             }
           } else {
             qw[u][h].x = *reinterpret_cast<const uint32_t*>(p + ks * 16 + 2 * q);
@@ -278,22 +280,37 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         }
       }
     }
-    float score_scale = A.scale_log2, q_scale = 1.f;
+    float q_scale[MT][2], by_row[MT][2];                  // (what turns a row's products into powers of two)
     if (E4M3) {
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) atomicMax(&q_top, top);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          top[i][h] = max(top[i][h], __shfl_xor_sync(0xffffffffu, top[i][h], 1));
+          top[i][h] = max(top[i][h], __shfl_xor_sync(0xffffffffu, top[i][h], 2));
+          if (q4 == 0) atomicMax(&q_top[E4M3 ? i * 16 + 8 * h + r8 : 0], top[i][h]);
+        }
       __syncthreads();
-      // the largest magnitude to 2^13 .. 2^14 (what is 2^-27 of it is still a normal number)
-      const int up = min(13 - ((int)(q_top >> 7) - 127), 126);
-      q_scale = __uint_as_float((uint32_t)(127 + up) << 23);
-      score_scale *= __uint_as_float((uint32_t)(127 - up) << 23);
+      // a row's largest magnitude to 2^13 .. 2^14 (what is 2^-27 of it is still a normal number), whatever the other rows'
+      auto up = [&](int row) { return min(13 - ((int)(q_top[E4M3 ? row : 0] >> 7) - 127), 126); };
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int to = up(i * 16 + 8 * h + r8);
+          q_scale[i][h] = __uint_as_float((uint32_t)(127 + to) << 23);
+          by_row[i][h] = A.scale_log2 * __uint_as_float((uint32_t)(127 - to) << 23);
+        }
     }
 #pragma unroll
     for (int u = 0; u < each; ++u) {
       uint32_t w[4] = {qw[u][0].x, qw[u][1].x, qw[u][0].y, qw[u][1].y};
       if (E4M3)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * q_scale, bf16_hi(w[e]) * q_scale);
+        for (int e = 0; e < 4; ++e) {
+          const float by = q_scale[u / (D / 64)][e & 1];
+          w[e] = pack_f16(bf16_lo(w[e]) * by, bf16_hi(w[e]) * by);
+        }
       *reinterpret_cast<uint4*>(q_sm + (u * kRowsThreads + threadIdx.x) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncthreads();
@@ -422,13 +439,12 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const int k = 16 * z + 8 * n + 2 * q4;
-          float by[2] = {score_scale, score_scale}, plus[2] = {0.f, 0.f};
+          float2 by, plus;
           if (E4M3) {
             const float* f = &scales[warp][stage][0][0] + k;
-            const float2 a = *reinterpret_cast<const float2*>(f), b = *reinterpret_cast<const float2*>(f + NK),
-                         c = *reinterpret_cast<const float2*>(f + 2 * NK);
-            by[0] *= a.x, by[1] *= a.y;
-            plus[0] = b.x, plus[1] = b.y;
+            const float2 c = *reinterpret_cast<const float2*>(f + 2 * NK);
+            by = *reinterpret_cast<const float2*>(f);
+            plus = *reinterpret_cast<const float2*>(f + NK);
             inv[z][n][0] = c.x, inv[z][n][1] = c.y;
           }
 #pragma unroll
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float& x = s[z][i][n][e];
-              x = E4M3 ? fmaf(x, by[e & 1], plus[e & 1]) : x * by[e & 1];
+              x = E4M3 ? fmaf(x, (e & 1 ? by.y : by.x) * by_row[i][e >> 1], e & 1 ? plus.y : plus.x) : x * A.scale_log2;
               if (edge && (key0 + k + (e & 1) >= lim[i][e >> 1] || !(mask >> (k + (e & 1)) & 1))) x = -INFINITY;
             }
         }

@@ -119,7 +119,8 @@ def test_rows_of_negative_length_hold_nothing(new, kv_len):
 
 
 # tiles of 16 and 32 query rows in the few-rows kernel, and of 128
-@pytest.mark.parametrize("new,group,pool", [(3, 4, "bf16"), (1, 2, "bf16"), (9, 5, "bf16"), (40, 4, "bf16"), (40, 4, "e4m3")])
+@pytest.mark.parametrize("new,group,pool", [(3, 4, "bf16"), (1, 2, "bf16"), (9, 5, "bf16"), (40, 4, "bf16"), (40, 4, "e4m3"),
+                                            (3, 4, "e4m3"), (1, 2, "e4m3"), (9, 5, "e4m3")])
 @pytest.mark.parametrize("high,low", [(100, -100), (60, 0), (40, -20)])
 def test_attend_a_query_is_not_measured_by_its_neighbours(high, low, new, group, pool):
     """Queries of one row and head group that are far apart in size, as an unused token's may be: each keeps its bits."""
