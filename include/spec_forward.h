@@ -114,7 +114,7 @@ size_t spec_attend_workspace_size(int heads, int group, int head_dim);
  *        it: it chooses between kernels and is not a limit.
  *   flags [B] uint32 or NULL, OR-ed: SPEC_F_BAD_IDX where a visible position
  *        has no valid page; such positions are left out.  SPEC_F_TIMEOUT where a
- *        bounded wait gave up (the row is not valid).  A call of 2^31 and more
+ *        wait passed its bound (the row is not to be relied on).  A call of 2^31 and more
  *        tiles of positions writes nothing and sets SPEC_F_BAD_IDX of row 0.
  * Tokens of the packed arrays that belong to no row are not written.
  * What a query does not see never reaches it, infinities and NaN included.
@@ -154,7 +154,7 @@ size_t spec_recur_workspace_size(int B, int T, int D);
  *          decode step in place.  last_slots: rows of `last`.
  *   flags  [B] or NULL: SPEC_F_BAD_IDX for a row whose slot or last_slot is out
  *          of range (h is zero, last is left alone); SPEC_F_TIMEOUT for a row
- *          where a bounded wait gave up (its h is not valid).
+ *          where a wait passed its bound (its h is not to be relied on).
  * The state is float32 throughout.
  * Errors: SPEC_E_NULL, SPEC_E_DIM, SPEC_E_DTYPE, SPEC_E_ALIGN,
  * SPEC_E_WORKSPACE, SPEC_E_ARCH, SPEC_E_CUDA. */

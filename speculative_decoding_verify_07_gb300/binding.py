@@ -55,12 +55,12 @@ class SpecError(RuntimeError):
         self.code = code
 
 
-def _load():
-    if not os.path.exists(_LIB_PATH):
+def _load(path=_LIB_PATH):
+    if not os.path.exists(path):
         raise ImportError(
-            f"{_LIB_PATH} is missing; build it with "
+            f"{path} is missing; build it with "
             "`python -m speculative_decoding_verify_07_gb300.build`")
-    lib = ctypes.CDLL(_LIB_PATH)
+    lib = ctypes.CDLL(path)
     vp, i32, u64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
     lib.spec_verify_workspace_size.argtypes = [i32, i32, i32]
     lib.spec_verify_workspace_size.restype = sz

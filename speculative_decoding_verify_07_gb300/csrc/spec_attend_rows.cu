@@ -187,12 +187,13 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   constexpr unsigned all = NK == 32 ? ~0u : 0xffffu;
   auto bring = [&](int stage) {
     if (!F.more) return;
+    const bool go = !mbar_given_up(&failed);       // (lanes may differ on it: they meet again whatever it is)
     const unsigned mask = __ballot_sync(0xffffffffu, F.page >= 0);
     unsigned found = 0;
     if (E4M3 && __any_sync(0xffffffffu, F.page >= 0 && F.ve - kRowsLow > kRowsHigh - kRowsLow))
       found = __reduce_or_sync(0xffffffffu, F.ve > kAttendTop ? 1u : F.ve > kRowsHigh ? 2u : F.page >= 0 && F.ve < kRowsLow ? 4u : 0u);
     unsigned char* const to = ring + stage * S::stage;
-    const unsigned bytes = failed ? 0 : __popc(mask & starts & all) * (box * 2 * S::row_bytes);
+    const unsigned bytes = __popc(mask & starts & all) * (box * 2 * S::row_bytes);
     if (E4M3) {
       float* s = &scales[warp][stage][0][0] + lane;
       s[0] = exp_value(F.ke);
@@ -214,14 +215,14 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     if (lane == 0) {
       there[warp][stage][0] = mask;
       there[warp][stage][1] = found;
-      mbar_arrive_expect_tx(&full[warp][stage], bytes);
+      if (go) mbar_arrive_expect_tx(&full[warp][stage], bytes);
     }
     __syncwarp();
     if (bytes) {
       for (int i0 = 0; i0 < copies_of; i0 += 32) {
         const int i = i0 + lane, part = i % (2 * S::halves), at = i / (2 * S::halves) * box;
         const int page = __shfl_sync(0xffffffffu, F.page, at % NK), slot = __shfl_sync(0xffffffffu, F.slot, at % NK);
-        if (i < copies_of && page >= 0) {
+        if (i < copies_of && page >= 0 && go) {
           const int half = part % S::halves;
           const bool v = part >= S::halves;
           tma_load_4d(smem_u32(to + (v ? S::kv_tile : 0) + half * S::half_tile + at * S::half_bytes), v ? &vmap : &kmap, half * 64,
@@ -724,6 +725,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     if (threadIdx.x == 0 && failed && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
     __syncthreads();
   }
+  mbar_settle(&failed);
 }
 
 template <int D, bool E4M3, int MT>

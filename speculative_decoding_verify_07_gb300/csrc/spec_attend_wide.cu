@@ -387,12 +387,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             copies += __popc(mask[j] & starts[j]);
           }
           if (t + 1 < W.b) look(t + 1);
-          const uint32_t bytes = failed ? 0 : copies * A.box * D * (E4M3 ? 1 : 2);
+          const uint32_t bytes = copies * A.box * D * (E4M3 ? 1 : 2);
           unsigned long long* full = v ? &bar.v_raw[st] : E4M3 ? &bar.k_raw[st] : &bar.k_full[st];
           mbar_await(v ? &bar.v_empty[st] : &bar.k_empty[st], (n / stages & 1) ^ 1, &failed);
           if (lane < 4) (v ? v_there : there)[n & 7][lane] = lane == 0 ? mask[0] : lane == 1 ? mask[1] : lane == 2 ? mask[2] : mask[3];
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          const bool go = !mbar_given_up(&failed);       // (lanes may differ on it: they meet again whatever it is)
+          if (lane == 0 && go) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
           const uint32_t to = smem_u32(sm + st * S::tile + (E4M3 ? (S::halves - 1) * S::half_tile : 0));
           for (int b0 = 0; b0 < boxes && bytes; b0 += 32) {
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const int pj = __shfl_sync(0xffffffffu, page[j], from), sj = __shfl_sync(0xffffffffu, slot[j], from);
               if (at / 32 == j) p = pj, s = sj;
             }
-            if (b0 + lane < boxes && p >= 0) {
+            if (b0 + lane < boxes && p >= 0 && go) {
               if (E4M3) {
                 tma_load_4d(to + at * pitch, map, 0, s, W.head, p, full);
               } else {
@@ -748,6 +749,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (SPLIT) wide_sync();      // both O have been read before either is written again
     }
   }
+  mbar_settle(&failed);
   tmem_before();
   __syncthreads();
   if (warp == mma_warp) {

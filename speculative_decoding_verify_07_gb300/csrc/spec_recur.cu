@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_
       if (both) A.last[to + c + 1] = s.y;
     }
   }
+  if (TMA) mbar_settle(&failed);
   if (tiles > 1 && threadIdx.x == 0 && atomicAdd(&W->done, 1u) == gridDim.x - 1) {
     W->ticket = 0;
     W->done = 0;

@@ -51,25 +51,51 @@ __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// One try that lets the thread sleep for up to a millisecond: threads that poll
+// How long a wait may take before its call is flagged, and how much longer before
+// it is given up.  (A variable of the build, so that a wait can be made to run out.)
+#ifndef SPEC_WAIT_NS
+#define SPEC_WAIT_NS 2000000000ull
+#endif
+constexpr unsigned long long kWaitNs = SPEC_WAIT_NS, kGiveUpNs = kWaitNs + 2000000000ull;
+constexpr int kLate = 1, kGivenUp = 2;
+
+// One try that lets the thread sleep for a while (none for 0 ns): threads that poll
 // take issue slots from those that they wait for.
-__device__ __forceinline__ bool mbar_sleep_wait(unsigned long long* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_sleep_wait(unsigned long long* bar, uint32_t parity, unsigned ns) {
   uint32_t ok;
+  if (ns == 0) {
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+  }
   asm volatile(
       "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(ns) : "memory");
   return ok != 0;
 }
 
-// Waits for the phase; sets *failed and returns when it does not come within
-// two seconds, or when another wait of this CTA has given up.
-__device__ __forceinline__ void mbar_await(unsigned long long* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_sleep_wait(bar, parity)) return;
+// Waits for the phase.  Where it does not come in time *failed becomes kLate and the
+// wait goes on, since what is on its way still lands here; where it does not come at
+// all, kGivenUp, from when on no wait of this CTA waits and nothing more is begun: a
+// barrier takes no arrival for the next phase before the last has ended.
+__device__ __forceinline__ void mbar_await(unsigned long long* bar, uint32_t parity, int* failed) {
+  constexpr unsigned nap = kWaitNs < 100000 ? (unsigned)kWaitNs : 100000;
+  if (mbar_sleep_wait(bar, parity, nap)) return;
   const unsigned long long began = global_ns();
-  while (!mbar_sleep_wait(bar, parity)) {
-    if (*failed) return;
-    if (global_ns() - began > 2000000000ull) *failed = 1;
+  while (!mbar_sleep_wait(bar, parity, nap)) {
+    if (*(volatile int*)failed == kGivenUp) return;
+    const unsigned long long waited = global_ns() - began;
+    if (waited >= kWaitNs) atomicMax(failed, waited >= kGiveUpNs ? kGivenUp : kLate);
   }
+}
+__device__ __forceinline__ bool mbar_given_up(const int* failed) { return *(const volatile int*)failed == kGivenUp; }
+
+// The end of a CTA that has given up: a second in which what is still on its way to
+// its memory lands there.
+__device__ __forceinline__ void mbar_settle(const int* failed) {
+  if (!mbar_given_up(failed)) return;
+  const unsigned long long began = global_ns();
+  for (int i = 0; i < 2000 && global_ns() - began < 1000000000ull; ++i) __nanosleep(1000000);
 }
 
 }  // namespace specv

@@ -129,3 +129,70 @@ def test_attend_a_query_is_not_measured_by_its_neighbours(high, low, new, group,
     size[::2, ::group] = 2.0 ** high
     size[::3, group - 1::group] = 2.0 ** low
     check_attend(b, group, q_size=size)
+
+
+@pytest.fixture(scope="module")
+def late(tmp_path_factory):
+    """The library with waits whose bound is zero, so that every wait which waits at all passes it."""
+    from speculative_decoding_verify_07_gb300 import binding, build
+    at = tmp_path_factory.mktemp("late")
+    return binding._load(build.build(defines=("SPEC_WAIT_NS=0",), lib=str(at / "lib" / "liblate.so"), objdir=str(at / "obj")))
+
+
+def flagged_late(flags):
+    assert not (flags & ~256).any()
+    return bool((flags & 256).any())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,new,total", [(40, 3, 8000), (2, 300, 3000), (1, 30, 60000)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_a_late_wait_is_flagged_and_ends_in_order(late, monkeypatch, dim, rows, new, total, pool):
+    """What passes its bound is reported; its copies are still waited for, and the workspace serves on."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    page, heads = 64, 4
+    pages = rows * -(-total // page)
+    pools = torch.randn((2, pages, heads, page, dim), device="cuda").to(torch.bfloat16)
+    exps = (None, None)
+    if pool == "e4m3":
+        pools = pools.float().to(torch.float8_e4m3fn)
+        exps = torch.full((2, pages, heads, page), 127, dtype=torch.uint8, device="cuda")
+    table = torch.randperm(pages, device="cuda").to(torch.int32).view(rows, -1)
+    args = (new * torch.arange(rows + 1, device="cuda", dtype=torch.int32), torch.full((rows,), total, dtype=torch.int32, device="cuda"),
+            table, *pools, *exps)
+    q = torch.randn((rows * new, 4 * heads, dim), device="cuda", dtype=torch.bfloat16)
+    ws = sv.new_attend_workspace(heads, 4, dim, "cuda")
+    call = dict(max_tokens=new, workspace=ws)
+    want = sv.spec_attend(q, *args, **call)
+    flags = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    with monkeypatch.context() as m:
+        m.setattr(sv, "LIB", late)
+        got = sv.spec_attend(q, *args, **call, flags=flags)
+    # (few rows of short vectors, or of 8 bits, take longer to compute than to copy)
+    assert flagged_late(flags) or (4 * new <= 64 and (dim == 64 or pool == "e4m3"))
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    flags.zero_()
+    again = sv.spec_attend(q, *args, **call, flags=flags)
+    assert not flags.any() and all(torch.equal(a, c) for a, c in zip(again, want))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T", [100, 3000])
+def test_recur_a_late_wait_is_flagged_and_ends_in_order(late, monkeypatch, T, dtype):
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, D = 3, 512
+    g, x, dh, state = scan_inputs(B, T, D, dtype, T)
+    ws, flags = sv.new_recur_workspace(B, T, D, "cuda"), torch.zeros((2, B), dtype=torch.int32, device="cuda")
+
+    def both(f=(None, None)):
+        h, last = sv.spec_recur(g, x, state[:B], workspace=ws, flags=f[0])
+        return [h, last, *sv.spec_recur_backward(g, h, dh, state[:B], workspace=ws, flags=f[1])]
+
+    want = both()
+    with monkeypatch.context() as m:
+        m.setattr(sv, "LIB", late)
+        got = both(flags)
+    assert flagged_late(flags[0]) and flagged_late(flags[1])
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    flags.zero_()
+    assert all(torch.equal(a, c) for a, c in zip(both(flags), want)) and not flags.any()
