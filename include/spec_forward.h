@@ -44,8 +44,9 @@ extern "C" {
  *     dense), so that layers or keys and values may be interleaved in a pool.
  *   k_exp, v_exp     [pages, heads, page_size] exponent bytes of an SPEC_E4M3
  *     cache (NULL for SPEC_BF16), exp_stride bytes from page to page (0:
- *     dense).  Code c under byte e stands for c * 2^(e - 127); byte 255 stands
- *     for a vector of NaN.  Codes 0x7f and 0xff are never written.
+ *     dense).  Code c under byte e stands for c * 2^(e - 127); byte 0, which is
+ *     never written, is read as 1, and byte 255 stands for a vector of NaN.
+ *     Codes 0x7f and 0xff are never written.
  *   page_table [B, max_pages] int32.  Only the entries of positions below
  *     kv_len[r] are read; one outside [0, pages) sets SPEC_F_BAD_IDX.
  *   cu_tokens [B + 1] int32 not decreasing from 0 to at most N; kv_len [B].

@@ -131,6 +131,22 @@ def test_attend_a_query_is_not_measured_by_its_neighbours(high, low, new, group,
     check_attend(b, group, q_size=size)
 
 
+@pytest.mark.parametrize("new,most", [(3, 3), (150, 150)])
+def test_exponent_byte_zero_is_read_as_one(new, most):
+    """By the read and by both attention kernels, for keys and values: the header's one case apart from c 2^(e - 127)."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    b = Batch([new], [new + 60], page=16, pool="e4m3", dim=64, seed=46)
+    q = (2.0 ** 120 * torch.randn((b.N, 8, 64), device="cuda")).to(torch.bfloat16)
+    got = []
+    for byte in (0, 1):
+        b.exps.fill_(byte)
+        got.append([*sv.spec_cache_read(b.N, *b.args()), *sv.spec_attend(q, *b.args(), max_tokens=most)])
+    assert all(torch.equal(a, c) for a, c in zip(*got)) and got[0][0].any() and got[0][2].any()
+    codes = b.k.view(torch.uint8).cpu().numpy()
+    _, _, _, page, slot = b.places()[0]
+    assert np.array_equal(got[0][0][0].double().cpu().numpy(), of.e4m3_value(codes[page, :, slot]) * 2.0 ** -126)
+
+
 @pytest.fixture(scope="module")
 def late(tmp_path_factory):
     """The library with waits whose bound is zero, so that every wait which waits at all passes it."""
