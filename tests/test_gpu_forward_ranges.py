@@ -75,9 +75,8 @@ def test_recur_errors_are_those_of_the_tokens_remembered(B, T, D, low, high, dty
 
 
 def test_recur_slow_decays_lean_to_no_side():
-    """1000 remembered tokens of one sign: an error of the decay that leans by 2.5e-8, as the fast power of two's does,
-    would show as 2.5e-5 in the mean; the series' own leaning there is 1e-10, and the roundings of 64 channels and 20
-    memories (2^-25 a token at random) leave 3e-8."""
+    """1000 remembered tokens of one sign: a decay that leans to one side by 1e-9 shows as 1e-6 in the mean.  The series
+    leans by 1e-10 there, and the roundings of 64 channels and 20 memories (2^-25 a token at random) leave 3e-8."""
     from speculative_decoding_verify_07_gb300 import binding as sv
     rng = np.random.default_rng(1)
     g = (-1e-3 * rng.uniform(0.8, 1.2, (1, 20000, 64))).astype(np.float32)
