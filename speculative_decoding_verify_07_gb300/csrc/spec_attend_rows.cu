@@ -55,7 +55,8 @@ struct RowsShape {
   static constexpr int pitch = D + 8;                            // floats a row of the joined values
   static constexpr int o_bytes = M * pitch * 4;
   static constexpr int ctas = 2;          // an SM
-  static constexpr int most = (225 * 1024 / ctas - 1024 - q_bytes - o_bytes - 6144) / (kRowsWarps * stage);
+  static constexpr int small = E4M3 ? 14336 : 6144;              // at least what the small arrays take, the scales among them
+  static constexpr int most = (225 * 1024 / ctas - 1024 - q_bytes - o_bytes - small) / (kRowsWarps * stage);
   static constexpr int stages = most > 6 ? 6 : most;
   static constexpr int smem = 1024 + stages * kRowsWarps * stage + q_bytes + o_bytes;
   static constexpr int part_floats = M * (D + 2);
