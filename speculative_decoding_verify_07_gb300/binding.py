@@ -664,7 +664,8 @@ def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, 
 
     q [N, heads * group, head_dim] bfloat16 (tokens may be strided); scale
     defaults to head_dim ** -0.5; max_tokens is the largest number of new
-    tokens of a row.  Returns (out [N, heads * group, head_dim] bfloat16,
+    tokens of a row.  Without a workspace the call makes one and zeroes it (40 MB
+    for heads of 128): a loop keeps one.  Returns (out [N, heads * group, head_dim] bfloat16,
     lse [N, heads * group] float32).
     """
     view, _, heads, head_dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)

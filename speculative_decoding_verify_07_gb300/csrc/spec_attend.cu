@@ -75,8 +75,11 @@ extern "C" int spec_attend(const uint16_t* q, int64_t token_stride, int N, int g
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
   const bool e4m3 = cache->dtype == SPEC_E4M3;
   // A tile of 16 or 32 query rows at a time, or of 128 or 256.  The few-rows kernel reads the cache again for every
-  // 32 rows, the other fills its tile with padding.  40 rows of 32x5 tokens at 8000: in 8 bits 211 us with few rows
-  // and 264 with many (which widens the codes first), in 16 bits 105 and 75.
+  // 32 rows, the other fills its tile with padding.  In 16 bits 32x5 tokens of group 8 (40 rows) at 8000 take 139 us with
+  // many rows, with few 231.  In 8 bits, where the other kernel widens the codes first, neither wins throughout from 33
+  // to 64 rows: few rows take 89 us and many 123 with one row of 9 tokens (group 4, one head) at 60000, 47.5 and 58 with
+  // 67 ragged ones over 800, 351 and 407 with 32x5 at 8000 in pages of one token; but 220 and 173 with these in pages
+  // of 16, and 305 and 206 with 64x8 at 4000.  Up to 32 rows few do (64x4 of group 8 239 us, 328).
   const long long rows = (long long)max_tokens * group;
   const bool wide = rows > (e4m3 ? 64 : 32);
   // the longest run of positions that never leaves a page, up to what is copied at a time

@@ -102,8 +102,8 @@ __device__ __forceinline__ long long attend_head_tiles(const AttendArgs& A, int 
 // `slack` tiles of the end of a longer one: then at the nearer end of the item,
 // since writing and joining the parts of an item takes as long as some tiles.  (A
 // share may be empty then.)  With WHOLE = 6 in the wide kernel, whose end of an
-// item is the longer one, 5x484 tokens over short contexts take 25 us and not 38,
-// ragged chunks 134 us and not 147; the few-rows kernel lost 2 % of its long
+// item is the longer one, 5x484 tokens over short contexts take 25.5 us and not 37,
+// ragged chunks 138 us and not 148; the few-rows kernel lost 2 % of its long
 // contexts by it and has WHOLE = 0.
 struct AttendShare {
   int begin, end, row, head, qt, tiles, a;
@@ -194,8 +194,8 @@ __device__ __forceinline__ void share_parts(const AttendShare& S, int item, int 
 
 // Walks a CTA's share, one segment (a run of position tiles of one item) after
 // another.  COUNT: the first item's tiles are counted again and not read from the
-// share, which gives the wide kernel the better code (2x2048 tokens in 413 us and
-// not 421) and the other the worse (32x5, group 8: 227 us and not 214).
+// share, which gives the wide kernel the better code (2x2048 tokens 2 % faster) and
+// the other the worse (32x5 tokens of group 8, 8 bits, 6 % slower).
 template <int M, int KT, bool COUNT>
 struct AttendWalk {
   const AttendArgs& A;

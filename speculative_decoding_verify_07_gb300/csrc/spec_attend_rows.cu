@@ -7,10 +7,10 @@
 // tcgen05 tile of 128 rows would spend its time on padding.
 //
 // The four warps of a CTA divide each tile of positions, 16 each (32 of an 8-bit
-// cache: as many bytes), and share nothing until an item ends: every warp brings its own positions by TMA (a box
-// a run of positions within a page) through a ring of its own, several tiles
-// ahead and across the ends of items, and keeps its own running maximum, sum
-// and weighted values in registers.  The maximum only moves when a score
+// cache: as many bytes), and share nothing until an item ends: every warp brings
+// its own positions by TMA (a box a run of positions within a page) through a ring
+// of its own, several tiles ahead and across the ends of items, and keeps its own
+// running maximum, sum and weighted values in registers.  The maximum only moves when a score
 // passes it by 2^8, which keeps weights below 2^8 and rescales the sums a few
 // times a row instead of at every tile.
 //
@@ -25,10 +25,11 @@
 // 2^((t_j - e_j - max t) / 2) squared instead, which is in range for all scales.
 //
 // Measured, 8 heads of 128, group 4, 64 rows of 3 tokens: over 8000 positions in
-// bf16 5700 GB/s (85 % of the copy bandwidth), over up to 12000 in e4m3 4400 GB/s
-// (66 %: issue slots and the warp-level products share the time with the loads);
-// one token over 333 positions 12 us, a chain of latencies (share, page table,
-// copy, products, join).
+// bf16 191 us, 5600 GB/s (84 % of the copy bandwidth), over up to 12000 in e4m3
+// 206 us, 4270 GB/s (64 %: issue slots are busy in 37 % of the cycles and the matrix
+// pipe in 22, with two warps a scheduler, each a chain of loads, conversions,
+// products and softmax, waiting for itself); one token over 333 positions 11.5 us,
+// a chain of latencies (share, page table, copy, products, join).
 #include "spec_attend.cuh"
 
 namespace specv {
@@ -742,7 +743,7 @@ static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
 
 template <int D, bool E4M3>
 static int launch_rows_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  // 16 rows where they suffice: 64x1 tokens of group 8 at 8000 103 us, with 32 rows 122; 64x3 189 and 222
+  // 16 rows where they suffice: 64x1 tokens of group 8 at 8000 105 us, with 32 rows 124; 64x3 of group 4 193 and 226
   return rows <= 16 ? launch_rows<D, E4M3, 1>(A, maps, st) : launch_rows<D, E4M3, 2>(A, maps, st);
 }
 

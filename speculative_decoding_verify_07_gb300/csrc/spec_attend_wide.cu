@@ -8,7 +8,7 @@
 // works for one while the other computes: on two tiles of 128 query rows, or,
 // where the item has no more than 128, on every other tile of positions of the
 // same rows, with two O that are joined at the end.  P is bf16 (the values are;
-// its rounding adds up to 2^-9 to a weight), everything else float32.
+// its rounding changes a weight by up to 2^-8), everything else float32.
 //
 // The maximum only moves when a row's scores pass it by 2^8, so O, which stays
 // in tensor memory, is rescaled a few times a row and not at every tile.
@@ -22,9 +22,10 @@
 // power-of-two scale (exact), so the rest of the kernel is the same.
 //
 // Measured: 2x2048 tokens at 9000 positions, 32 query heads of 128, bf16, 415 us,
-// 1310 TFLOP/s (70 % of cuBLAS's rate here): each group's chain from scores to
-// weights to products, two in flight, leaves the matrix unit idle for the rest.
-// 8 bits: 2x1024 at 8000 225 us, 940 TFLOP/s: widening both operands takes as long
+// 1310 TFLOP/s (70 % of cuBLAS's rate here; by calls back to back 427 us): the matrix
+// pipe is busy in 55 % of the cycles and issue slots in 39, and each group's chain
+// from scores to weights to products, two in flight, waits for itself.
+// 8 bits: 2x1024 at 8000 227 us, 930 TFLOP/s: widening both operands takes as long
 // as the softmax.  Heads of 64 have half the products for the same softmax.
 #include "spec_attend.cuh"
 
@@ -771,8 +772,8 @@ static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
 
 template <int D, bool E4M3>
 static int launch_wide_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  // One tile of query rows where it suffices: 16x5 tokens of group 8 over up to 30000 75.8 us, with two tiles 80.3; 32x5 of group 16,
-  // heads of 64, 66.0 and 72.8.  Above 128 rows two: 2x2048 tokens 415 us, with one tile 642; 16x17 of group 16 88 and 103.
+  // One tile of query rows where it suffices: 16x5 tokens of group 8 over up to 30000 76.8 us, with two tiles 79.7; 32x5 of group 16,
+  // heads of 64, 66.5 and 74.0.  Above 128 rows two: 2x2048 tokens 415 us, with one tile 670; 16x17 of group 16 88 and 108.
   return rows <= 128 ? launch_wide<D, E4M3, true>(A, maps, st) : launch_wide<D, E4M3, false>(A, maps, st);
 }
 

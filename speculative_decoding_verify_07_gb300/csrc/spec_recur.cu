@@ -7,10 +7,10 @@
 // the pairs are handed along the row, and each tile is walked from the state that
 // enters it.  Every sum is taken in the same order on every call.
 //
-// Measured: 1x65536x2048 bf16 180 us, 4470 GB/s (67 % of the copy bandwidth; issue
-// slots, of which the decays take most, and the barriers of a tile), its backward
-// pass 266 us, 5040 GB/s (75 %); 8x4096x1024 float32 5060 and 5350 GB/s; 64x3x4096
-// 3.6 us.
+// Measured: 1x65536x2048 bf16 184 us, 4380 GB/s (65 % of the copy bandwidth; issue
+// slots are busy in 65 % of the cycles, the barriers of a tile and the chain along
+// the row take the rest), its backward pass 267 us, 5030 GB/s (75 %); 8x4096x1024
+// float32 5030 and 5350 GB/s; 64x3x4096 3.6 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -329,9 +329,9 @@ struct ScanMaps {
 // the chain have to go.  Its tokens are read twice from shared memory, once to
 // reduce them and once, when the state that enters is known, to walk them; the
 // decay is computed both times, which leaves registers for four CTAs an SM (five
-// forward: 182 us, with four 201), and their loads and chain steps hide one another.
+// forward: with four 10 % slower), and their loads and chain steps hide one another.
 // Rows that do not begin at 16-byte boundaries are copied word by word (4x8192x1337
-// float32 152 us forward, 3460 GB/s; 8x4096x1024 by TMA 5060 GB/s, by words 3400).
+// float32 149 us forward, 3530 GB/s; 8x4096x1024 by TMA 5030 GB/s, by words 3400).
 template <bool BF16, bool HBF16, bool BWD, bool TMA>
 __global__ void __launch_bounds__(kScanWarps * 32, (TMA && !BWD ? 5 : 4)) recur_scan_kernel(const RecurArgs A, const __grid_constant__ ScanMaps maps,
                                                                          ScanHeader* W, Word* agg, Word* inc, int tiles, int blocks,
@@ -590,7 +590,7 @@ static int launch_scan(const RecurArgs& A, const ScanMaps& maps, const ScanShape
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), kScanWarps * scan_steps<BF16>() * token_bytes, &allowed)) return SPEC_E_CUDA;
   // Every tile of a small call runs at once and a link of the chain is all it waits for: long groups.  (1x65536x2048
-  // would take 195 us with groups of 32, and takes 182 with 16; 4x4096x128 is as fast with either.)  The groups decide
+  // takes 7 % longer with groups of 32 than with 16; 4x4096x128 is as fast with either.)  The groups decide
   // the order of the products, so they go by the sizes alone, not by how the rows are aligned.
   const int group = grid <= 4 * 152 ? kScanGroupMost : 16;
   kernel<<<(unsigned)grid, S.warps * 32, smem, st>>>(A, maps, W, agg, inc, S.tiles, blocks, group);
