@@ -119,26 +119,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ float exp2_wide(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
 // Whether any thread of the four warps that make tiles ready says so; a barrier among them.
 __device__ __forceinline__ bool ready_any(bool mine) {
   uint32_t any;
@@ -553,7 +533,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         top *= scale;
         float keep = 1.f;
         if (top > m + kWideSlack) {
-          keep = exp2_wide(m - top);
+          keep = exp2_fast(m - top);
           m = top;
           // The multiply-add of the weights leaves what m lost by rounding, 2^6 at 2^30 and soon more than an exponent.
           // From there on a score that is smaller at all is smaller by 2^6: brought to that size by a power of two, the
@@ -587,8 +567,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float2 x = fma2(make_float2(__uint_as_float(s[c * 32 + i]), __uint_as_float(s[c * 32 + i + 1])), scale2, from2);
-            x.x = exp2_wide(x.x);
-            x.y = exp2_wide(x.y);
+            x.x = exp2_fast(x.x);
+            x.y = exp2_fast(x.y);
             sum[i / 2 & 1] = add2(sum[i / 2 & 1], x);
             p[i / 2] = pack_bf16(x.x, x.y);
           }
@@ -625,8 +605,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         two = item_b - item_a > 1;
         m = two ? fmaxf(m0, m1) : m0;
         const float ref = m == -INFINITY ? 0.f : m;
-        f0 = exp2_wide(m0 - ref);
-        f1 = exp2_wide(m1 - ref);
+        f0 = exp2_fast(m0 - ref);
+        f1 = exp2_fast(m1 - ref);
         l = stats[128 + row] * f0 + (two ? stats[384 + row] * f1 : 0.f);
       }
       int c0 = 0, c1 = 0;
@@ -716,7 +696,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const float ref = high == -INFINITY ? 0.f : high;
           for (int c = c0; c <= c1; ++c) {
             const float* p = A.parts + ((size_t)c * 2 + (c == c0)) * S::part_floats + M * D + qt * 128 + row;
-            sum += __ldcg(p + M) * exp2_wide(__ldcg(p) - ref);
+            sum += __ldcg(p + M) * exp2_fast(__ldcg(p) - ref);
           }
           const float by = sum == 0.f ? 1.f : 1.f / sum;
           // neighbouring threads have neighbouring rows, and a part keeps four columns of all rows together
@@ -731,7 +711,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               float4 y[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) y[i] = __ldcg(reinterpret_cast<const float4*>(p) + (d / 4 + i) * M + qt * 128 + row);
-              const float f = exp2_wide(__ldcg(p + M * D + qt * 128 + row) - ref);
+              const float f = exp2_fast(__ldcg(p + M * D + qt * 128 + row) - ref);
 #pragma unroll
               for (int i = 0; i < 8; ++i) x[i].x += y[i].x * f, x[i].y += y[i].y * f, x[i].z += y[i].z * f, x[i].w += y[i].w * f;
             }

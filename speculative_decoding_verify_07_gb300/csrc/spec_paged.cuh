@@ -1,4 +1,4 @@
-// The paged cache as kernels see it: argument checks, page lookup, e4m3 values.
+// The paged cache as kernels see it: argument checks, page lookup, e4m3 values, and the arithmetic the forward shares.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -114,11 +114,16 @@ __device__ __forceinline__ float exp_value(uint32_t e) {
   return __uint_as_float(e >= 255u ? 0x7fc00000u : (e < 1u ? 1u : e) << 23);
 }
 
+// Two pairs of e4m3 codes as fp16.
+__device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(*lo), "=r"(*hi) : "r"(w));
+}
+
 // Four e4m3 codes as floats (exact).
 __device__ __forceinline__ float4 e4m3x4_float(uint32_t w) {
   uint32_t lo, hi;
-  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi) : "r"(w));
+  e4m3_f16(w, &lo, &hi);
   float4 f;
   asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}"
       : "=f"(f.x), "=f"(f.y) : "r"(lo));
@@ -132,5 +137,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both_of(float x) { return make_float2(x, x); }
 
 }  // namespace specv
