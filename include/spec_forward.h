@@ -121,9 +121,11 @@ size_t spec_attend_workspace_size(int heads, int group, int head_dim);
  * What a query does not see never reaches it, infinities and NaN included.
  * Values of an 8-bit cache under exponent bytes above 221 (2^103 and more) are
  * taken for NaN.
- * Scores, their maximum and sum and the output sums are float32; softmax
- * weights are rounded to bf16 for the product with the values.  One call's
- * results do not depend on timing.
+ * Scores, their maximum and sum and the output sums are float32.  For the
+ * product with the values softmax weights are rounded to bf16, or, with few
+ * rows over an 8-bit cache, to fp16 together with the values' scales, where a
+ * term of a row 2^-25 below its largest is lost.  One call's results do not
+ * depend on timing.
  * Errors: as spec_cache_write, and SPEC_E_WORKSPACE. */
 int spec_attend(const uint16_t* q, int64_t token_stride, int N, int group, float scale, int max_tokens,
                 const spec_cache_t* cache, uint16_t* out, float* lse, uint32_t* flags, void* workspace,
