@@ -358,7 +358,9 @@ int spec_version(void);
 }
 #endif
 
-/* The paged cache, the attention over it and the recurrence of the forward. */
+/* The paged cache, the attention over it and the recurrence of the forward, and the
+ * mixers of hybrid targets and of groups of samples. */
 #include "spec_forward.h"
+#include "spec_hybrid.h"
 
 #endif /* SPEC_VERIFY_H */

@@ -42,11 +42,19 @@ F_TIMEOUT = 256
 
 SPEC_MAX_V = 524288
 SPEC_MAX_K = 16
+SPEC_MAX_CONV = 8
 
 
 # spec_cache_t of include/spec_forward.h, as bytes: k_pages, v_pages, k_exp, v_exp, page_table, cu_tokens, kv_len;
 # page_stride, exp_stride; dtype, B, max_pages, pages, heads, page_size, head_dim.
 CACHE_T = struct.Struct("@7Q2q7i")
+# spec_conv_t of include/spec_hybrid.h: x, weight, bias, state, slot, lens, y, states, last, last_slot, flags; x_row,
+# x_tok; dtype, B, T, C, width, slots, last_slots, silu.
+CONV_T = struct.Struct("@11Q2q8i")
+# spec_scan_t of include/spec_hybrid.h: x, dt, z, b, c, a, skip, dt_bias, state, slot, lens, y, states, last, last_slot,
+# flags; row and token strides of x, dt, z, then row, token and group strides of b, c; dtype, B, T, D, N, groups, slots,
+# last_slots, softplus.
+SCAN_T = struct.Struct("@16Q12q9i4x")
 
 
 class SpecError(RuntimeError):
@@ -97,6 +105,12 @@ def _load(path=_LIB_PATH):
     lib.spec_recur_backward.argtypes = [vp, i64, i64, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp,
                                         vp, vp, sz, vp]
     lib.spec_recur_backward.restype = i32
+    lib.spec_conv.argtypes = [ctypes.c_char_p, vp]
+    lib.spec_conv.restype = i32
+    lib.spec_scan_workspace_size.argtypes = [i32] * 4
+    lib.spec_scan_workspace_size.restype = sz
+    lib.spec_scan.argtypes = [ctypes.c_char_p, vp, sz, vp]
+    lib.spec_scan.restype = i32
     lib.spec_philox4x32_10.argtypes = [vp, u64, vp, ctypes.c_int64, vp]
     lib.spec_philox4x32_10.restype = i32
     lib.spec_status_string.argtypes = [i32]
@@ -798,3 +812,124 @@ def spec_recur_backward(g, h, dh, state=None, slot=None, lens=None, d_last=None,
                                  d_state.data_ptr(), _at(flags), *_space(workspace, dev), _queue(stream, dev))
     _done(rc, "spec_recur_backward")
     return dg, dx, d_state
+
+
+# The mixers of hybrid targets and of groups of samples (include/spec_hybrid.h).
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _mixer_out(given, name, shape, dtype, dev, stream):
+    if given is None:
+        return _empty(shape, dtype, dev, stream)
+    _expect(given, name, dtype, shape, dev)
+    return given
+
+
+def _mixer_states(state, states, last, inner, dtype, B, T, dev, stream):
+    """state, states and last of a call, checked: (slots, last, last_slots)."""
+    slots = 0
+    if state is not None:
+        slots = state.shape[0]
+        _expect(state, "state", dtype, (slots, *inner), dev)
+    if states is not None:
+        _expect(states, "states", dtype, (B, T, *inner), dev)
+    if last is None:
+        return slots, _empty((B, *inner), dtype, dev, stream), B
+    _expect(last, "last", dtype, (last.shape[0], *inner), dev)
+    return slots, last, last.shape[0]
+
+
+def _mixer_rows(B, dev, **given):
+    for name, t in given.items():
+        if t is not None:
+            _expect(t, name, torch.int32, (B,), dev)
+
+
+def spec_conv(x, weight, bias=None, state=None, slot=None, lens=None, *, silu=True, y=None, states=None, last=None,
+              last_slot=None, flags=None, stream=None):
+    """The short causal convolution of a state space layer (see spec_conv in spec_hybrid.h).
+
+    x [B, T, C] float32 or bfloat16 (rows and tokens may be strided); weight [width, C], bias [C] float32; state
+    [slots, width - 1, C] of x's dtype, slot [B], lens [B] int32, each or None.  states [B, T, width - 1, C], where given,
+    receives the state behind each token.  Returns (y [B, T, C], last).  last [B, width - 1, C] is made where None is
+    given; last=state, last_slot=slot updates a cache in place.
+    """
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [B, T, C] and weight [width, C]")
+    shape, dev, dt = x.shape, x.device, _io_dtype(x, "x")
+    B, T, C = shape
+    width = weight.shape[0]
+    if not 2 <= width <= SPEC_MAX_CONV:
+        raise ValueError(f"spec_conv takes 2 to {SPEC_MAX_CONV} taps, not {width}")
+    x_row, x_tok = _recur_strides(x, "x", shape, x.dtype, dev)
+    _expect(weight, "weight", torch.float32, (width, C), dev)
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, (C,), dev)
+    _mixer_rows(B, dev, slot=slot, lens=lens, last_slot=last_slot, flags=flags)
+    queue = _queue(stream, dev)
+    slots, last, last_slots = _mixer_states(state, states, last, (width - 1, C), x.dtype, B, T, dev, stream)
+    y = _mixer_out(y, "y", shape, x.dtype, dev, stream)
+    view = CONV_T.pack(x.data_ptr(), weight.data_ptr(), _address(bias), _address(state), _address(slot), _address(lens),
+                       y.data_ptr(), _address(states), last.data_ptr(), _address(last_slot), _address(flags), x_row, x_tok, dt,
+                       B, T, C, width, slots, last_slots, bool(silu))
+    _done(LIB.spec_conv(view, queue), "spec_conv")
+    return y, last
+
+
+def new_scan_workspace(B: int, T: int, D: int, N: int, device) -> torch.Tensor:
+    """A workspace for spec_scan: calls of these sizes, one at a time."""
+    n = int(LIB.spec_scan_workspace_size(int(B), int(T), int(D), int(N)))
+    if n == 0:
+        raise ValueError(f"spec_scan takes no {B} rows of {T} tokens over {D} channels of {N} states")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _scan_groups(t, name, shape, dtype, dev):
+    """Strides of row, token and group of [B, T, groups, N], N dense."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}")
+    *outer, one = t.stride()
+    if one != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have dense states")
+    return outer
+
+
+def spec_scan(x, dt, a, b, c, skip=None, z=None, dt_bias=None, state=None, slot=None, lens=None, *, softplus=True, y=None,
+              states=None, last=None, last_slot=None, flags=None, workspace=None, stream=None):
+    """The selective scan of a state space layer (see spec_scan in spec_hybrid.h).
+
+    x, dt, z [B, T, D] and b, c [B, T, groups, N] float32 or bfloat16 (strided, with dense channels and states); a [D, N],
+    skip, dt_bias [D] float32; state [slots, D, N] float32, slot [B], lens [B] int32; z, skip, dt_bias, state, slot, lens
+    may be None.  states [B, T, D, N] float32, where given, receives the state behind each token.  Returns (y [B, T, D] of
+    x's dtype, last).  last [B, D, N] float32 is made where None is given; last=state, last_slot=slot updates a cache in
+    place.
+    """
+    if x.dim() != 3 or a.dim() != 2 or b.dim() != 4:
+        raise ValueError("x must be [B, T, D], a [D, N] and b [B, T, groups, N]")
+    shape, dev, kind = x.shape, x.device, _io_dtype(x, "x")
+    B, T, D = shape
+    N, groups = a.shape[1], b.shape[2]
+    strides = [*_recur_strides(x, "x", shape, x.dtype, dev), *_recur_strides(dt, "dt", shape, x.dtype, dev)]
+    strides += (0, 0) if z is None else _recur_strides(z, "z", shape, x.dtype, dev)
+    for t, name in ((b, "b"), (c, "c")):
+        strides += _scan_groups(t, name, (B, T, groups, N), x.dtype, dev)
+    f32 = torch.float32
+    _expect(a, "a", f32, (D, N), dev)
+    for t, name in ((skip, "skip"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _expect(t, name, f32, (D,), dev)
+    _mixer_rows(B, dev, slot=slot, lens=lens, last_slot=last_slot, flags=flags)
+    queue = _queue(stream, dev)
+    slots, last, last_slots = _mixer_states(state, states, last, (D, N), f32, B, T, dev, stream)
+    y = _mixer_out(y, "y", shape, x.dtype, dev, stream)
+    if workspace is None:
+        with _on(stream):
+            workspace = new_scan_workspace(B, T, D, N, dev)
+    view = SCAN_T.pack(x.data_ptr(), dt.data_ptr(), _address(z), b.data_ptr(), c.data_ptr(), a.data_ptr(), _address(skip),
+                       _address(dt_bias), _address(state), _address(slot), _address(lens), y.data_ptr(), _address(states),
+                       last.data_ptr(), _address(last_slot), _address(flags), *strides, kind, B, T, D, N, groups, slots,
+                       last_slots, bool(softplus))
+    _done(LIB.spec_scan(view, *_space(workspace, dev), queue), "spec_scan")
+    return y, last
