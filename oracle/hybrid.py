@@ -73,23 +73,29 @@ def scan(x, dt, a, b, c, skip, z, dt_bias, first, lens, softplus):
     return y, last, states, (ey, el, es)
 
 
-def shared_table(table, shared_rows, shared_len, cu, kv_len, page_size):
-    """The page table that spec_attend would be given for the same results: where a group of two rows or more with new
-    tokens shares a page's positions in whole tiles of 128, they come from its first row's table.  None where a page
-    holds positions of both kinds under different entries (no such table is there)."""
-    B, out = len(kv_len), np.array(table)
-    rows = np.asarray(shared_rows)
+def shared_positions(table, shared_rows, shared_len, cu, kv_len, pages, page_size):
+    """Where each row finds each of its positions, [B, positions]: page * page_size + slot, or -1 without a valid page.
+
+    What a group of two rows or more with new tokens has in common, in whole tiles of 128, is found through its first
+    row's table.  With the cache seen as pages of one position this is the table that spec_attend would be given."""
+    B, n = len(kv_len), table.shape[1] * page_size
+    i, slot = np.divmod(np.arange(n), page_size)
+    own = np.where((table >= 0) & (table < pages), table, -1)[:, i]
+    own = np.where(own >= 0, own * page_size + slot, -1)
+    out, rows = own.copy(), np.asarray(shared_rows)
     if (rows < 0).any() or (rows > B).any() or (np.diff(rows) < 0).any():
         return out
     for g in range(len(shared_len)):
         mine = [r for r in range(rows[g], rows[g + 1]) if cu[r + 1] > cu[r]]
         if len(mine) < 2:
             continue
-        n = min([int(shared_len[g]), table.shape[1] * page_size] + [max(0, int(kv_len[r])) - int(cu[r + 1] - cu[r]) for r in mine])
-        n = max(0, n) // 128 * 128
-        for r in mine:
-            whole, more = divmod(n, page_size)
-            out[r, :whole] = table[rows[g], :whole]
-            if more and table[r, whole] != table[rows[g], whole]:
-                return None
+        common = min([int(shared_len[g]), n] + [max(0, int(kv_len[r])) - int(cu[r + 1] - cu[r]) for r in mine])
+        common = max(0, common) // 128 * 128
+        out[mine, :common] = own[rows[g], :common]
     return out
+
+
+def one_a_page(values):
+    """[pages, heads, page_size, D] as pages of one position."""
+    pages, heads, page_size, dim = values.shape
+    return values.transpose(0, 2, 1, 3).reshape(pages * page_size, heads, 1, dim)

@@ -111,6 +111,10 @@ def _load(path=_LIB_PATH):
     lib.spec_scan_workspace_size.restype = sz
     lib.spec_scan.argtypes = [ctypes.c_char_p, vp, sz, vp]
     lib.spec_scan.restype = i32
+    lib.spec_attend_shared_workspace_size.argtypes = [i32] * 5
+    lib.spec_attend_shared_workspace_size.restype = sz
+    lib.spec_attend_shared.argtypes = [vp, i64, i32, i32, ctypes.c_float, i32, cache, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+    lib.spec_attend_shared.restype = i32
     lib.spec_philox4x32_10.argtypes = [vp, u64, vp, ctypes.c_int64, vp]
     lib.spec_philox4x32_10.restype = i32
     lib.spec_status_string.argtypes = [i32]
@@ -670,6 +674,25 @@ def new_attend_workspace(heads: int, group: int, head_dim: int, device) -> torch
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def _attend_io(q, out, lse, heads, head_dim, dev, stream):
+    """(token stride of q, N, query heads, out, lse) of an attention's arrays, checked."""
+    stride = _token_stride(q, "q")
+    N, hq, dim = q.shape
+    if q.dtype is not torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if dim != head_dim or hq % heads or q.device != dev:
+        raise ValueError(f"q must be [N, a multiple of {heads}, {head_dim}] on {dev}")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    else:
+        _expect(out, "out", torch.bfloat16, (N, hq, dim), dev)
+    if lse is None:
+        lse = _empty((N, hq), torch.float32, dev, stream)
+    else:
+        _expect(lse, "lse", torch.float32, (N, hq), dev)
+    return stride, N, hq, out, lse
+
+
 def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, *, max_tokens, scale=None,
                 out=None, lse=None, flags=None, workspace=None, stream=None):
     """Causal attention of each row's new tokens over its paged cache (see
@@ -683,21 +706,8 @@ def spec_attend(q, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, 
     lse [N, heads * group] float32).
     """
     view, _, heads, head_dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
-    stride, dev = _token_stride(q, "q"), k_pages.device
-    shape = q.shape
-    N, hq, dim = shape
-    if q.dtype is not torch.bfloat16:
-        raise TypeError("q must be bfloat16")
-    if dim != head_dim or hq % heads or q.device != dev:
-        raise ValueError(f"q must be [N, a multiple of {heads}, {head_dim}] on {dev}")
-    if out is None:
-        out = _empty(shape, torch.bfloat16, dev, stream)
-    else:
-        _expect(out, "out", torch.bfloat16, (N, hq, dim), dev)
-    if lse is None:
-        lse = _empty((N, hq), torch.float32, dev, stream)
-    else:
-        _expect(lse, "lse", torch.float32, (N, hq), dev)
+    dev, dim = k_pages.device, head_dim
+    stride, N, hq, out, lse = _attend_io(q, out, lse, heads, head_dim, dev, stream)
     if workspace is None:
         with _on(stream):
             workspace = new_attend_workspace(heads, hq // heads, dim, dev)
@@ -933,3 +943,39 @@ def spec_scan(x, dt, a, b, c, skip=None, z=None, dt_bias=None, state=None, slot=
                        last_slots, bool(softplus))
     _done(LIB.spec_scan(view, *_space(workspace, dev), queue), "spec_scan")
     return y, last
+
+
+def new_attend_shared_workspace(tokens: int, rows: int, heads: int, group: int, head_dim: int, device) -> torch.Tensor:
+    """A zero-filled workspace for spec_attend_shared: up to `tokens` new tokens in up to `rows` rows over a cache of
+    `heads` heads of head_dim, each read by `group` query heads; one stream."""
+    n = int(LIB.spec_attend_shared_workspace_size(int(tokens), int(rows), int(heads), int(group), int(head_dim)))
+    if n == 0:
+        raise ValueError(f"spec_attend_shared takes no {tokens} tokens in {rows} rows over {heads} heads of {head_dim} read by {group}")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def spec_attend_shared(q, shared_rows, shared_len, cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp=None, v_exp=None, *,
+                       max_tokens, scale=None, out=None, lse=None, flags=None, workspace=None, stream=None):
+    """spec_attend for groups of rows that have their first positions in common, which are read once a group (see
+    spec_attend_shared in spec_hybrid.h).
+
+    shared_rows [groups + 1] int32: group g are rows shared_rows[g] .. shared_rows[g + 1] - 1; shared_len [groups] int32: the
+    positions that they share, read through the page table of the group's first row.  All else as for spec_attend, but
+    for the workspace, which new_attend_shared_workspace makes.
+    """
+    view, B, heads, head_dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
+    dev = k_pages.device
+    stride, N, hq, out, lse = _attend_io(q, out, lse, heads, head_dim, dev, stream)
+    if shared_len.dim() != 1 or shared_len.shape[0] > B:
+        raise ValueError(f"shared_len must be [groups], at most {B} groups")
+    groups = shared_len.shape[0]
+    _expect(shared_len, "shared_len", torch.int32, (groups,), dev)
+    _expect(shared_rows, "shared_rows", torch.int32, (groups + 1,), dev)
+    if workspace is None:
+        with _on(stream):
+            workspace = new_attend_shared_workspace(N, B, heads, hq // heads, head_dim, dev)
+    rc = LIB.spec_attend_shared(q.data_ptr(), stride, N, hq // heads, head_dim ** -0.5 if scale is None else scale, max_tokens, view,
+                                shared_rows.data_ptr(), shared_len.data_ptr(), groups, out.data_ptr(), lse.data_ptr(), _at(flags),
+                                *_space(workspace, dev), _queue(stream, dev))
+    _done(rc, "spec_attend_shared")
+    return out, lse

@@ -21,7 +21,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
 SOURCES = ["spec_verify.cu", "spec_kernel.cu", "spec_commit.cu", "spec_api.cu", "spec_noalloc.cu", "spec_draft.cu",
            "spec_cache.cu", "spec_attend.cu", "spec_attend_rows.cu", "spec_attend_wide.cu",
-           "spec_recur.cu", "spec_conv.cu", "spec_scan.cu"]
+           "spec_recur.cu", "spec_conv.cu", "spec_scan.cu", "spec_shared.cu", "spec_attend_rows_common.cu",
+           "spec_attend_rows_own.cu", "spec_attend_wide_common.cu", "spec_attend_wide_own.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

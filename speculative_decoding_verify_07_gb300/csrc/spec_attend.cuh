@@ -14,6 +14,11 @@
 
 namespace specv {
 
+// What positions a launch is about: all that a query sees; those that the rows of a group have in common, for all of
+// their tokens together; or a row's others.
+enum : int { kAll = 0, kCommon = 1, kOwn = 2 };
+constexpr int kCommonTile = 128;     // what is taken as common ends with a tile of either kernel
+
 struct AttendArgs {
   PagedCache C;
   const uint16_t* q;
@@ -27,6 +32,13 @@ struct AttendArgs {
   float scale_log2;      // scale * log2(e): scores are powers of two
   unsigned* joined;      // workspace: per CTA, how many parts of its last item have come
   float* parts;          // workspace: per CTA, two partial results
+  // kCommon: the rows of the cache's view are groups, whose tokens and lengths cu and kv_len have; group g are the
+  // batch's rows group_row[g] .. group_row[g + 1] - 1, and the first one's page table is read
+  const int32_t* group_row;
+  const int32_t* own_from;   // kOwn: the first position of each row that is not common (a multiple of kCommonTile)
+  // The results over the common positions: by (token, head), with the logarithm to base 2 of the sum of weights
+  float* common;
+  float* common_lse;
 };
 
 // 8-bit cache: values under a larger exponent byte are taken for NaN, by either kernel.
@@ -46,17 +58,50 @@ constexpr size_t kAttendCounters = kAttendCtas * sizeof(unsigned);
 // of an item that lie in several CTAs are joined, in the order of their
 // positions, by the CTA that finishes last.
 
+template <int PART>
 struct AttendRow {
   int first, n, kv;     // its packed tokens, and what is cached with them
+  int from;             // kOwn: the first position
 };
 
-__device__ __forceinline__ AttendRow attend_row(const AttendArgs& A, int r) {
-  AttendRow R;
+template <int PART>
+__device__ __forceinline__ AttendRow<PART> attend_row(const AttendArgs& A, int r) {
+  AttendRow<PART> R;
   R.first = __ldg(A.C.cu + r);
   R.n = __ldg(A.C.cu + r + 1) - R.first;
   R.kv = paged_kv_len(A.C, r);
+  if (PART == kOwn) R.from = __ldg(A.own_from + r);
   if (R.first < 0 || R.n < 0 || R.n > A.N - R.first) R.n = 0;
+  if (PART == kCommon && R.kv == 0) R.n = 0;       // (nothing in common is no work)
   return R;
+}
+
+// The batch's row whose page table is read, and flags of a row or of all rows of a group that have tokens.
+template <int PART>
+__device__ __forceinline__ int attend_cache_row(const AttendArgs& A, int row) {
+  return PART == kCommon ? __ldg(A.group_row + row) : row;
+}
+template <int PART>
+__device__ __forceinline__ void attend_flag(const AttendArgs& A, int row, uint32_t flag) {
+  if (!A.flags) return;
+  if (PART != kCommon) {
+    atomicOr(&A.flags[row], flag);
+    return;
+  }
+  const int r1 = __ldg(A.group_row + row + 1);
+  for (int r = __ldg(A.group_row + row); r < r1; ++r)
+    if (__ldg(A.own_from + r) > 0) atomicOr(&A.flags[r], flag);
+}
+
+// The weights with which a query row's results over its own and over the common positions are joined, each given with the
+// logarithm to base 2 of its sum of weights, and the logarithm of both.
+struct AttendJoin {
+  float own, common, lse;
+};
+__device__ __forceinline__ AttendJoin attend_join(float own, float common) {
+  const float top = fmaxf(own, common), ref = top == -INFINITY ? 0.f : top;
+  const float a = exp2_fast(own - ref), b = exp2_fast(common - ref), sum = a + b, by = sum == 0.f ? 0.f : 1.f / sum;
+  return {a * by, b * by, sum == 0.f ? -INFINITY : top + log2f(sum)};
 }
 
 // a / group, for a >= 0.  (The compiler's division is several times as long, and a
@@ -70,26 +115,33 @@ __device__ __forceinline__ int attend_token(const AttendArgs& A, int a) {
 }
 
 // How many positions the row's i-th new token sees; none that the page table cannot hold.
-__device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow& R, int i) {
+template <int PART>
+__device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow<PART>& R, int i) {
+  if (PART == kCommon) return R.kv;
   return max(0, min(R.kv - R.n + i + 1, A.C.max_pages * A.C.page_size));
 }
 
-template <int M, int KT>
-__device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow& R, int qt) {
+// (kOwn: those from the first position on)
+template <int M, int KT, int PART>
+__device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow<PART>& R, int qt) {
+  static_assert(kCommonTile % KT == 0, "common positions end with a tile");
+  if (PART == kCommon) return R.kv / KT;
   const int last = min((qt + 1) * M, R.n * A.group) - 1;
-  return max(1, (attend_sees(A, R, attend_token(A, last)) + KT - 1) / KT);
+  const int tiles = (attend_sees(A, R, attend_token(A, last)) + KT - 1) / KT;
+  return max(1, PART == kOwn ? tiles - R.from / KT : tiles);
 }
 
-template <int M>
-__device__ __forceinline__ int attend_qtiles(const AttendArgs& A, const AttendRow& R) {
+template <int M, int PART>
+__device__ __forceinline__ int attend_qtiles(const AttendArgs& A, const AttendRow<PART>& R) {
   return (R.n * A.group + M - 1) / M;
 }
 
 // The tiles of one head of a row.
-template <int M, int KT>
+template <int M, int KT, int PART>
 __device__ __forceinline__ long long attend_head_tiles(const AttendArgs& A, int r) {
-  const AttendRow R = attend_row(A, r);
+  const AttendRow<PART> R = attend_row<PART>(A, r);
   const int qts = attend_qtiles<M>(A, R);
+  if (PART == kCommon) return (long long)qts * (R.kv / KT);
   long long sum = 0;
 #pragma unroll 4
   for (int q = 0; q < qts; ++q) sum += attend_tiles<M, KT>(A, R, q);
@@ -116,15 +168,15 @@ __device__ __forceinline__ int share_of(const AttendShare& S, int tile) {
   return tile < high ? tile / (S.each + 1) : S.more + (tile - high) / S.each;
 }
 
-template <int M, int KT, int THREADS, int WHOLE>
+template <int M, int KT, int THREADS, int WHOLE, int PART>
 __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* out, long long* sums) {
   const int t = threadIdx.x, each = (A.C.B + THREADS - 1) / THREADS, r0 = min(t * each, A.C.B), r1 = min(r0 + each, A.C.B);
   long long mine = 0;
   for (int r = r0; r < r1; ++r) {
-    mine += attend_head_tiles<M, KT>(A, r) * A.C.heads;
+    mine += attend_head_tiles<M, KT, PART>(A, r) * A.C.heads;
     // (no tile is counted, and so nothing looked up, for positions beyond the page table: they have no page)
-    const AttendRow R = attend_row(A, r);
-    if (R.n > 0 && R.kv > A.C.max_pages * A.C.page_size && blockIdx.x == 0 && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_BAD_IDX);
+    const AttendRow<PART> R = attend_row<PART>(A, r);
+    if (PART != kCommon && R.n > 0 && R.kv > A.C.max_pages * A.C.page_size && blockIdx.x == 0 && A.flags) atomicOr(&A.flags[r], (uint32_t)SPEC_F_BAD_IDX);
   }
   sums[t] = mine;
   __syncthreads();
@@ -157,11 +209,11 @@ __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* o
     if (begin == end || x < before || x >= before + mine) continue;
     int a = x - (int)before, row = r0, per_head;
     for (;; ++row) {
-      per_head = (int)attend_head_tiles<M, KT>(A, row);
+      per_head = (int)attend_head_tiles<M, KT, PART>(A, row);
       if (a < per_head * A.C.heads) break;
       a -= per_head * A.C.heads;
     }
-    const AttendRow R = attend_row(A, row);
+    const AttendRow<PART> R = attend_row<PART>(A, row);
     const int head = a / per_head;
     a -= head * per_head;
     int qt = 0, tiles;
@@ -196,19 +248,19 @@ __device__ __forceinline__ void share_parts(const AttendShare& S, int item, int 
 // another.  COUNT: the first item's tiles are counted again and not read from the
 // share, which gives the wide kernel the better code (2x2048 tokens 2 % faster) and
 // the other the worse (32x5 tokens of group 8, 8 bits, 6 % slower).
-template <int M, int KT, bool COUNT>
+template <int M, int KT, bool COUNT, int PART>
 struct AttendWalk {
   const AttendArgs& A;
-  AttendRow R;
+  AttendRow<PART> R;
   int row, head, qt, tiles;      // the item, and its position tiles
-  int a, b;                      // this segment's
+  int a, b;                      // this segment's, by position
   int at, end;                   // the next tile of all, and the share's end
   int next_a;
 
   __device__ __forceinline__ AttendWalk(const AttendArgs& args, const AttendShare& S)
       : A(args), row(S.row), head(S.head), qt(S.qt), tiles(COUNT ? 0 : S.tiles), a(0), b(0), at(S.begin), end(S.end), next_a(S.a) {
     if (at >= end) return;
-    R = attend_row(A, row);
+    R = attend_row<PART>(A, row);
     if (COUNT) tiles = attend_tiles<M, KT>(A, R, qt);
   }
   // The next segment; false at the end of the share.
@@ -220,7 +272,7 @@ struct AttendWalk {
         qt = 0;
         if (++head >= A.C.heads) {
           head = 0;
-          do R = attend_row(A, ++row); while (R.n == 0);
+          do R = attend_row<PART>(A, ++row); while (R.n == 0);
         }
       }
       tiles = attend_tiles<M, KT>(A, R, qt);
@@ -229,11 +281,14 @@ struct AttendWalk {
     b = min(tiles, a + (end - at));
     at += b - a;
     next_a = b;
+    if (PART == kOwn) a += first(), b += first();
     return true;
   }
-  __device__ __forceinline__ bool whole() const { return a == 0 && b == tiles; }
+  // The tile of positions that the item begins with.
+  __device__ __forceinline__ int first() const { return PART == kOwn ? R.from / KT : 0; }
+  __device__ __forceinline__ bool whole() const { return a == first() && b == first() + tiles; }
   // The first tile of this item among all.
-  __device__ __forceinline__ int item_begin() const { return at - b; }
+  __device__ __forceinline__ int item_begin() const { return at - (b - first()); }
 };
 
 // ---------------------------------------------------------------------- copies
@@ -249,7 +304,17 @@ __device__ __forceinline__ unsigned attend_starts(int box, int j) {
 int attend_map(CUtensorMap* map, void* pool, const PagedCache& C, bool e4m3, int box, bool swizzled);
 
 // The launches.  `maps`: keys, values.
+template <int PART>
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
+template <int PART>
 int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
+
+// Either of them, for items of up to `rows` query rows.
+template <int PART>
+int attend_launch(AttendArgs& A, bool e4m3, long long rows, cudaStream_t st);
+
+// The arguments of spec_attend, checked and laid out; `done`: there is nothing to do.
+int attend_check(const uint16_t* q, int64_t token_stride, int N, int group, float scale, int max_tokens, const spec_cache_t* cache,
+                 uint16_t* out, float* lse, uint32_t* flags, void* workspace, AttendArgs* A, bool* done);
 
 }  // namespace specv

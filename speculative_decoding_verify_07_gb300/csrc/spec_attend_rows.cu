@@ -104,9 +104,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 // What a warp brings next: its positions of a tile, looked up a tile before
 // their copies begin.
-template <int M, int NK, bool E4M3>
+template <int M, int NK, bool E4M3, int PART>
 struct RowsFetch {
-  AttendWalk<M, NK * kRowsWarps, false> I;
+  AttendWalk<M, NK * kRowsWarps, false, PART> I;
   int t, limit;          // the tile, and the positions that its item sees
   bool more;
   int page, slot;        // of position `lane` (NK of them)
@@ -125,8 +125,8 @@ struct RowsFetch {
     const AttendArgs& A = I.A;
     const int pos = (t * kRowsWarps + warp) * NK + lane;
     if ((NK == 32 || lane < NK) && pos < limit) {
-      page = paged_lookup(A.C, I.row, pos, &slot);
-      if (page < 0 && A.flags) atomicOr(&A.flags[I.row], (uint32_t)SPEC_F_BAD_IDX);
+      page = paged_lookup(A.C, attend_cache_row<PART>(A, I.row), pos, &slot);
+      if (page < 0) attend_flag<PART>(A, I.row, SPEC_F_BAD_IDX);
       if (E4M3 && page >= 0) {
         const long long e = page * A.C.exp_bytes + (unsigned)(I.head * A.C.page_size + slot);
         ke = __ldg(A.C.k_exp + e);
@@ -139,7 +139,7 @@ struct RowsFetch {
   }
 };
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3, int MT, int PART>
 __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     attend_rows_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = RowsShape<D, E4M3, MT>;
@@ -168,9 +168,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     for (int i = 0; i < kRowsWarps * S::stages; ++i) mbar_init(&full[0][0] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  attend_share<M, KT, kRowsThreads, 0>(A, &share, sums);
+  attend_share<M, KT, kRowsThreads, 0, PART>(A, &share, sums);
 
-  RowsFetch<M, NK, E4M3> F(A, share);
+  RowsFetch<M, NK, E4M3, PART> F(A, share);
   F.look(warp, lane);
   // a box of one 64-byte row would not begin at a multiple of 128 bytes: its lane copies it
   const bool by_hand = S::half_bytes == 64 && A.box == 1;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
   int stage = 0;
   uint32_t phase = 0;
   const int q4 = lane % 4, r8 = lane / 4;
-  AttendWalk<M, KT, false> W(A, share);
+  AttendWalk<M, KT, false, PART> W(A, share);
   while (W.next()) {
     const int rows = min(M, W.R.n * A.group - W.qt * M);  // query rows of this tile
     if (threadIdx.x == 0) odd = 0, first_nan = 0x7fffffff;
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         // values of NaN: rows that see the first of them
         for (int k = W.a * KT + threadIdx.x; k < k1; k += kRowsThreads) {
           int slot;
-          const int page = paged_lookup(A.C, W.row, k, &slot);
+          const int page = paged_lookup(A.C, attend_cache_row<PART>(A, W.row), k, &slot);
           if (page >= 0 && A.C.v_exp[page * A.C.exp_bytes + (long long)W.head * A.C.page_size + slot] > kAttendTop) atomicMin(&first_nan, k);
         }
         __syncthreads();
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         // values that are not finite at positions that only some rows see
         for (int k = max(fewest, W.a * KT); k < k1; ++k) {
           int slot;
-          const int page = paged_lookup(A.C, W.row, k, &slot);
+          const int page = paged_lookup(A.C, attend_cache_row<PART>(A, W.row), k, &slot);
           if (page < 0) continue;
           const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)W.head * A.C.page_size + slot) * D;
           for (int d = threadIdx.x; d < D; d += kRowsThreads) {
@@ -707,39 +707,70 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
         const long long at = out_at[row];
         float by = sum == 0.f ? 1.f : 1.f / sum;
         if (E4M3) by *= __uint_as_float((127 - kRowsShift) << 23);
-        *reinterpret_cast<uint4*>(A.out + at * D + d) =
-            make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
-                       pack_bf16(x[6] * by, x[7] * by));
-        if (d == 0 && A.lse)
-          A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum) + (E4M3 ? kRowsShift : 0)) * 0.6931471805599453f;
+        if (PART == kAll) {
+          *reinterpret_cast<uint4*>(A.out + at * D + d) =
+              make_uint4(pack_bf16(x[0] * by, x[1] * by), pack_bf16(x[2] * by, x[3] * by), pack_bf16(x[4] * by, x[5] * by),
+                         pack_bf16(x[6] * by, x[7] * by));
+          if (d == 0 && A.lse)
+            A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum) + (E4M3 ? kRowsShift : 0)) * 0.6931471805599453f;
+        } else {
+          float lse = sum == 0.f ? -INFINITY : top + log2f(sum) + (E4M3 ? kRowsShift : 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= by;
+          float4* const common = reinterpret_cast<float4*>(A.common + at * D + d);
+          if (PART == kCommon) {
+            __stcg(common, make_float4(x[0], x[1], x[2], x[3]));
+            __stcg(common + 1, make_float4(x[4], x[5], x[6], x[7]));
+            if (d == 0) __stcg(A.common_lse + at, lse);
+          } else {
+            if (W.first() > 0) {
+              const AttendJoin J = attend_join(lse, __ldcg(A.common_lse + at));
+              const float4 a = __ldcg(common), b = __ldcg(common + 1);
+              const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = x[e] * J.own + y[e] * J.common;
+              lse = J.lse;
+            }
+            *reinterpret_cast<uint4*>(A.out + at * D + d) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            if (d == 0 && A.lse) A.lse[at] = lse * 0.6931471805599453f;
+          }
+        }
       }
     }
-    if (threadIdx.x == 0 && failed && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_TIMEOUT);
+    if (threadIdx.x == 0 && failed) attend_flag<PART>(A, W.row, SPEC_F_TIMEOUT);
     __syncthreads();
   }
   mbar_settle(&failed);
 }
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3, int MT, int PART>
 static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_t st) {
   using S = RowsShape<D, E4M3, MT>;
   static_assert(S::stages >= 2, "a ring needs two stages");
-  const auto kernel = attend_rows_kernel<D, E4M3, MT>;
+  const auto kernel = attend_rows_kernel<D, E4M3, MT, PART>;
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
   kernel<<<S::ctas * 152, kRowsThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int PART>
 static int launch_rows_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
   // 16 rows where they suffice: 64x1 tokens of group 8 at 8000 105 us, with 32 rows 124; 64x3 of group 4 193 and 226
-  return rows <= 16 ? launch_rows<D, E4M3, 1>(A, maps, st) : launch_rows<D, E4M3, 2>(A, maps, st);
+  return rows <= 16 ? launch_rows<D, E4M3, 1, PART>(A, maps, st) : launch_rows<D, E4M3, 2, PART>(A, maps, st);
 }
 
+template <int PART>
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  if (A.C.D == 128) return e4m3 ? launch_rows_of<128, true>(A, rows, maps, st) : launch_rows_of<128, false>(A, rows, maps, st);
-  return e4m3 ? launch_rows_of<64, true>(A, rows, maps, st) : launch_rows_of<64, false>(A, rows, maps, st);
+  if (A.C.D == 128) return e4m3 ? launch_rows_of<128, true, PART>(A, rows, maps, st) : launch_rows_of<128, false, PART>(A, rows, maps, st);
+  return e4m3 ? launch_rows_of<64, true, PART>(A, rows, maps, st) : launch_rows_of<64, false, PART>(A, rows, maps, st);
 }
+
+// One part a translation unit, so that they compile side by side.
+#ifndef SPEC_ATTEND_PART
+#define SPEC_ATTEND_PART kAll
+#endif
+template int launch_attend_rows<SPEC_ATTEND_PART>(const AttendArgs&, bool, int, const CUtensorMap*, cudaStream_t);
 
 }  // namespace specv

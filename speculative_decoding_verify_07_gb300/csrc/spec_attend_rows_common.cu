@@ -1,0 +1,3 @@
+// The attention kernel of spec_attend_rows.cu over what the rows of a group have in common (spec_attend_shared).
+#define SPEC_ATTEND_PART kCommon
+#include "spec_attend_rows.cu"

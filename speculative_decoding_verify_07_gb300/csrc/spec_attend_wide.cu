@@ -138,13 +138,27 @@ __device__ __forceinline__ uint32_t e4m3_bf16(uint32_t high, uint32_t scale) {
 }
 constexpr uint32_t kWideExp = 134;     // the largest exponent byte whose scale, times 2^120, is a bf16 number
 
+// 32 columns of a row's own result, times `by`, with the common positions' where `join`.
+__device__ __forceinline__ void store_joined(uint16_t* out, const float* o, float by, const float4* common, float times, bool join) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (join) a = __ldcg(common + i / 4), b = __ldcg(common + i / 4 + 1);
+    const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = o[i + e] * by + y[e] * times;
+    *reinterpret_cast<uint4*>(out + i) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+}
+
 struct WideBars {
   unsigned long long k_raw[4], k_full[4], k_empty[4];      // keys: codes copied, ready, read
   unsigned long long v_raw[4], v_full[4], v_empty[4];      // values: copied, ready, read
   unsigned long long q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
 };
 
-template <int D, bool E4M3, bool SPLIT>
+template <int D, bool E4M3, bool SPLIT, int PART>
 __global__ void __launch_bounds__(kWideThreads, 1)
     attend_wide_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = WideShape<D, E4M3, SPLIT>;
@@ -190,11 +204,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tmem_before();
   }
-  attend_share<M, KT, kWideThreads, kWideWhole>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
+  attend_share<M, KT, kWideThreads, kWideWhole, PART>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
   fence_proxy_async();
   tmem_after();
   const uint32_t tmem = tmem_base;
-  AttendWalk<M, KT, true> W(A, share);
+  AttendWalk<M, KT, true, PART> W(A, share);
 
   if (warp >= ready_warp && warp < mma_warp) {
     // --------------------------------------------- keys and values made ready
@@ -210,7 +224,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t ke = 0, ve = 0;
       auto look = [&](int t) {
         const int pos = t * KT + tid;
-        entry = pos < limit ? paged_entry(A.C, W.row, pos, &slot) : -1;
+        entry = pos < limit ? paged_entry(A.C, attend_cache_row<PART>(A, W.row), pos, &slot) : -1;
       };
       auto fetch = [&]() {
         const int page = paged_page(A.C, entry);
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 for (int i = 0; i < 4; ++i) {
                   const int pos = t * KT + row0 + 32 * i;
                   int slot;
-                  const int page = pos < limit ? paged_lookup(A.C, W.row, pos, &slot) : -1;
+                  const int page = pos < limit ? paged_lookup(A.C, attend_cache_row<PART>(A, W.row), pos, &slot) : -1;
                   uint32_t e = 0;
                   if (page >= 0) e = (v ? A.C.v_exp : A.C.k_exp)[page * A.C.exp_bytes + (unsigned)(W.head * A.C.page_size + slot)];
                   if (e <= kWideExp || e > (v ? kAttendTop : 254u)) continue;
@@ -351,8 +365,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int j = 0; j < 4; ++j) {
             const int pos = t * KT + 32 * j + lane;
             next_slot[j] = 0;
-            next_page[j] = pos < limit ? paged_lookup(A.C, W.row, pos, &next_slot[j]) : -1;
-            if (next_page[j] < 0 && pos < limit && A.flags) atomicOr(&A.flags[W.row], (uint32_t)SPEC_F_BAD_IDX);
+            next_page[j] = pos < limit ? paged_lookup(A.C, attend_cache_row<PART>(A, W.row), pos, &next_slot[j]) : -1;
+            if (next_page[j] < 0 && pos < limit) attend_flag<PART>(A, W.row, SPEC_F_BAD_IDX);
           }
         };
         look(W.a);
@@ -466,10 +480,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     int done = 0, n = 0, segment = 0;          // this group's steps so far; tiles; items
     constexpr int across = D / 8, turns = across;      // lanes a row of Q or of the result, and turns for a warp's 32 rows
     while (W.next()) {
-      const AttendRow R = W.R;
+      const AttendRow<PART> R = W.R;
       const int item_row = W.row, item_head = W.head, item_qt = W.qt, item_tiles = W.tiles, item_a = W.a, item_b = W.b;
       const bool whole = W.whole();
-      const int item = W.item_begin();
+      const int item = W.item_begin(), item_first = W.first();
       const int mine = item_qt * M + qt * 128 + row, rows = R.n * A.group;
       const bool real = mine < rows;
       const int token = attend_token(A, min(mine, rows - 1)), head = item_head * A.group + min(mine, rows - 1) - token * A.group;
@@ -614,6 +628,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
+      // the common positions' share of the result, for a row's own
+      AttendJoin J = {1.f, 0.f, 0.f};
+      const bool join = PART == kOwn && item_first > 0 && real;
+      if (PART != kAll) {
+        J.lse = l == 0.f ? -INFINITY : m + log2f(l);
+        if (join && whole) J = attend_join(J.lse, __ldcg(A.common_lse + out_row));
+      }
 #pragma unroll 1
       for (int c = 0; c < cols / 32; ++c) {
         const int d = d0 + c * 32;
@@ -635,7 +656,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           } else {
             for (int k = odd; k < k1; ++k) {
               int slot;
-              const int page = paged_lookup(A.C, item_row, k, &slot);
+              const int page = paged_lookup(A.C, attend_cache_row<PART>(A, item_row), k, &slot);
               if (page < 0) continue;
               const uint16_t* v = reinterpret_cast<const uint16_t*>(A.C.v + page * A.C.page_bytes) + ((long long)item_head * A.C.page_size + slot) * D + d;
 #pragma unroll
@@ -652,6 +673,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             __stcg(reinterpret_cast<float4*>(part) + (d + i) / 4 * M + qt * 128 + row, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        } else if (PART != kAll) {
+          float4* const common = reinterpret_cast<float4*>(A.common + out_row * D + d);
+          if (PART == kCommon) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) __stcg(common + i / 4, make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
+          } else {
+            store_joined(A.out + out_row * D + d, o, inv * J.own, common, J.common, join);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
@@ -663,7 +692,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
       }
-      if (!SPLIT && whole) {
+      if (!SPLIT && whole && PART == kAll) {
         // the warp's rows leave by way of Q's place, so that neighbouring lanes write neighbouring columns
         __syncwarp();
 #pragma unroll
@@ -675,7 +704,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         __syncwarp();
       }
-      if (whole && real && d0 == 0 && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      if (PART == kAll) {
+        if (whole && real && d0 == 0 && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      } else if (whole && real && d0 == 0) {
+        if (PART == kCommon) __stcg(A.common_lse + out_row, J.lse);
+        else if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
+      }
       if (!whole) {
         if (real && d0 == 0) {
           __stcg(part + M * D + qt * 128 + row, m);
@@ -699,6 +733,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sum += __ldcg(p + M) * exp2_fast(__ldcg(p) - ref);
           }
           const float by = sum == 0.f ? 1.f : 1.f / sum;
+          if (PART != kAll) {
+            J.lse = sum == 0.f ? -INFINITY : high + log2f(sum);
+            if (join) J = attend_join(J.lse, __ldcg(A.common_lse + out_row));
+          }
           // neighbouring threads have neighbouring rows, and a part keeps four columns of all rows together
 #pragma unroll 1
           for (int d = d0; d < d0 + cols; d += 32) {
@@ -715,16 +753,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) x[i].x += y[i].x * f, x[i].y += y[i].y * f, x[i].z += y[i].z * f, x[i].w += y[i].w * f;
             }
+            if (PART != kAll) {
+              float4* const common = reinterpret_cast<float4*>(A.common + out_row * D + d);
+              if (PART == kCommon) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) __stcg(common + i, make_float4(x[i].x * by, x[i].y * by, x[i].z * by, x[i].w * by));
+              } else {
+                store_joined(A.out + out_row * D + d, &x[0].x, by * J.own, common, J.common, join);
+              }
+              continue;
+            }
 #pragma unroll
             for (int i = 0; i < 8; i += 2)
               *reinterpret_cast<uint4*>(A.out + out_row * D + d + 4 * i) =
                   make_uint4(pack_bf16(x[i].x * by, x[i].y * by), pack_bf16(x[i].z * by, x[i].w * by),
                              pack_bf16(x[i + 1].x * by, x[i + 1].y * by), pack_bf16(x[i + 1].z * by, x[i + 1].w * by));
           }
-          if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
+          if (PART == kAll) {
+            if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
+          } else if (d0 == 0) {
+            if (PART == kCommon) __stcg(A.common_lse + out_row, J.lse);
+            else if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
+          }
         }
       }
-      if (failed && threadIdx.x == 0 && A.flags) atomicOr(&A.flags[item_row], (uint32_t)SPEC_F_TIMEOUT);
+      if (failed && threadIdx.x == 0) attend_flag<PART>(A, item_row, SPEC_F_TIMEOUT);
       tmem_before();
       ++segment;
       if (SPLIT) wide_sync();      // both O have been read before either is written again
@@ -739,27 +792,34 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-template <int D, bool E4M3, bool SPLIT>
+template <int D, bool E4M3, bool SPLIT, int PART>
 static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_t st) {
   using S = WideShape<D, E4M3, SPLIT>;
   static_assert(S::v_stages >= 2, "a ring needs two stages");
-  const auto kernel = attend_wide_kernel<D, E4M3, SPLIT>;
+  const auto kernel = attend_wide_kernel<D, E4M3, SPLIT, PART>;
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
   kernel<<<152, kWideThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int PART>
 static int launch_wide_of(const AttendArgs& A, int rows, const CUtensorMap* maps, cudaStream_t st) {
   // One tile of query rows where it suffices: 16x5 tokens of group 8 over up to 30000 76.8 us, with two tiles 79.7; 32x5 of group 16,
   // heads of 64, 66.5 and 74.0.  Above 128 rows two: 2x2048 tokens 415 us, with one tile 670; 16x17 of group 16 88 and 108.
-  return rows <= 128 ? launch_wide<D, E4M3, true>(A, maps, st) : launch_wide<D, E4M3, false>(A, maps, st);
+  return rows <= 128 ? launch_wide<D, E4M3, true, PART>(A, maps, st) : launch_wide<D, E4M3, false, PART>(A, maps, st);
 }
 
+template <int PART>
 int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st) {
-  if (A.C.D == 128) return e4m3 ? launch_wide_of<128, true>(A, rows, maps, st) : launch_wide_of<128, false>(A, rows, maps, st);
-  return e4m3 ? launch_wide_of<64, true>(A, rows, maps, st) : launch_wide_of<64, false>(A, rows, maps, st);
+  if (A.C.D == 128) return e4m3 ? launch_wide_of<128, true, PART>(A, rows, maps, st) : launch_wide_of<128, false, PART>(A, rows, maps, st);
+  return e4m3 ? launch_wide_of<64, true, PART>(A, rows, maps, st) : launch_wide_of<64, false, PART>(A, rows, maps, st);
 }
+
+// One part a translation unit, so that they compile side by side.
+#ifndef SPEC_ATTEND_PART
+#define SPEC_ATTEND_PART kAll
+#endif
+template int launch_attend_wide<SPEC_ATTEND_PART>(const AttendArgs&, bool, int, const CUtensorMap*, cudaStream_t);
 
 }  // namespace specv

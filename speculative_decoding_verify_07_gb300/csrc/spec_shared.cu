@@ -1,0 +1,134 @@
+// spec_attend_shared: the attention of rows that have their first positions in common.
+//
+// What the rows of a group share is one cache for all their tokens: where n rows of T
+// tokens read the prompt, n T group query rows a head stand against it, which is a
+// product for the tensor cores over bytes that are read once, and not n reads of
+// them.  So there are two attentions: of each group's tokens over the common positions
+// (no mask: every token is behind all of them), and of each row's tokens over its own,
+// causal.  Both are the kernels of spec_attend, which divide their work evenly over the
+// device whatever the lengths.  The first leaves its results, divided by their sums,
+// and the logarithms of the sums in float32 in the workspace; the second joins them as
+// it writes the results.
+//
+// Common positions end with a multiple of 128, the larger tile of the kernels, so that
+// neither has a tile of both kinds; the up to 127 that are left go to each row.
+#include "spec_attend.cuh"
+
+namespace specv {
+
+constexpr int kGroupThreads = 1024;
+
+// Finds what each group has in common: shared_len, but nothing behind the first new token of any of its rows or
+// beyond the page table, in whole tiles, and nothing for a single row.  A warp a group.
+static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(const PagedCache C, int N, const int32_t* shared_rows, const int32_t* shared_len,
+                                                                      int groups, int32_t* group_row, int32_t* group_cu, int32_t* group_len,
+                                                                      int32_t* own_from) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  bool ok = true;
+  for (int g = threadIdx.x; g < groups; g += kGroupThreads) {
+    const int a = __ldg(shared_rows + g), b = __ldg(shared_rows + g + 1);
+    ok = ok && a >= 0 && a <= b && b <= C.B;
+  }
+  ok = __syncthreads_and(ok);
+  const int first = ok ? __ldg(shared_rows) : 0, last = ok ? __ldg(shared_rows + groups) : 0;
+  for (int r = threadIdx.x; r < C.B; r += kGroupThreads)
+    if (r < first || r >= last) own_from[r] = 0;
+  for (int g = warp; g < groups; g += kGroupThreads / 32) {
+    const int a = ok ? __ldg(shared_rows + g) : 0, b = ok ? __ldg(shared_rows + g + 1) : 0;
+    const int t0 = __ldg(C.cu + a), t1 = __ldg(C.cu + b);
+    int least = t0 < 0 || t1 > N ? 0 : 0x7fffffff, busy = 0;     // (a row's tokens are among the group's, which are there)
+    for (int r = a + lane; r < b; r += 32) {
+      const int c0 = __ldg(C.cu + r), c1 = __ldg(C.cu + r + 1);
+      if (c0 < t0 || c1 > t1) least = 0;
+      if (c0 < c1 && least > 0) {
+        least = min(least, paged_kv_len(C, r) - (c1 - c0));
+        ++busy;
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    busy = __reduce_add_sync(0xffffffffu, busy);
+    int len = 0;
+    if (busy > 1) len = max(0, min(min(least, __ldg(shared_len + g)), C.max_pages * C.page_size)) / kCommonTile * kCommonTile;
+    for (int r = a + lane; r < b; r += 32) own_from[r] = __ldg(C.cu + r + 1) > __ldg(C.cu + r) ? len : 0;
+    if (lane == 0) {
+      group_len[g] = len;
+      group_row[g] = a;
+      group_cu[g] = t0;
+      if (g == groups - 1) {
+        group_row[groups] = b;
+        group_cu[groups] = t1;
+      }
+    }
+  }
+}
+
+// Workspace, behind that of spec_attend: the groups' rows, tokens and lengths and the rows' first own positions, then
+// the results over the common positions.
+struct SharedSpace {
+  size_t group_row, group_cu, group_len, own_from, lse, out, bytes;
+
+  SharedSpace(size_t base, int N, int B, long long hq, int D) {
+    auto take = [&](size_t n) {
+      const size_t at = base;
+      base = (base + n + 255) / 256 * 256;
+      return at;
+    };
+    base = (base + 255) / 256 * 256;
+    group_row = take(((size_t)B + 1) * 4);
+    group_cu = take(((size_t)B + 1) * 4);
+    group_len = take((size_t)B * 4);
+    own_from = take((size_t)B * 4);
+    lse = take((size_t)N * hq * 4);
+    out = take((size_t)N * hq * D * 4);
+    bytes = base;
+  }
+};
+
+}  // namespace specv
+
+extern "C" size_t spec_attend_shared_workspace_size(int N, int B, int heads, int group, int head_dim) {
+  const size_t base = spec_attend_workspace_size(heads, group, head_dim);
+  if (base == 0 || N < 0 || B < 0 || (long long)heads * group > 65535) return 0;
+  return specv::SharedSpace(base, N, B, (long long)heads * group, head_dim).bytes;
+}
+
+extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N, int group, float scale, int max_tokens,
+                                  const spec_cache_t* cache, const int32_t* shared_rows, const int32_t* shared_len, int groups,
+                                  uint16_t* out, float* lse, uint32_t* flags, void* workspace, size_t workspace_bytes,
+                                  void* cuda_stream) {
+  using namespace specv;
+  AttendArgs A;
+  bool done;
+  const int rc = attend_check(q, token_stride, N, group, scale, max_tokens, cache, out, lse, flags, workspace, &A, &done);
+  if (rc != SPEC_OK) return rc;
+  if (groups < 0 || groups > A.C.B) return SPEC_E_DIM;
+  if (done) return SPEC_OK;
+  if (groups > 0 && (!shared_rows || !shared_len)) return SPEC_E_NULL;
+  if (!paged_aligned(shared_rows, 4) || !paged_aligned(shared_len, 4)) return SPEC_E_ALIGN;
+  if (workspace_bytes < spec_attend_shared_workspace_size(N, A.C.B, A.C.heads, group, A.C.D)) return SPEC_E_WORKSPACE;
+  const int arc = check_arch();
+  if (arc != SPEC_OK) return arc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  const bool e4m3 = cache->dtype == SPEC_E4M3;
+  const long long rows = (long long)max_tokens * group;
+  if (groups == 0) return attend_launch<kAll>(A, e4m3, rows, st);
+  char* const base = static_cast<char*>(workspace);
+  const SharedSpace S(spec_attend_workspace_size(A.C.heads, group, A.C.D), N, A.C.B, A.hq, A.C.D);
+  int32_t* const group_row = reinterpret_cast<int32_t*>(base + S.group_row);
+  int32_t* const group_cu = reinterpret_cast<int32_t*>(base + S.group_cu);
+  int32_t* const group_len = reinterpret_cast<int32_t*>(base + S.group_len);
+  int32_t* const own_from = reinterpret_cast<int32_t*>(base + S.own_from);
+  attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group_row, group_cu, group_len, own_from);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_E_CUDA;
+  A.group_row = group_row;
+  A.own_from = own_from;
+  A.common = reinterpret_cast<float*>(base + S.out);
+  A.common_lse = reinterpret_cast<float*>(base + S.lse);
+  AttendArgs common = A;
+  common.C.B = groups;
+  common.C.cu = group_cu;
+  common.C.kv_len = group_len;
+  // a group's tokens are not known here: as many as each would have of all
+  const int each = attend_launch<kCommon>(common, e4m3, ((long long)N + groups - 1) / groups * group, st);
+  return each != SPEC_OK ? each : attend_launch<kOwn>(A, e4m3, rows, st);
+}

@@ -5,6 +5,8 @@ import re
 import pytest
 import torch
 
+from tests.test_forward_abi_cpu import CACHE, view
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 4096   # a fake, aligned address: never dereferenced
 OK, NULL, DIM, DTYPE, ALIGN, WORKSPACE = 0, -1, -2, -3, -4, -5
@@ -74,11 +76,37 @@ def test_scan_checks(sv):
     assert sv.LIB.spec_scan_workspace_size(1, 1, 8, 16) >= 256
 
 
+def shared(sv, n=4, q=P, rows=P, lens=P, groups=2, out=P, lse=P, group=4, most=3, stride=0, flags=None, ws=P, wsb=1 << 40, **kw):
+    return sv.LIB.spec_attend_shared(q, stride, n, group, 0.1, most, view(sv, **kw), rows, lens, groups, out, lse, flags, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", CACHE)
+def test_shared_checks_the_cache(sv, kw, code):
+    assert shared(sv, **{"groups": 0, **kw} if kw.get("B") == 0 else kw) == code
+
+
+def test_shared_checks(sv):
+    assert shared(sv, n=-1) == DIM and shared(sv, group=0) == DIM and shared(sv, group=65) == DIM and shared(sv, most=-1) == DIM
+    assert shared(sv, stride=64) == DIM and shared(sv, groups=-1) == DIM and shared(sv, groups=3) == DIM
+    assert shared(sv, n=0, q=None) == OK
+    for name in ("q", "rows", "lens", "out", "ws"):
+        assert shared(sv, **{name: None}) == NULL
+    assert shared(sv, q=P + 2) == ALIGN and shared(sv, out=P + 8) == ALIGN and shared(sv, lse=P + 2) == ALIGN
+    assert shared(sv, rows=P + 2) == ALIGN and shared(sv, lens=P + 1) == ALIGN and shared(sv, flags=P + 2) == ALIGN
+    assert shared(sv, ws=P + 16) == ALIGN
+    size = sv.LIB.spec_attend_shared_workspace_size
+    assert shared(sv, wsb=size(4, 2, 2, 4, 64) - 1) == WORKSPACE
+    assert size(-1, 2, 2, 4, 64) == 0 and size(4, -1, 2, 4, 64) == 0 and size(4, 2, 0, 4, 64) == 0 and size(4, 2, 2, 65, 64) == 0
+    assert size(4, 2, 2, 4, 80) == 0 and size(4, 2, 65535, 2, 64) == 0
+    assert size(4, 2, 2, 4, 64) >= sv.LIB.spec_attend_workspace_size(2, 4, 64) + 4 * 8 * 65 * 4
+
+
 def test_valid_calls_reach_the_device(sv):
     if torch.cuda.is_available():
         pytest.skip("the calls would run")
     none = {n: None for n in ("state", "slot", "lens", "states", "last_slot", "flags")}
     assert conv(sv) in REACHED and conv(sv, **none, bias=None, dtype=0, silu=0) in REACHED and conv(sv, T=0, x=None) in REACHED
+    assert shared(sv) in REACHED and shared(sv, rows=None, lens=None, groups=0) in REACHED
     assert scan(sv) in REACHED and scan(sv, **none, z=None, skip=None, dt_bias=None, dtype=0) in REACHED
 
 
@@ -122,3 +150,13 @@ def test_binding_refuses_tensors(sv):
     refuses(TypeError, sv.spec_scan, **s, lens=torch.zeros(2))
     refuses(ValueError, sv.spec_scan, **s)                                       # on the host
     refuses(ValueError, sv.new_scan_workspace, 1, 1, 8, 12, "cpu")
+    kv, i32 = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16), lambda *v: torch.tensor(v, dtype=torch.int32)
+    cache = i32(0, 1, 2), i32(3, 3), torch.zeros((2, 3), dtype=torch.int32), kv, kv
+    q = torch.zeros((2, 8, 64), dtype=torch.bfloat16)
+    refuses(ValueError, sv.spec_attend_shared, q, i32(0, 2), i32(3, 3), *cache, max_tokens=1)
+    refuses(ValueError, sv.spec_attend_shared, q, i32(0, 1, 2, 2), i32(3, 3, 3), *cache, max_tokens=1)
+    refuses(TypeError, sv.spec_attend_shared, q, i32(0, 2).long(), i32(3), *cache, max_tokens=1)
+    refuses(TypeError, sv.spec_attend_shared, q.float(), i32(0, 2), i32(3), *cache, max_tokens=1)
+    refuses(ValueError, sv.spec_attend_shared, q[:, :5], i32(0, 2), i32(3), *cache, max_tokens=1)
+    refuses(ValueError, sv.spec_attend_shared, q, i32(0, 2), i32(3), *cache, max_tokens=1)           # on the host
+    refuses(ValueError, sv.new_attend_shared_workspace, 2, 2, 2, 4, 80, "cpu")

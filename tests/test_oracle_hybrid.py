@@ -68,11 +68,25 @@ def test_scan_groups_gate_softplus_and_lengths():
     assert all((e >= 0).all() for e in err)
 
 
-def test_shared_table():
-    table = np.array([[0, 1, 2], [0, 3, 4], [5, 6, 7], [8, 9, 10]])
+def test_shared_positions():
+    table = np.array([[0, 1, 2], [-1, 3, 4], [5, 6, 7], [8, 9, 11]])
     cu, kv = np.array([0, 1, 2, 3, 3]), np.array([300, 200, 300, 300])
-    same = lambda rows, n: oh.shared_table(table, rows, n, cu, kv, 128)
-    assert np.array_equal(same([0, 2], [300])[1], [0, 3, 4])       # row 1's own token is at 199: one tile
-    assert np.array_equal(same([2, 4], [300]), table)              # row 3 has no new tokens
-    assert np.array_equal(same([0, 3], [300])[2], [0, 6, 7])
-    assert np.array_equal(same([3, 1], [300]), table) and np.array_equal(same([0, 5], [300]), table)
+    same = lambda rows, n: oh.shared_positions(table, rows, n, cu, kv, 11, 128)
+    own = same([0], [])
+    assert own[0, 130] == 130 and own[1, 5] == -1 and own[2, 300] == 7 * 128 + 44 and (own[3, 256:] == -1).all()
+    got = same([0, 2], [300])                                   # row 1's own token is at 199: one tile
+    assert np.array_equal(got[1, :128], own[0, :128]) and np.array_equal(got[1, 128:], own[1, 128:])
+    assert np.array_equal(np.delete(got, 1, 0), np.delete(own, 1, 0))
+    for rows in ([2, 4], [3, 1], [0, 5], [-1, 2]):              # one row with tokens; no order; out of range
+        assert np.array_equal(same(rows, [300]), own)
+    assert np.array_equal(same([0, 3], [127]), own) and np.array_equal(same([0, 3], [-5]), own)
+
+
+def test_pages_of_one_position_are_the_same_cache():
+    rng = np.random.default_rng(5)
+    k, v, q = rng.standard_normal((4, 2, 6, 8)), rng.standard_normal((4, 2, 6, 8)), rng.standard_normal((3, 4, 8))
+    cu, kv, table = np.array([0, 1, 3]), np.array([9, 14]), np.array([[2, 0, -1], [3, 1, 9]])
+    a = of.attend(q, cu, kv, table, k, v, 0.3)
+    at = oh.shared_positions(table, [0], [], cu, kv, 4, 6)
+    b = of.attend(q, cu, kv, at, oh.one_a_page(k), oh.one_a_page(v), 0.3)
+    assert all(np.array_equal(x, y) for x, y in zip(a, b)) and a[2].tolist() == [0, of.F_BAD_IDX]
