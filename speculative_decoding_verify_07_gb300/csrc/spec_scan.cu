@@ -11,10 +11,6 @@
 #include "spec_mixer.cuh"
 #include "spec_tma.cuh"
 
-#ifndef SPEC_SCAN_CTAS
-#define SPEC_SCAN_CTAS 2
-#endif
-
 namespace specv {
 
 struct ScanArgs {
@@ -30,24 +26,24 @@ struct ScanArgs {
   bool softplus;
 };
 
-// ln(1 + exp(v)) within 12 half steps (2^-24) of itself: max(v, 0) + 2 atanh(e / (2 + e)), e = exp(-|v|), by
-// the series of atanh up to s^15, s = e / (2 + e) at most 1/3 (what is left out is 2^-26 of it).
-__device__ __forceinline__ float2 softplus(float2 v) {
-  const float2 pos = make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
-  const float2 m = make_float2(-fminf(fabsf(v.x), 87.f), -fminf(fabsf(v.y), 87.f));
-  // exp(m) with the rounding of m log2(e) made up for
-  const float2 p = mul2(m, both_of(kLog2e)), low = fma2(m, both_of(1.92596299e-8f), fma2(m, both_of(kLog2e), make_float2(-p.x, -p.y)));
-  const float2 e0 = make_float2(exp2_fast(p.x), exp2_fast(p.y)), e = fma2(e0, mul2(low, both_of(0.6931471805599453f)), e0);
-  const float2 s = make_float2(__fdividef(e.x, 2.f + e.x), __fdividef(e.y, 2.f + e.y)), q = mul2(s, s);
-  float2 t = both_of(1.f / 15.f);
-  t = fma2(t, q, both_of(1.f / 13.f));
-  t = fma2(t, q, both_of(1.f / 11.f));
-  t = fma2(t, q, both_of(1.f / 9.f));
-  t = fma2(t, q, both_of(1.f / 7.f));
-  t = fma2(t, q, both_of(1.f / 5.f));
-  t = fma2(t, q, both_of(1.f / 3.f));
-  t = fma2(t, q, both_of(1.f));
-  return fma2(add2(s, s), t, pos);
+// ln(1 + exp(v)) within 12 half steps (2^-24) of itself: max(v, 0) + ln(1 + e), e = exp(-|v|), with the polynomial
+// of degree 8 that is nearest to ln(1 + e) / e over [0, 1] (by Remez's method; 1.3e-7 of it off as evaluated here).
+__device__ __forceinline__ float softplus(float v) {
+  float pos;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(pos) : "f"(v));
+  // exp(-m) with the roundings of log2(e) and of the product made up for
+  const float m = fminf(fabsf(v), 87.f), p = m * -kLog2e, low = fmaf(m, -1.92596299e-8f, fmaf(m, -kLog2e, -p));
+  const float e0 = exp2_fast(p), e = fmaf(e0, low * 0.6931471805599453f, e0);
+  float t = 0x1.56ee0ap-8f;
+  t = fmaf(t, e, -0x1.e369f2p-6f);
+  t = fmaf(t, e, 0x1.4069dcp-4f);
+  t = fmaf(t, e, -0x1.17d2c2p-3f);
+  t = fmaf(t, e, 0x1.874a80p-3f);
+  t = fmaf(t, e, -0x1.fcc8c6p-3f);
+  t = fmaf(t, e, 0x1.553004p-2f);
+  t = fmaf(t, e, -0x1.fffeacp-2f);
+  t = fmaf(t, e, 0x1.fffffep-1f);
+  return fmaf(t, e, pos);
 }
 
 // exp(g) of two states, y = g log2(e).  An error of the decay adds up over the tokens that
@@ -158,12 +154,11 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanA
       b[k].load(A.b, bb + t * A.b_tok, wide);
       c[k].load(A.c, cb + t * A.c_tok, wide);
     }
-    if (A.softplus) {
-      const float2 s = softplus(make_float2(delta[0], delta[1]));
-      delta[0] = s.x, delta[1] = s.y;
-    }
 #pragma unroll
-    for (int k = 0; k < own; ++k) put[k] = delta[k] * x[k];
+    for (int k = 0; k < own; ++k) {
+      if (A.softplus) delta[k] = softplus(delta[k]);
+      put[k] = delta[k] * x[k];
+    }
     float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -203,31 +198,39 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanA
 
 // --------------------------------------------------------------- many tokens
 //
-// A CTA walks tiles of tokens of its channels: delta, delta x, b and c of a tile are made
-// in shared memory by all threads, each lane then takes two channels by four states through
-// the tile's tokens and leaves its part of each sum there, and what goes through a token's
-// elements again (the sum, skip, gate, output) is done by the thread that fetched them.  Two
-// channels a lane share the loads of b and c.
+// A CTA walks tiles of tokens of its channels, with two halves of its warps one behind the
+// other.  One half makes delta, delta x, b and c of a tile in shared memory.  The other takes
+// it from there, a lane two channels by four states, through the tile's tokens and leaves each
+// lane's part of the sums.  The first then goes through the tile's elements again (the sum,
+// skip, gate, output).
+//
+// Bound by issue slots and the latency of a lane's chain (decay, state), with few warps an
+// SM; the elements' own arithmetic (softplus, gate, a third of all) is off that chain.
 //
 // Decays are ex2.approx alone here, whose lean to one side (see scan_decay) would add up over
 // the tokens that a state remembers.  So the tile's decays are also multiplied, and at its end
 // the state that entered gets the difference to the exact decay of the tile's sum of delta.
 
-#ifndef SPEC_SCAN_THREADS
-#define SPEC_SCAN_THREADS 256
+#ifndef SPEC_SCAN_CTAS
+#define SPEC_SCAN_CTAS 2
 #endif
-constexpr int kScanThreads = SPEC_SCAN_THREADS;
-constexpr int kScanPair = 2;           // channels of a lane
+#ifndef SPEC_SCAN_GROUP
+#define SPEC_SCAN_GROUP 4
+#endif
+constexpr int kScanThreads = 128;      // of each half
+constexpr int kScanLane = 2;           // channels of a lane
 constexpr int kScanTile = 16;          // tokens of a tile
+constexpr int kScanGroup = SPEC_SCAN_GROUP;          // tokens that a lane takes together
 
 template <bool BF16, int N, int VEC>
 struct ScanShape {
   static constexpr int L = N / 4;                              // lanes of a channel
-  static constexpr int CH = kScanThreads / L * kScanPair;      // channels of a CTA
+  static constexpr int CH = kScanThreads / L * kScanLane;      // channels of a CTA
   static constexpr int vecs = CH / VEC;                        // a token's channels, VEC at a time
-  static constexpr int rows = kScanThreads / vecs;             // tokens fetched at a time
+  static constexpr int rows = kScanThreads / vecs;             // tokens of a fetch
   static constexpr int per = rows > kScanTile ? 1 : kScanTile / rows;
-  static constexpr int bc = kScanTile * N / 2 < kScanThreads ? 1 : kScanTile * N / 2 / kScanThreads;    // pairs of states of b and c a thread
+  static constexpr int bc_rows = kScanThreads / (N / 2);       // the same of pairs of states of b and c
+  static constexpr int bc = bc_rows > kScanTile ? 1 : kScanTile / bc_rows;
 };
 
 // VEC neighbouring elements as they are in memory.
@@ -252,10 +255,9 @@ struct ScanVec {
       w[0] = v.x, w[kWords / 4] = v.y, w[kWords / 2] = v.z, w[kWords / 4 * 3] = v.w;
     }
   }
-  // Elements 2 i and 2 i + 1 (zero where there is none).
-  __device__ __forceinline__ float2 get(int i) const {
-    if (BF16) return make_float2(bf16_lo(w[i]), VEC > 1 ? bf16_hi(w[i]) : 0.f);
-    return make_float2(__uint_as_float(w[VEC > 1 ? 2 * i : 0]), VEC > 1 ? __uint_as_float(w[VEC > 1 ? 2 * i + 1 : 0]) : 0.f);
+  __device__ __forceinline__ float get(int i) const {
+    if (BF16) return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    return __uint_as_float(w[BF16 ? 0 : i]);
   }
 };
 
@@ -278,57 +280,84 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& A, int ch) {
 
 template <int N, int CH, bool Y>
 struct ScanShared {
-  float2 step[kScanTile][CH];                    // (delta, delta x)
-  float b[kScanTile][N], c[Y ? kScanTile : 1][N];
-  float part[Y ? kScanTile : 1][kScanPair][kScanThreads];     // each thread's part of the sums of its channels
+  struct Tile {
+    float4 step[kScanTile][CH / 2];              // (delta, delta, delta x, delta x) of two channels
+    float b[kScanTile][N], c[Y ? kScanTile : 1][N];
+    // each lane's parts of the sums of its two channels; rows are so far apart that a warp's 256 bytes meet no bank more
+    // than twice
+    float2 part[Y ? kScanTile : 1][N / 4][CH / 2 + (N < 128 ? 128 / N : 2)];
+  } tile[2];
+  float bias[CH], skip[Y ? CH : 1];
+
+  __device__ __forceinline__ static void fill(float* to, const float* p, const ScanPlace& P) {
+    for (int c = threadIdx.x; c < CH; c += 2 * kScanThreads) to[c] = p && c < P.left ? __ldg(p + P.d0 + c) : 0.f;
+  }
 };
+
+// The halves' barriers, one of each for either buffer: a tile is made, a tile has been walked.
+constexpr int kScanMade = 1, kScanWalked = 3;
+template <int ID>
+__device__ __forceinline__ void scan_wait(bool second) {
+  if (second) asm volatile("bar.sync %0, 256;" ::"n"(ID + 1) : "memory");
+  else asm volatile("bar.sync %0, 256;" ::"n"(ID) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void scan_tell(bool second) {
+  if (second) asm volatile("bar.arrive %0, 256;" ::"n"(ID + 1) : "memory");
+  else asm volatile("bar.arrive %0, 256;" ::"n"(ID) : "memory");
+}
 
 // A tile's elements on their way, and where this thread's lie.
 template <bool BF16, int N, int VEC, bool Y, bool GATE>
 struct ScanFetch {
   using S = ScanShape<BF16, N, VEC>;
+  using Shared = ScanShared<N, S::CH, Y>;
+  using Tile = typename Shared::Tile;
   static constexpr int es = BF16 ? 2 : 4;
   ScanVec<BF16, VEC> x[S::per], dt[S::per], z[GATE ? S::per : 1];
   ScanVec<BF16, 2> b[S::bc], c[Y ? S::bc : 1];
-  const unsigned char *px, *pdt, *pz;              // of the row's token 0
-  const unsigned char *pb, *pc;
-  bool whole;                                      // all channels of the CTA are there
+  const unsigned char *px, *pdt, *pz, *pb, *pc;    // of this thread's first element in the row's first tile
 
-  // The i-th fetch's token of the tile, and the first channel.
-  static __device__ __forceinline__ int token(int i) { return threadIdx.x / S::vecs + i * S::rows; }
+  // The i-th fetch's token of the tile, and its first channel.
+  static __device__ __forceinline__ int token(int i) { return threadIdx.x % kScanThreads / S::vecs + i * S::rows; }
   static __device__ __forceinline__ int channel() { return threadIdx.x % S::vecs * VEC; }
   static __device__ __forceinline__ bool real(int i) { return S::rows <= kScanTile || token(i) < kScanTile; }
+  // The same of b and c: a pair of states.
+  static __device__ __forceinline__ int bc_token(int i) { return threadIdx.x % kScanThreads / (N / 2) + i * S::bc_rows; }
+  static __device__ __forceinline__ int bc_state() { return threadIdx.x % (N / 2) * 2; }
+  static __device__ __forceinline__ bool bc_real(int i) { return S::bc_rows <= kScanTile || bc_token(i) < kScanTile; }
 
   __device__ __forceinline__ ScanFetch(const ScanArgs& A, const ScanPlace& P) {
-    px = static_cast<const unsigned char*>(A.x) + (P.r * A.x_row + P.d0) * es;
-    pdt = static_cast<const unsigned char*>(A.dt) + (P.r * A.dt_row + P.d0) * es;
-    if (GATE) pz = static_cast<const unsigned char*>(A.z) + (P.r * A.z_row + P.d0) * es;
-    pb = static_cast<const unsigned char*>(A.b) + (P.r * A.b_row + P.g * A.b_group) * es;
-    if (Y) pc = static_cast<const unsigned char*>(A.c) + (P.r * A.c_row + P.g * A.c_group) * es;
-    whole = P.left == S::CH;
+    const int c = P.d0 + channel(), t = token(0);
+    px = static_cast<const unsigned char*>(A.x) + (P.r * A.x_row + t * A.x_tok + c) * es;
+    pdt = static_cast<const unsigned char*>(A.dt) + (P.r * A.dt_row + t * A.dt_tok + c) * es;
+    if (GATE) pz = static_cast<const unsigned char*>(A.z) + (P.r * A.z_row + t * A.z_tok + c) * es;
+    pb = static_cast<const unsigned char*>(A.b) + (P.r * A.b_row + P.g * A.b_group + bc_token(0) * A.b_tok + bc_state()) * es;
+    if (Y) pc = static_cast<const unsigned char*>(A.c) + (P.r * A.c_row + P.g * A.c_group + bc_token(0) * A.c_tok + bc_state()) * es;
   }
   __device__ __forceinline__ void load(const ScanArgs& A, const ScanPlace& P, int t0, int end, bool pairs) {
-    const bool all = whole && t0 + kScanTile <= end;
+    const int rows = end - t0;
+    const unsigned char *qx = px + t0 * A.x_tok * es, *qdt = pdt + t0 * A.dt_tok * es, *qz = pz;
+    if (GATE) qz += t0 * A.z_tok * es;
 #pragma unroll
     for (int i = 0; i < S::per; ++i) {
-      const int t = t0 + token(i), c = channel();
-      if (real(i) && (all || (t < end && c < P.left))) {
-        x[i].load(px + (t * A.x_tok + c) * es);
-        dt[i].load(pdt + (t * A.dt_tok + c) * es);
-        if (GATE) z[GATE ? i : 0].load(pz + (t * A.z_tok + c) * es);
-      } else {
-        x[i].zero(), dt[i].zero();
-        if (GATE) z[GATE ? i : 0].zero();
+      x[i].zero(), dt[i].zero();
+      if (GATE) z[GATE ? i : 0].zero();
+      if (real(i) && token(i) < rows && channel() < P.left) {
+        x[i].load(qx + i * (S::rows * es) * A.x_tok);
+        dt[i].load(qdt + i * (S::rows * es) * A.dt_tok);
+        if (GATE) z[GATE ? i : 0].load(qz + i * (S::rows * es) * A.z_tok);
       }
     }
+    const unsigned char *qb = pb + t0 * A.b_tok * es, *qc = pc;
+    if (Y) qc += t0 * A.c_tok * es;
 #pragma unroll
     for (int i = 0; i < S::bc; ++i) {
-      const int at = i * kScanThreads + threadIdx.x, t = t0 + at / (N / 2), n = at % (N / 2) * 2;
       b[i].zero();
       if (Y) c[Y ? i : 0].zero();
-      if (at < kScanTile * N / 2 && t < end) {
-        get(b[i], pb + (t * A.b_tok + n) * es, pairs);
-        if (Y) get(c[Y ? i : 0], pc + (t * A.c_tok + n) * es, pairs);
+      if (bc_real(i) && bc_token(i) < rows) {
+        get(b[i], qb + i * (S::bc_rows * es) * A.b_tok, pairs);
+        if (Y) get(c[Y ? i : 0], qc + i * (S::bc_rows * es) * A.c_tok, pairs);
       }
     }
   }
@@ -344,63 +373,60 @@ struct ScanFetch {
     }
   }
   // The tile in shared memory.  Tokens behind `end` leave the state.
-  __device__ __forceinline__ void put(const ScanArgs& A, const ScanPlace& P, int t0, int end, ScanShared<N, S::CH, Y>& sm) const {
-    const bool all = whole && t0 + kScanTile <= end;
+  __device__ __forceinline__ void put(const ScanArgs& A, const ScanPlace& P, int t0, int end, const float* bias, Tile& sm) const {
 #pragma unroll
     for (int i = 0; i < S::per; ++i) {
-      const int t = token(i), c = channel();
       if (!real(i)) continue;
-      const bool there = all || (t0 + t < end && c < P.left);
+      const int at = channel();
+      const bool there = token(i) < end - t0 && at < P.left;
+      float delta[VEC], in[VEC];
 #pragma unroll
-      for (int v = 0; v < (VEC + 1) / 2; ++v) {
-        float2 bias = make_float2(0.f, 0.f);
-        if (A.dt_bias && there) {
-          if (VEC > 1) bias = __ldg(reinterpret_cast<const float2*>(A.dt_bias + P.d0 + c) + v);
-          else bias.x = __ldg(A.dt_bias + P.d0 + c);
-        }
-        float2 delta = add2(dt[i].get(v), bias);
-        if (A.softplus) delta = softplus(delta);
-        if (!there) delta = make_float2(0.f, 0.f);
-        const float2 in = mul2(delta, x[i].get(v));
-        if (VEC > 1) *reinterpret_cast<float4*>(&sm.step[t][c + 2 * v]) = make_float4(delta.x, in.x, delta.y, in.y);
-        else sm.step[t][c] = make_float2(delta.x, in.x);
+      for (int v = 0; v < VEC; ++v) {
+        delta[v] = dt[i].get(v) + bias[at + v];
+        if (A.softplus) delta[v] = softplus(delta[v]);
+        if (!there) delta[v] = 0.f;
+        in[v] = delta[v] * x[i].get(v);
       }
+      float4* const to = &sm.step[token(i)][at / 2];
+      if (VEC == 1) {
+        float* const one = reinterpret_cast<float*>(to) + at % 2;
+        one[0] = delta[0];
+        one[2] = in[0];
+      }
+#pragma unroll
+      for (int v = 0; v + 1 < VEC; v += 2) to[v / 2] = make_float4(delta[v], delta[VEC > 1 ? v + 1 : 0], in[v], in[VEC > 1 ? v + 1 : 0]);
     }
 #pragma unroll
     for (int i = 0; i < S::bc; ++i) {
-      const int at = i * kScanThreads + threadIdx.x, t = at / (N / 2), n = at % (N / 2) * 2;
-      if (at < kScanTile * N / 2) {
-        *reinterpret_cast<float2*>(&sm.b[t][n]) = b[i].get(0);
-        if (Y) *reinterpret_cast<float2*>(&sm.c[Y ? t : 0][n]) = c[Y ? i : 0].get(0);
-      }
+      if (!bc_real(i)) continue;
+      *reinterpret_cast<float2*>(&sm.b[bc_token(i)][bc_state()]) = make_float2(b[i].get(0), b[i].get(1));
+      if (Y) *reinterpret_cast<float2*>(&sm.c[Y ? bc_token(i) : 0][bc_state()]) = make_float2(c[Y ? i : 0].get(0), c[Y ? i : 0].get(1));
     }
   }
 };
 
-// A lane's four states of two channels.
+// A lane's four states of two channels, side by side.
 struct ScanStates {
-  float2 v[kScanPair][2];
+  float2 v[4];
   __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-    for (int c = 0; c < kScanPair; ++c) v[c][0] = v[c][1] = both_of(x);
+    for (int n = 0; n < 4; ++n) v[n] = both_of(x);
   }
-  // channel d of `p`, [channel][N], and the next one where there is one
+  // channel d of `p`, [channel][N], from state q on, and the next one where there is one
   __device__ __forceinline__ void load(const float* p, long long d, int N, int q, bool both) {
-#pragma unroll
-    for (int c = 0; c < kScanPair; ++c) {
-      const float4 s = *reinterpret_cast<const float4*>(p + (d + (both ? c : 0)) * N + q);
-      v[c][0] = make_float2(s.x, s.y);
-      v[c][1] = make_float2(s.z, s.w);
-    }
+    const float4 x = *reinterpret_cast<const float4*>(p + d * N + q), y = *reinterpret_cast<const float4*>(p + (d + (both ? 1 : 0)) * N + q);
+    v[0] = make_float2(x.x, y.x);
+    v[1] = make_float2(x.y, y.y);
+    v[2] = make_float2(x.z, y.z);
+    v[3] = make_float2(x.w, y.w);
   }
   __device__ __forceinline__ void store(float* p, long long d, int N, int q, bool both) const {
-#pragma unroll
-    for (int c = 0; c < kScanPair; ++c)
-      if (c == 0 || both) *reinterpret_cast<float4*>(p + (d + c) * N + q) = make_float4(v[c][0].x, v[c][0].y, v[c][1].x, v[c][1].y);
+    *reinterpret_cast<float4*>(p + d * N + q) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+    if (both) *reinterpret_cast<float4*>(p + (d + 1) * N + q) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
   }
   __device__ __forceinline__ void times(float by) {
 #pragma unroll
-    for (int c = 0; c < kScanPair; ++c) v[c][0] = mul2(v[c][0], both_of(by)), v[c][1] = mul2(v[c][1], both_of(by));
+    for (int n = 0; n < 4; ++n) v[n] = mul2(v[n], both_of(by));
   }
 };
 
@@ -414,173 +440,210 @@ struct ScanSplit {
 };
 
 template <bool BF16, int N, int VEC, bool GATE>
-__global__ void __launch_bounds__(kScanThreads, SPEC_SCAN_CTAS) scan_tile_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
+__global__ void __launch_bounds__(2 * kScanThreads, SPEC_SCAN_CTAS) scan_tile_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
   using S = ScanShape<BF16, N, VEC>;
   using F = ScanFetch<BF16, N, VEC, true, GATE>;
+  using Shared = ScanShared<N, S::CH, true>;
   constexpr int L = S::L, CH = S::CH;
   extern __shared__ __align__(16) unsigned char raw[];
-  ScanShared<N, CH, true>& sm = *reinterpret_cast<ScanShared<N, CH, true>*>(raw);
+  Shared& sm = *reinterpret_cast<Shared*>(raw);
   const ScanPlace P = scan_place(A, CH);
   const MixerRow R = mixer_row(A, P.r, P.seg == 0 && P.d0 == 0 && threadIdx.x == 0);
   const int first = P.seg * W.span, stop = (int)min((long long)first + W.span, (long long)A.T), end = min(stop, R.len);
-  const int ch = threadIdx.x / L * kScanPair, lane = threadIdx.x % L, q = lane * 4, d = P.d0 + min(ch, P.left - 1);
-  const bool mine = ch < P.left, both = ch + 1 < P.left;
-  F in(A, P);
-  if (first < end) in.load(A, P, first, end, pairs);
-  ScanStates a, h;
-  a.load(A.a, d, N, q, both);
-  a.times(kLog2e);
-  h.fill(0.f);
-  if (W.segments > 1) h.load(W.states, (long long)(P.r * W.segments + P.seg) * A.D + d, N, q, both);
-  else if (R.from >= 0) h.load(A.state, (long long)R.from * A.D + d, N, q, both);
+  const int tiles = first < end ? (end - first + kScanTile - 1) / kScanTile : 0;
   const long long out = (long long)P.r * A.T * A.D + P.d0;
-  for (int t0 = first; t0 < end; t0 += kScanTile) {
-    in.put(A, P, t0, end, sm);
-    ScanVec<BF16, VEC> x[S::per], z[GATE ? S::per : 1];
-#pragma unroll
-    for (int i = 0; i < S::per; ++i) {
-      x[i] = in.x[i];
-      if (GATE) z[GATE ? i : 0] = in.z[GATE ? i : 0];
-    }
+  sm.fill(sm.bias, A.dt_bias, P);
+  sm.fill(sm.skip, A.skip, P);
+  if (threadIdx.x >= kScanThreads) {
+    // ------------------------------------------------------ the elements
+    F in(A, P);
+    if (tiles) in.load(A, P, first, end, pairs);
+    // of the tiles that are being walked (single elements would be too many, and are fetched again)
+    constexpr bool hold = VEC > 1;
+    ScanVec<BF16, VEC> x[2][hold ? S::per : 1], z[2][hold && GATE ? S::per : 1];
     __syncthreads();
-    if (t0 + kScanTile < end) in.load(A, P, t0 + kScanTile, end, pairs);
-    const ScanStates was = h;
-    ScanStates all;
-    all.fill(1.f);
-    float2 sum = make_float2(0.f, 0.f);
+    for (int k0 = 0; k0 < tiles + 2; k0 += 2)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + u;
+        if (k >= 2 && k - 2 < tiles) {
+          scan_wait<kScanWalked>(u);
+          const int t0 = first + (k - 2) * kScanTile;
+#pragma unroll
+          for (int i = 0; i < S::per; ++i) {
+            const int t = F::token(i), at = F::channel();
+            if (!F::real(i) || t >= end - t0 || at >= P.left) continue;
+            // the lanes' parts, of VEC channels at a time
+            float y[VEC], two[VEC];
+#pragma unroll
+            for (int m = 0; m < L; ++m) {
+              float e[VEC];
+              const float* const p = reinterpret_cast<const float*>(&sm.tile[u].part[t][m][0]) + at;
+              if (VEC > 1) *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(p);
+              else e[0] = p[0];
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) {
+                if (m % 2 == 0) two[v] = e[v];
+                else y[v] = m > 1 ? y[v] + (two[v] + e[v]) : two[v] + e[v];
+              }
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+              if (!hold) {
+                x[u][0].load(in.px + ((t0 + (long long)i * S::rows) * A.x_tok) * F::es);
+                if (GATE) z[u][0].load(in.pz + ((t0 + (long long)i * S::rows) * A.z_tok) * F::es);
+              }
+              y[v] = fmaf(sm.skip[at + v], x[u][hold ? i : 0].get(v), y[v]);
+              if (GATE) y[v] *= silu(z[u][hold && GATE ? i : 0].get(v));
+            }
+            const long long to = out + (long long)(t0 + t) * A.D + at;
+            constexpr int n1 = VEC > 1 ? 1 : 0, n2 = VEC > 1 ? 2 : 0, n3 = VEC > 1 ? 3 : 0;
+            if (VEC == 1) store_one<BF16>(A.y, to, y[0]);
+            else if (BF16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + to) = make_uint2(pack_bf16(y[0], y[n1]), pack_bf16(y[n2], y[n3]));
+            else *reinterpret_cast<float4*>(static_cast<float*>(A.y) + to) = make_float4(y[0], y[n1], y[n2], y[n3]);
+          }
+        }
+        if (k < tiles) {
+          const int t0 = first + k * kScanTile;
+          in.put(A, P, t0, end, sm.bias, sm.tile[u]);
+#pragma unroll
+          for (int i = 0; i < (hold ? S::per : 0); ++i) {
+            x[u][i] = in.x[i];
+            if (GATE) z[u][GATE ? i : 0] = in.z[GATE ? i : 0];
+          }
+          scan_tell<kScanMade>(u);
+          if (k + 1 < tiles) in.load(A, P, t0 + kScanTile, end, pairs);
+        }
+      }
+    for (long long i = (long long)max(first, R.len) * P.left + threadIdx.x % kScanThreads; i < (long long)stop * P.left; i += kScanThreads)
+      store_one<BF16>(A.y, out + i / P.left * A.D + i % P.left, 0.f);
+  } else {
+    // -------------------------------------------------------- the states
+    const int ch = threadIdx.x / L * kScanLane, lane = threadIdx.x % L, q = lane * 4, d = P.d0 + min(ch, P.left - 1);
+    const bool both = ch + 1 < P.left;      // (lanes without channels follow the last one)
+    ScanStates a, h;
+    a.load(A.a, d, N, q, both);
+    a.times(kLog2e);
+    h.fill(0.f);
+    if (W.segments > 1) h.load(W.states, (long long)(P.r * W.segments + P.seg) * A.D + d, N, q, both);
+    else if (R.from >= 0) h.load(A.state, (long long)R.from * A.D + d, N, q, both);
+    __syncthreads();
 #pragma unroll 1
-    for (int t = 0; t < kScanTile; t += 4) {
+    for (int k = 0; k < tiles; ++k) {
+      typename Shared::Tile& tile = sm.tile[k & 1];
+      scan_wait<kScanMade>(k & 1);
+      const ScanStates was = h;
+      ScanStates all;
+      all.fill(1.f);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int t = 0; t < kScanTile; t += kScanGroup) {
+        // (loads first, then the arithmetic of all tokens, then stores, which the compiler moves no load across)
+        float4 s[kScanGroup], b[kScanGroup], c[kScanGroup];
+        float2 y[kScanGroup];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 s = *reinterpret_cast<const float4*>(&sm.step[t + j][ch]);
-        const float4 b = *reinterpret_cast<const float4*>(&sm.b[t + j][q]), c = *reinterpret_cast<const float4*>(&sm.c[t + j][q]);
-        sum = add2(sum, make_float2(s.x, s.z));
-#pragma unroll
-        for (int k = 0; k < kScanPair; ++k) {
-          const float step = k ? s.z : s.x, in = k ? s.w : s.y;
-          const float2 w0 = make_float2(exp2_fast(step * a.v[k][0].x), exp2_fast(step * a.v[k][0].y));
-          const float2 w1 = make_float2(exp2_fast(step * a.v[k][1].x), exp2_fast(step * a.v[k][1].y));
-          all.v[k][0] = mul2(all.v[k][0], w0);
-          all.v[k][1] = mul2(all.v[k][1], w1);
-          h.v[k][0] = fma2(w0, h.v[k][0], make_float2(in * b.x, in * b.y));
-          h.v[k][1] = fma2(w1, h.v[k][1], make_float2(in * b.z, in * b.w));
-          const float2 y = fma2(make_float2(c.z, c.w), h.v[k][1], mul2(make_float2(c.x, c.y), h.v[k][0]));
-          sm.part[t + j][k][threadIdx.x] = y.x + y.y;
+        for (int j = 0; j < kScanGroup; ++j) {
+          s[j] = tile.step[t + j][ch / 2];
+          b[j] = *reinterpret_cast<const float4*>(&tile.b[t + j][q]);
+          c[j] = *reinterpret_cast<const float4*>(&tile.c[t + j][q]);
         }
+#pragma unroll
+        for (int j = 0; j < kScanGroup; ++j) {
+          const float bb[4] = {b[j].x, b[j].y, b[j].z, b[j].w}, cc[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+          const float2 step = make_float2(s[j].x, s[j].y), put = make_float2(s[j].z, s[j].w);
+          sum = add2(sum, step);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float2 e = mul2(step, a.v[n]), w = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            all.v[n] = mul2(all.v[n], w);
+            h.v[n] = fma2(w, h.v[n], mul2(put, both_of(bb[n])));
+            y[j] = n ? fma2(both_of(cc[n]), h.v[n], y[j]) : mul2(both_of(cc[n]), h.v[n]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kScanGroup; ++j) tile.part[t + j][lane][ch / 2] = y[j];
       }
-    }
+      scan_tell<kScanWalked>(k & 1);
 #pragma unroll
-    for (int k = 0; k < kScanPair; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 w = scan_decay(mul2(both_of(k ? sum.y : sum.x), a.v[k][j]));
+      for (int n = 0; n < 4; ++n) {
+        const float2 w = scan_decay(mul2(sum, a.v[n])), u = was.v[n];
         // (a state that is not finite stays what it has become)
-        const float2 s = make_float2(fabsf(was.v[k][j].x) < INFINITY ? was.v[k][j].x : 0.f, fabsf(was.v[k][j].y) < INFINITY ? was.v[k][j].y : 0.f);
-        h.v[k][j] = fma2(add2(w, make_float2(-all.v[k][j].x, -all.v[k][j].y)), s, h.v[k][j]);
+        const float2 s = make_float2(fabsf(u.x) < INFINITY ? u.x : 0.f, fabsf(u.y) < INFINITY ? u.y : 0.f);
+        h.v[n] = fma2(add2(w, make_float2(-all.v[n].x, -all.v[n].y)), s, h.v[n]);
       }
-    __syncthreads();
-    const bool every = in.whole && t0 + kScanTile <= end;
-#pragma unroll
-    for (int i = 0; i < S::per; ++i) {
-      const int t = F::token(i), c = F::channel();
-      if (!F::real(i) || !(every || (t0 + t < end && c < P.left))) continue;
-      float2 y[(VEC + 1) / 2];
-#pragma unroll
-      for (int v = 0; v < (VEC + 1) / 2; ++v) {
-        float2 skip = make_float2(0.f, 0.f);
-        y[v] = make_float2(0.f, 0.f);
-        // the parts of a channel's lanes
-        const float* p = &sm.part[t][VEC > 1 ? 0 : c & 1][(c / 2 + v) * L];
-        if (L == 2) {
-          const float2 e = *reinterpret_cast<const float2*>(p);
-          y[v].x = e.x + e.y;
-          if (VEC > 1) {
-            const float2 o = *reinterpret_cast<const float2*>(p + kScanThreads);
-            y[v].y = o.x + o.y;
-          }
-        } else {
-#pragma unroll
-          for (int m = 0; m < L / 4; ++m) {
-            const float4 e = *reinterpret_cast<const float4*>(p + 4 * m);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (VEC > 1) o = *reinterpret_cast<const float4*>(p + kScanThreads + 4 * m);
-            y[v] = add2(y[v], add2(add2(make_float2(e.x, o.x), make_float2(e.y, o.y)), add2(make_float2(e.z, o.z), make_float2(e.w, o.w))));
-          }
-        }
-        if (A.skip) {
-          if (VEC > 1) skip = __ldg(reinterpret_cast<const float2*>(A.skip + P.d0 + c) + v);
-          else skip.x = __ldg(A.skip + P.d0 + c);
-        }
-        y[v] = fma2(skip, x[i].get(v), y[v]);
-        if (GATE) {
-          const float2 g = z[GATE ? i : 0].get(v);
-          y[v] = mul2(y[v], make_float2(silu(g.x), VEC > 1 ? silu(g.y) : 0.f));
-        }
-      }
-      const long long to = out + (long long)(t0 + t) * A.D + c;
-      constexpr int last = (VEC + 1) / 2 - 1;
-      if (VEC == 1) store_one<BF16>(A.y, to, y[0].x);
-      else if (BF16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + to) = make_uint2(pack_bf16(y[0].x, y[0].y), pack_bf16(y[last].x, y[last].y));
-      else *reinterpret_cast<float4*>(static_cast<float*>(A.y) + to) = make_float4(y[0].x, y[0].y, y[last].x, y[last].y);
     }
+    // the segment of the last token has the last state
+    if (ch < P.left && R.to >= 0 && (W.segments == 1 || (R.len > 0 ? first < R.len && R.len <= stop : P.seg == 0)))
+      h.store(A.last, (long long)R.to * A.D + d, N, q, both);
   }
-  for (long long i = (long long)max(first, R.len) * P.left + threadIdx.x; i < (long long)stop * P.left; i += kScanThreads)
-    store_one<BF16>(A.y, out + i / P.left * A.D + i % P.left, 0.f);
-  // the segment of the last token has the last state
-  if (mine && R.to >= 0 && (W.segments == 1 || (R.len > 0 ? first < R.len && R.len <= stop : P.seg == 0)))
-    h.store(A.last, (long long)R.to * A.D + d, N, q, both);
 }
 
 // The state behind a segment that begins with zeros, from its last token to the first:
 // sum_t exp(a (delta of the tokens after t)) delta_t x_t b_t.  Each weight is taken by
 // itself, so nothing adds up.
 template <bool BF16, int N, int VEC>
-__global__ void __launch_bounds__(kScanThreads) scan_segment_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
+__global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
   using S = ScanShape<BF16, N, VEC>;
+  using Shared = ScanShared<N, S::CH, false>;
   constexpr int L = S::L, CH = S::CH;
   extern __shared__ __align__(16) unsigned char raw[];
-  ScanShared<N, CH, false>& sm = *reinterpret_cast<ScanShared<N, CH, false>*>(raw);
+  Shared& sm = *reinterpret_cast<Shared*>(raw);
   const ScanPlace P = scan_place(A, CH);
   const MixerRow R = mixer_row(A, P.r, false);
   const int first = P.seg * W.span, end = min((int)min((long long)first + W.span, (long long)A.T), R.len);
-  const int ch = threadIdx.x / L * kScanPair, lane = threadIdx.x % L, q = lane * 4, d = P.d0 + min(ch, P.left - 1);
-  const bool both = ch + 1 < P.left;
-  ScanFetch<BF16, N, VEC, false, false> in(A, P);
   const int tiles = first < end ? (end - first + kScanTile - 1) / kScanTile : 0;
-  if (tiles) in.load(A, P, first + (tiles - 1) * kScanTile, end, pairs);
-  ScanStates a, h;
-  a.load(A.a, d, N, q, both);
-  a.times(kLog2e);
-  h.fill(0.f);
-  float2 behind = make_float2(0.f, 0.f);                  // the delta of the tiles behind this one
-  for (int k = tiles - 1; k >= 0; --k) {
-    const int t0 = first + k * kScanTile;
-    if (k < tiles - 1) __syncthreads();
-    in.put(A, P, t0, end, sm);
+  sm.fill(sm.bias, A.dt_bias, P);
+  if (threadIdx.x >= kScanThreads) {
+    ScanFetch<BF16, N, VEC, false, false> in(A, P);
+    if (tiles) in.load(A, P, first + (tiles - 1) * kScanTile, end, pairs);
     __syncthreads();
-    if (k) in.load(A, P, t0 - kScanTile, end, pairs);
-    float2 here = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int t = kScanTile - 1; t >= 0; --t) {
-      const float4 s = *reinterpret_cast<const float4*>(&sm.step[t][ch]);
-      const float4 b = *reinterpret_cast<const float4*>(&sm.b[t][q]);
-      const float2 after = add2(behind, here);
-#pragma unroll
-      for (int c = 0; c < kScanPair; ++c) {
-        const float far = c ? after.y : after.x, in = c ? s.w : s.y;
-        h.v[c][0] = fma2(make_float2(exp2_fast(far * a.v[c][0].x), exp2_fast(far * a.v[c][0].y)), make_float2(in * b.x, in * b.y), h.v[c][0]);
-        h.v[c][1] = fma2(make_float2(exp2_fast(far * a.v[c][1].x), exp2_fast(far * a.v[c][1].y)), make_float2(in * b.z, in * b.w), h.v[c][1]);
-      }
-      here = add2(here, make_float2(s.x, s.z));
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+      const int t0 = first + (tiles - 1 - k) * kScanTile;
+      if (k >= 2) scan_wait<kScanWalked>(k & 1);
+      in.put(A, P, t0, end, sm.bias, sm.tile[k & 1]);
+      scan_tell<kScanMade>(k & 1);
+      if (k + 1 < tiles) in.load(A, P, t0 - kScanTile, end, pairs);
     }
-    behind = add2(behind, here);
-  }
-  if (ch < P.left) {
-    const long long at = (long long)(P.r * W.segments + P.seg) * A.D + d;
-    h.store(W.states, at, N, q, both);
-    if (lane == 0) {
-      W.sums[at] = behind.x;
-      if (both) W.sums[at + 1] = behind.y;
+    // (what is told is also waited for)
+    if (tiles >= 2) scan_wait<kScanWalked>(tiles & 1);
+    if (tiles >= 1) scan_wait<kScanWalked>((tiles - 1) & 1);
+  } else {
+    const int ch = threadIdx.x / L * kScanLane, lane = threadIdx.x % L, q = lane * 4, d = P.d0 + min(ch, P.left - 1);
+    const bool both = ch + 1 < P.left;
+    ScanStates a, h;
+    a.load(A.a, d, N, q, both);
+    a.times(kLog2e);
+    h.fill(0.f);
+    float2 behind = make_float2(0.f, 0.f);           // the delta of the tiles behind this one
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+      const typename Shared::Tile& tile = sm.tile[k & 1];
+      scan_wait<kScanMade>(k & 1);
+      float2 here = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int t = kScanTile - 1; t >= 0; --t) {
+        const float4 b = *reinterpret_cast<const float4*>(&tile.b[t][q]), s = tile.step[t][ch / 2];
+        const float bb[4] = {b.x, b.y, b.z, b.w};
+        const float2 far = add2(behind, here), put = make_float2(s.z, s.w);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float2 e = mul2(far, a.v[n]);
+          h.v[n] = fma2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), mul2(put, both_of(bb[n])), h.v[n]);
+        }
+        here = add2(here, make_float2(s.x, s.y));
+      }
+      scan_tell<kScanWalked>(k & 1);
+      behind = add2(behind, here);
+    }
+    if (ch < P.left) {
+      const long long at = (long long)(P.r * W.segments + P.seg) * A.D + d;
+      h.store(W.states, at, N, q, both);
+      if (lane == 0) {
+        W.sums[at] = behind.x;
+        if (both) W.sums[at + 1] = behind.y;
+      }
     }
   }
 }
@@ -597,7 +660,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
   const float2 a[2] = {mul2(make_float2(av.x, av.y), both_of(kLog2e)), mul2(make_float2(av.z, av.w), both_of(kLog2e))};
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (R.from >= 0) h = *reinterpret_cast<const float4*>(A.state + ((long long)R.from * A.D + d) * N + q);
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < W.segments; ++s) {
     const long long at = (long long)(r * W.segments + s) * A.D + d;
     float4* const p = reinterpret_cast<float4*>(W.states + at * N + q);
@@ -611,11 +674,11 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
 
 constexpr int kScanStepTokens = 16;    // up to so many are walked by scan_step_kernel
 #ifndef SPEC_SCAN_FILL
-#define SPEC_SCAN_FILL 600
+#define SPEC_SCAN_FILL 300
 #endif
 
 static int scan_blocks(int D, int each, int N) {
-  const int ch = kScanThreads / (N / 4) * kScanPair;
+  const int ch = kScanThreads / (N / 4) * kScanLane;
   return (each + ch - 1) / ch * (D / each);
 }
 
@@ -645,14 +708,16 @@ static int launch_tiles(const ScanArgs& A, bool pairs, char* workspace, cudaStre
   constexpr int smem = sizeof(ScanShared<N, S::CH, true>), less = sizeof(ScanShared<N, S::CH, false>);
   const dim3 grid((unsigned)blocks * W.segments, A.B);
   if (W.segments > 1) {
-    scan_segment_kernel<BF16, N, VEC><<<grid, kScanThreads, less, st>>>(A, W, pairs);
+    static std::atomic<unsigned long long> allowed;
+    if (!allow_shared(reinterpret_cast<const void*>(scan_segment_kernel<BF16, N, VEC>), less, &allowed)) return SPEC_E_CUDA;
+    scan_segment_kernel<BF16, N, VEC><<<grid, 2 * kScanThreads, less, st>>>(A, W, pairs);
     const dim3 joins((unsigned)(((long long)A.D * S::L + kScanThreads - 1) / kScanThreads), A.B);
     scan_join_kernel<N><<<joins, kScanThreads, 0, st>>>(A, W);
   }
   static std::atomic<unsigned long long> allowed[2];
   const auto gated = scan_tile_kernel<BF16, N, VEC, true>, plain = scan_tile_kernel<BF16, N, VEC, false>;
   if (!allow_shared(reinterpret_cast<const void*>(A.z ? gated : plain), smem, &allowed[A.z != nullptr])) return SPEC_E_CUDA;
-  (A.z ? gated : plain)<<<grid, kScanThreads, smem, st>>>(A, W, pairs);
+  (A.z ? gated : plain)<<<grid, 2 * kScanThreads, smem, st>>>(A, W, pairs);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
@@ -663,7 +728,7 @@ static int launch_scan(const ScanArgs& A, bool wide, void* workspace, cudaStream
     // four channels, and pairs of states, by one access where they are aligned
     const bool four = A.each % 4 == 0 && (A.x_row | A.x_tok | A.dt_row | A.dt_tok | A.z_row | A.z_tok) % 4 == 0 &&
                       paged_aligned(A.x, 4 * es) && paged_aligned(A.dt, 4 * es) && paged_aligned(A.z, 4 * es) &&
-                      paged_aligned(A.y, 4 * es) && paged_aligned(A.skip, 8) && paged_aligned(A.dt_bias, 8);
+                      paged_aligned(A.y, 4 * es);
     const bool pairs = (A.b_row | A.b_tok | A.b_group | A.c_row | A.c_tok | A.c_group) % 2 == 0 && paged_aligned(A.b, 2 * es) &&
                        paged_aligned(A.c, 2 * es);
     char* const ws = static_cast<char*>(workspace);
