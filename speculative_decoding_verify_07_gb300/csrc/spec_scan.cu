@@ -211,16 +211,11 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanA
 // the tokens that a state remembers.  So the tile's decays are also multiplied, and at its end
 // the state that entered gets the difference to the exact decay of the tile's sum of delta.
 
-#ifndef SPEC_SCAN_CTAS
-#define SPEC_SCAN_CTAS 2
-#endif
-#ifndef SPEC_SCAN_GROUP
-#define SPEC_SCAN_GROUP 4
-#endif
 constexpr int kScanThreads = 128;      // of each half
 constexpr int kScanLane = 2;           // channels of a lane
 constexpr int kScanTile = 16;          // tokens of a tile
-constexpr int kScanGroup = SPEC_SCAN_GROUP;          // tokens that a lane takes together
+constexpr int kScanGroup = 8;          // tokens that a lane takes together
+constexpr int kScanCtas = 2;           // an SM
 
 template <bool BF16, int N, int VEC>
 struct ScanShape {
@@ -430,17 +425,19 @@ struct ScanStates {
   }
 };
 
-// Workspace of a call whose tokens are split: each segment's sum of delta by (row, segment, channel), then by (row,
-// segment, channel, state) the state behind the segment if it began with zeros, which scan_join_kernel turns into
-// the state that enters it.
+// A row's tokens where they are split into segments, and the workspace of such a call: each part's sum of delta by (row,
+// part, channel), then by (row, part, channel, state) the state behind the part if it began with zeros, which
+// scan_join_kernel turns into the state that enters it.  A segment has `fine` parts: scan_segment_kernel has fewer
+// registers and takes more CTAs an SM.
 struct ScanSplit {
-  int segments, span;                  // tokens of a segment
+  int segments, span, fine;            // span: tokens of a segment
   float* sums;
   float* states;
 };
+constexpr int kScanFine = 4, kScanLeast = 128;      // at most; no part is of fewer tokens
 
 template <bool BF16, int N, int VEC, bool GATE>
-__global__ void __launch_bounds__(2 * kScanThreads, SPEC_SCAN_CTAS) scan_tile_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
+__global__ void __launch_bounds__(2 * kScanThreads, kScanCtas) scan_tile_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
   using S = ScanShape<BF16, N, VEC>;
   using F = ScanFetch<BF16, N, VEC, true, GATE>;
   using Shared = ScanShared<N, S::CH, true>;
@@ -487,12 +484,12 @@ __global__ void __launch_bounds__(2 * kScanThreads, SPEC_SCAN_CTAS) scan_tile_ke
                 else y[v] = m > 1 ? y[v] + (two[v] + e[v]) : two[v] + e[v];
               }
             }
+            if (!hold) {
+              x[u][0].load(in.px + (t0 + (long long)i * S::rows) * A.x_tok * F::es);
+              if (GATE) z[u][0].load(in.pz + (t0 + (long long)i * S::rows) * A.z_tok * F::es);
+            }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-              if (!hold) {
-                x[u][0].load(in.px + ((t0 + (long long)i * S::rows) * A.x_tok) * F::es);
-                if (GATE) z[u][0].load(in.pz + ((t0 + (long long)i * S::rows) * A.z_tok) * F::es);
-              }
               y[v] = fmaf(sm.skip[at + v], x[u][hold ? i : 0].get(v), y[v]);
               if (GATE) y[v] *= silu(z[u][hold && GATE ? i : 0].get(v));
             }
@@ -525,7 +522,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, SPEC_SCAN_CTAS) scan_tile_ke
     a.load(A.a, d, N, q, both);
     a.times(kLog2e);
     h.fill(0.f);
-    if (W.segments > 1) h.load(W.states, (long long)(P.r * W.segments + P.seg) * A.D + d, N, q, both);
+    if (W.segments > 1) h.load(W.states, ((long long)P.r * W.segments + P.seg) * W.fine * A.D + d, N, q, both);
     else if (R.from >= 0) h.load(A.state, (long long)R.from * A.D + d, N, q, both);
     __syncthreads();
 #pragma unroll 1
@@ -590,7 +587,7 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const ScanPlace P = scan_place(A, CH);
   const MixerRow R = mixer_row(A, P.r, false);
-  const int first = P.seg * W.span, end = min((int)min((long long)first + W.span, (long long)A.T), R.len);
+  const int span = W.span / W.fine, first = P.seg * span, end = min((int)min((long long)first + span, (long long)A.T), R.len);
   const int tiles = first < end ? (end - first + kScanTile - 1) / kScanTile : 0;
   sm.fill(sm.bias, A.dt_bias, P);
   if (threadIdx.x >= kScanThreads) {
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
       behind = add2(behind, here);
     }
     if (ch < P.left) {
-      const long long at = (long long)(P.r * W.segments + P.seg) * A.D + d;
+      const long long at = ((long long)P.r * W.segments * W.fine + P.seg) * A.D + d;
       h.store(W.states, at, N, q, both);
       if (lane == 0) {
         W.sums[at] = behind.x;
@@ -648,7 +645,7 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
   }
 }
 
-// Walks the segments of four states: what is behind one enters the next.
+// Walks the parts of four states: what is behind one enters the next.
 template <int N>
 __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs A, const ScanSplit W) {
   constexpr int L = N / 4;
@@ -661,8 +658,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (R.from >= 0) h = *reinterpret_cast<const float4*>(A.state + ((long long)R.from * A.D + d) * N + q);
 #pragma unroll 8
-  for (int s = 0; s < W.segments; ++s) {
-    const long long at = (long long)(r * W.segments + s) * A.D + d;
+  for (int s = 0; s < W.segments * W.fine; ++s) {
+    const long long at = ((long long)r * W.segments * W.fine + s) * A.D + d;
     float4* const p = reinterpret_cast<float4*>(W.states + at * N + q);
     const float4 put = *p;
     const float sum = W.sums[at];
@@ -673,44 +670,47 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
 }
 
 constexpr int kScanStepTokens = 16;    // up to so many are walked by scan_step_kernel
-#ifndef SPEC_SCAN_FILL
-#define SPEC_SCAN_FILL 300
-#endif
 
 static int scan_blocks(int D, int each, int N) {
   const int ch = kScanThreads / (N / 4) * kScanLane;
   return (each + ch - 1) / ch * (D / each);
 }
 
-// Into how many segments a row's tokens are split, so that there are CTAs for all SMs.
-static int scan_segments(int B, int T, int D, int each, int N) {
+// A row's segments: one where there are CTAs for most SMs, otherwise as many as fill all of them once.  The first pass
+// makes a split cost half as much again: 64 CTAs of 4096 tokens take 184 us in four segments, 247 in one, and a row of 512
+// tokens 37 and 34; 256 CTAs of 2048 tokens took 220 us whole and 300 and more in two.
+static ScanSplit scan_split(int B, int T, int D, int each, int N) {
   const long long ctas = (long long)scan_blocks(D, each, N) * B;
-  const long long want = ctas >= SPEC_SCAN_FILL / 2 ? 1 : (SPEC_SCAN_FILL + ctas - 1) / ctas;
-  return (int)std::max(1ll, std::min(want, (long long)T / 128));
+  const long long want = ctas >= 100 ? 1 : std::max(1ll, 152 * kScanCtas / ctas);
+  ScanSplit W = {};
+  W.segments = (int)std::max(1ll, std::min(want, (long long)T / kScanLeast));
+  W.fine = W.segments > 1 ? std::max(1, std::min(kScanFine, T / W.segments / kScanLeast)) : 1;
+  const int unit = kScanTile * W.fine;
+  W.span = (int)(((long long)T + (long long)W.segments * unit - 1) / ((long long)W.segments * unit) * unit);
+  W.segments = (int)(((long long)T + W.span - 1) / W.span);
+  return W;
 }
 
-// (the most segments that a call of these sizes may have, whatever its groups: one group has the fewest CTAs)
+// (the most parts that a call of these sizes may have, whatever its groups: one group has the fewest CTAs)
 static size_t scan_split_bytes(int B, int T, int D, int N) {
-  const size_t n = scan_segments(B, T, D, D, N);
-  return n > 1 ? (n * B * D * 4 + 255) / 256 * 256 + n * B * D * N * 4 : 0;
+  const ScanSplit W = scan_split(B, std::max(T, 1), D, D, N);
+  const size_t n = W.segments > 1 ? (size_t)W.segments * W.fine : 0;
+  return (n * B * D * 4 + 255) / 256 * 256 + n * B * D * N * 4;
 }
 
 template <bool BF16, int N, int VEC>
 static int launch_tiles(const ScanArgs& A, bool pairs, char* workspace, cudaStream_t st) {
   using S = ScanShape<BF16, N, VEC>;
   const int blocks = scan_blocks(A.D, A.each, N);
-  ScanSplit W;
-  W.segments = scan_segments(A.B, A.T, A.D, A.each, N);
-  W.span = ((A.T + W.segments - 1) / W.segments + kScanTile - 1) / kScanTile * kScanTile;
-  W.segments = (A.T + W.span - 1) / W.span;
+  ScanSplit W = scan_split(A.B, A.T, A.D, A.each, N);
   W.sums = reinterpret_cast<float*>(workspace);
-  W.states = reinterpret_cast<float*>(workspace + ((size_t)W.segments * A.B * A.D * 4 + 255) / 256 * 256);
+  W.states = reinterpret_cast<float*>(workspace + ((size_t)W.segments * W.fine * A.B * A.D * 4 + 255) / 256 * 256);
   constexpr int smem = sizeof(ScanShared<N, S::CH, true>), less = sizeof(ScanShared<N, S::CH, false>);
   const dim3 grid((unsigned)blocks * W.segments, A.B);
   if (W.segments > 1) {
     static std::atomic<unsigned long long> allowed;
     if (!allow_shared(reinterpret_cast<const void*>(scan_segment_kernel<BF16, N, VEC>), less, &allowed)) return SPEC_E_CUDA;
-    scan_segment_kernel<BF16, N, VEC><<<grid, 2 * kScanThreads, less, st>>>(A, W, pairs);
+    scan_segment_kernel<BF16, N, VEC><<<dim3(grid.x * W.fine, A.B), 2 * kScanThreads, less, st>>>(A, W, pairs);
     const dim3 joins((unsigned)(((long long)A.D * S::L + kScanThreads - 1) / kScanThreads), A.B);
     scan_join_kernel<N><<<joins, kScanThreads, 0, st>>>(A, W);
   }
