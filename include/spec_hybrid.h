@@ -155,8 +155,8 @@ int spec_scan(const spec_scan_t* scan, void* workspace, size_t workspace_bytes, 
 size_t spec_attend_shared_workspace_size(int N, int B, int heads, int group, int head_dim);
 
 /* spec_attend_shared - spec_attend for rows that have their first positions in
- * common, as samples of one prompt have: the same results, but what is shared is
- * read once for all of a group's rows.
+ * common, as samples of one prompt have: the same definition, within the same
+ * roundings, but what is shared is read once for all of a group's rows.
  *   shared_rows  [groups + 1] int32, not decreasing, within [0, B]: group g are rows
  *                shared_rows[g] .. shared_rows[g+1]-1.  Rows of no group, and all
  *                rows where shared_rows is out of order, share nothing.

@@ -39,6 +39,7 @@ static size_t attend_parts(int D) { return (size_t)152 * 2 * 256 * (D + 2) * siz
 int attend_check(const uint16_t* q, int64_t token_stride, int N, int group, float scale, int max_tokens, const spec_cache_t* cache,
                  uint16_t* out, float* lse, uint32_t* flags, void* workspace, AttendArgs* args, bool* done) {
   AttendArgs& A = *args;
+  A = {};
   *done = false;
   const int rc = paged_check(cache, N, &A.C);
   if (rc != SPEC_OK) return rc;
@@ -65,20 +66,26 @@ int attend_check(const uint16_t* q, int64_t token_stride, int N, int group, floa
   A.scale_log2 = scale * 1.4426950408889634f;
   A.joined = static_cast<unsigned*>(workspace);
   A.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttendCounters);
-  A.group_row = A.own_from = nullptr;
-  A.common = A.common_lse = nullptr;
   return SPEC_OK;
 }
 
-template <int PART>
-int attend_launch(AttendArgs& A, bool e4m3, long long rows, cudaStream_t st) {
+bool attend_is_wide(bool e4m3, long long rows) {
   // A tile of 16 or 32 query rows at a time, or of 128 or 256.  The few-rows kernel reads the cache again for every
   // 32 rows, the other fills its tile with padding.  In 16 bits 32x5 tokens of group 8 (40 rows) at 8000 take 139 us with
   // many rows, with few 231.  In 8 bits, where the other kernel widens the codes first, neither wins throughout from 33
   // to 64 rows: few rows take 89 us and many 123 with one row of 9 tokens (group 4, one head) at 60000, 47.5 and 58 with
   // 67 ragged ones over 800, 351 and 407 with 32x5 at 8000 in pages of one token; but 220 and 173 with these in pages
   // of 16, and 305 and 206 with 64x8 at 4000.  Up to 32 rows few do (64x4 of group 8 239 us, 328).
-  const bool wide = rows > (e4m3 ? 64 : 32);
+  return rows > (e4m3 ? 64 : 32);
+}
+
+int attend_tile_rows(bool e4m3, long long rows) {
+  return attend_is_wide(e4m3, rows) ? (rows <= 128 ? 128 : 256) : (rows <= 16 ? 16 : 32);
+}
+
+template <int PART>
+int attend_launch(AttendArgs& A, bool e4m3, long long rows, cudaStream_t st) {
+  const bool wide = attend_is_wide(e4m3, rows);
   // the longest run of positions that never leaves a page, up to what is copied at a time
   const int most = wide ? 128 : e4m3 ? 32 : 16;
   A.box = 1;

@@ -36,10 +36,21 @@ struct AttendArgs {
   // batch's rows group_row[g] .. group_row[g + 1] - 1, and the first one's page table is read
   const int32_t* group_row;
   const int32_t* own_from;   // kOwn: the first position of each row that is not common (a multiple of kCommonTile)
-  // The results over the common positions: by (token, head), with the logarithm to base 2 of the sum of weights
+  // The results over the common positions by (token, head), each divided by its sum of weights and with the logarithm to
+  // base 2 of that.  An item that several CTAs have parts of is in those until they are joined: common_items tells by
+  // (head, query tile), those of all groups side by side, the first and the last of these CTAs, or -1.
   float* common;
   float* common_lse;
+  float* common_parts;
+  int2* common_items;
+  int common_rows;           // query rows of a tile
+  long long common_tiles;    // query tiles of a head, all groups'
 };
+
+// Where the query tiles of group g, whose tokens begin at `first`, begin among all.  (A group's last tile may be begun
+// alone: one more for each group.)
+__device__ __forceinline__ long long common_tile(const AttendArgs& A, int g, int first) { return (long long)first * A.group / A.common_rows + g; }
+
 
 // 8-bit cache: values under a larger exponent byte are taken for NaN, by either kernel.
 constexpr unsigned kAttendTop = 221;
@@ -103,6 +114,11 @@ __device__ __forceinline__ AttendJoin attend_join(float own, float common) {
   const float a = exp2_fast(own - ref), b = exp2_fast(common - ref), sum = a + b, by = sum == 0.f ? 0.f : 1.f / sum;
   return {a * by, b * by, sum == 0.f ? -INFINITY : top + log2f(sum)};
 }
+
+// The next launch of the stream may begin before this one ends, if it was made so; what it reads of this one's results
+// waits for its end.
+__device__ __forceinline__ void launch_may_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void launch_before_is_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // a / group, for a >= 0.  (The compiler's division is several times as long, and a
 // kernel of several roles is short of instruction cache.)
@@ -308,6 +324,26 @@ template <int PART>
 int launch_attend_rows(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
 template <int PART>
 int launch_attend_wide(const AttendArgs& A, bool e4m3, int rows, const CUtensorMap* maps, cudaStream_t st);
+
+// A launch that may begin before the last one of the stream has ended (see launch_may_follow).
+template <class Kernel, class... Args>
+inline int launch_early(Kernel kernel, unsigned ctas, int threads, int smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(ctas);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = st;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
+}
+
+// Whether items of up to `rows` query rows go to the many-rows kernel, and the query rows of a tile.
+bool attend_is_wide(bool e4m3, long long rows);
+int attend_tile_rows(bool e4m3, long long rows);
 
 // Either of them, for items of up to `rows` query rows.
 template <int PART>

@@ -37,6 +37,7 @@ namespace specv {
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr float kRowsSlack = 8.f;
+constexpr int kOwnWhole = 16;        // a row's own positions: items of so few tiles stay in one CTA (64x3 tokens, 500 on average: 11 us less)
 constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
 static_assert(254 - (int)kAttendTop - kRowsShift >= 1, "so 2^-e of the largest scale is a normal number");
 constexpr unsigned kRowsLow = 64, kRowsHigh = 144;   // the ordinary range: within 2^80 a weight of 2^-46 stays a normal number
@@ -168,7 +169,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     for (int i = 0; i < kRowsWarps * S::stages; ++i) mbar_init(&full[0][0] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  attend_share<M, KT, kRowsThreads, 0, PART>(A, &share, sums);
+  if (PART == kCommon) launch_may_follow();
+  attend_share<M, KT, kRowsThreads, PART == kOwn ? kOwnWhole : 0, PART>(A, &share, sums);
 
   RowsFetch<M, NK, E4M3, PART> F(A, share);
   F.look(warp, lane);
@@ -635,7 +637,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     const int item = W.item_begin();
     int c0 = 0, c1 = 0;
     if (!whole) share_parts(share, item, W.tiles, &c0, &c1);
-    if (!whole) {
+    if (PART == kCommon && threadIdx.x == 0 && W.a == 0)
+      __stcg(A.common_items + W.head * A.common_tiles + common_tile(A, W.row, W.R.first) + W.qt, whole ? make_int2(-1, -1) : make_int2(c0, c1));
+    if (PART != kCommon && !whole) {
       float* part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       for (int i = threadIdx.x; i < M * D / 4; i += kRowsThreads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
@@ -663,10 +667,11 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     }
     // The parts' maxima first, then what they add up to: no part's loads wait for the part before.
     constexpr int ways = kRowsThreads / M;
-    if (whole ? threadIdx.x < M : last_part) {
+    const bool here = whole || PART == kCommon;      // this segment's result is what is written
+    if (here ? threadIdx.x < M : last_part) {
       const int row = threadIdx.x % M;
       float top = -INFINITY;
-      if (whole) {
+      if (here) {
 #pragma unroll
         for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w][row]);
       } else {
@@ -677,11 +682,12 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
       tops[threadIdx.x / M][row] = top;
     }
     __syncthreads();
-    if (whole || last_part) {
+    if (PART == kOwn) launch_before_is_done();
+    if (here || last_part) {
       for (int i = threadIdx.x; i < rows * (D / 8); i += kRowsThreads) {
         const int row = i / (D / 8), d = i % (D / 8) * 8;
         float x[8], top = tops[0][row], sum = 0.f;
-        if (whole) {
+        if (here) {
 #pragma unroll
           for (int w = 0; w < kRowsWarps; ++w) sum += times_exp2(sm_l[w][row], top == -INFINITY ? 0.f : sm_m[w][row] - top);
 #pragma unroll
@@ -717,14 +723,16 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
           float lse = sum == 0.f ? -INFINITY : top + log2f(sum) + (E4M3 ? kRowsShift : 0);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= by;
-          float4* const common = reinterpret_cast<float4*>(A.common + at * D + d);
           if (PART == kCommon) {
-            __stcg(common, make_float4(x[0], x[1], x[2], x[3]));
-            __stcg(common + 1, make_float4(x[4], x[5], x[6], x[7]));
-            if (d == 0) __stcg(A.common_lse + at, lse);
+            float* const part = A.common_parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * (M * (D + 1));
+            float4* const to = reinterpret_cast<float4*>(whole ? A.common + at * D + d : part + row * D + d);
+            __stcg(to, make_float4(x[0], x[1], x[2], x[3]));
+            __stcg(to + 1, make_float4(x[4], x[5], x[6], x[7]));
+            if (d == 0) __stcg(whole ? A.common_lse + at : part + M * D + row, lse);
           } else {
             if (W.first() > 0) {
               const AttendJoin J = attend_join(lse, __ldcg(A.common_lse + at));
+              const float4* const common = reinterpret_cast<const float4*>(A.common + at * D + d);
               const float4 a = __ldcg(common), b = __ldcg(common + 1);
               const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -741,6 +749,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     if (threadIdx.x == 0 && failed) attend_flag<PART>(A, W.row, SPEC_F_TIMEOUT);
     __syncthreads();
   }
+  if (PART == kOwn) launch_before_is_done();
   mbar_settle(&failed);
 }
 
@@ -751,6 +760,7 @@ static int launch_rows(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
   const auto kernel = attend_rows_kernel<D, E4M3, MT, PART>;
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
+  if (PART == kOwn) return launch_early(kernel, S::ctas * 152, kRowsThreads, S::smem, st, A, maps[0], maps[1]);
   kernel<<<S::ctas * 152, kRowsThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }

@@ -139,11 +139,11 @@ __device__ __forceinline__ uint32_t e4m3_bf16(uint32_t high, uint32_t scale) {
 constexpr uint32_t kWideExp = 134;     // the largest exponent byte whose scale, times 2^120, is a bf16 number
 
 // 32 columns of a row's own result, times `by`, with the common positions' where `join`.
-__device__ __forceinline__ void store_joined(uint16_t* out, const float* o, float by, const float4* common, float times, bool join) {
+__device__ __forceinline__ void store_joined(uint16_t* out, const float* o, float by, const float* common, float times, bool join) {
 #pragma unroll
   for (int i = 0; i < 32; i += 8) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (join) a = __ldcg(common + i / 4), b = __ldcg(common + i / 4 + 1);
+    if (join) a = __ldcg(reinterpret_cast<const float4*>(common + i)), b = __ldcg(reinterpret_cast<const float4*>(common + i + 4));
     const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float x[8];
 #pragma unroll
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tmem_before();
   }
+  if (PART == kCommon) launch_may_follow();
   attend_share<M, KT, kWideThreads, kWideWhole, PART>(A, &share, reinterpret_cast<long long*>(base));   // (shared memory is free yet)
   fence_proxy_async();
   tmem_after();
@@ -628,12 +629,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float* const part = A.parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * S::part_floats;
       const long long out_row = (long long)(R.first + token) * A.hq + head;
       const float inv = l == 0.f ? 1.f : 1.f / l;
-      // the common positions' share of the result, for a row's own
+      const bool join = PART == kOwn && item_first > 0;
       AttendJoin J = {1.f, 0.f, 0.f};
-      const bool join = PART == kOwn && item_first > 0 && real;
-      if (PART != kAll) {
-        J.lse = l == 0.f ? -INFINITY : m + log2f(l);
-        if (join && whole) J = attend_join(J.lse, __ldcg(A.common_lse + out_row));
+      float* to = nullptr;
+      if (PART != kAll) J.lse = l == 0.f ? -INFINITY : m + log2f(l);
+      if (PART == kCommon) {
+        float* const mine_part = A.common_parts + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0)) * (M * (D + 1));
+        const int local = qt * 128 + row;
+        to = whole ? A.common + out_row * D : mine_part + local * D;
+        if (real && d0 == 0) __stcg(whole ? A.common_lse + out_row : mine_part + M * D + local, J.lse);
+        if (threadIdx.x == 0 && item_a == 0)
+          __stcg(A.common_items + item_head * A.common_tiles + common_tile(A, item_row, R.first) + item_qt, whole ? make_int2(-1, -1) : make_int2(c0, c1));
+      }
+      if (PART == kOwn && whole) {
+        launch_before_is_done();
+        if (join && real) J = attend_join(J.lse, __ldcg(A.common_lse + out_row));
       }
 #pragma unroll 1
       for (int c = 0; c < cols / 32; ++c) {
@@ -669,18 +679,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         if (!real) {
           // (rows of padding)
+        } else if (PART == kCommon) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) __stcg(reinterpret_cast<float4*>(to + d + i), make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
         } else if (!whole) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             __stcg(reinterpret_cast<float4*>(part) + (d + i) / 4 * M + qt * 128 + row, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
-        } else if (PART != kAll) {
-          float4* const common = reinterpret_cast<float4*>(A.common + out_row * D + d);
-          if (PART == kCommon) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) __stcg(common + i / 4, make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
-          } else {
-            store_joined(A.out + out_row * D + d, o, inv * J.own, common, J.common, join);
-          }
+        } else if (PART == kOwn) {
+          store_joined(A.out + out_row * D + d, o, inv * J.own, A.common + out_row * D + d, J.common, join);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
@@ -706,11 +713,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       if (PART == kAll) {
         if (whole && real && d0 == 0 && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      } else if (whole && real && d0 == 0) {
-        if (PART == kCommon) __stcg(A.common_lse + out_row, J.lse);
-        else if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
+      } else if (PART == kOwn && whole && real && d0 == 0) {
+        if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
       }
-      if (!whole) {
+      if (!whole && PART != kCommon) {
         if (real && d0 == 0) {
           __stcg(part + M * D + qt * 128 + row, m);
           __stcg(part + M * D + M + qt * 128 + row, l);
@@ -733,7 +739,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sum += __ldcg(p + M) * exp2_fast(__ldcg(p) - ref);
           }
           const float by = sum == 0.f ? 1.f : 1.f / sum;
-          if (PART != kAll) {
+          if (PART == kOwn) {
+            launch_before_is_done();
             J.lse = sum == 0.f ? -INFINITY : high + log2f(sum);
             if (join) J = attend_join(J.lse, __ldcg(A.common_lse + out_row));
           }
@@ -753,14 +760,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) x[i].x += y[i].x * f, x[i].y += y[i].y * f, x[i].z += y[i].z * f, x[i].w += y[i].w * f;
             }
-            if (PART != kAll) {
-              float4* const common = reinterpret_cast<float4*>(A.common + out_row * D + d);
-              if (PART == kCommon) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) __stcg(common + i, make_float4(x[i].x * by, x[i].y * by, x[i].z * by, x[i].w * by));
-              } else {
-                store_joined(A.out + out_row * D + d, &x[0].x, by * J.own, common, J.common, join);
-              }
+            if (PART == kOwn) {
+              store_joined(A.out + out_row * D + d, &x[0].x, by * J.own, A.common + out_row * D + d, J.common, join);
               continue;
             }
 #pragma unroll
@@ -771,9 +772,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           if (PART == kAll) {
             if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;
-          } else if (d0 == 0) {
-            if (PART == kCommon) __stcg(A.common_lse + out_row, J.lse);
-            else if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
+          } else if (PART == kOwn && d0 == 0) {
+            if (A.lse) A.lse[out_row] = J.lse * 0.6931471805599453f;
           }
         }
       }
@@ -783,6 +783,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (SPLIT) wide_sync();      // both O have been read before either is written again
     }
   }
+  if (PART == kOwn) launch_before_is_done();
   mbar_settle(&failed);
   tmem_before();
   __syncthreads();
@@ -799,6 +800,7 @@ static int launch_wide(const AttendArgs& A, const CUtensorMap* maps, cudaStream_
   const auto kernel = attend_wide_kernel<D, E4M3, SPLIT, PART>;
   static std::atomic<unsigned long long> allowed;
   if (!allow_shared(reinterpret_cast<const void*>(kernel), S::smem, &allowed)) return SPEC_E_CUDA;
+  if (PART == kOwn) return launch_early(kernel, 152, kWideThreads, S::smem, st, A, maps[0], maps[1]);
   kernel<<<152, kWideThreads, S::smem, st>>>(A, maps[0], maps[1]);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }

@@ -7,11 +7,15 @@
 // (no mask: every token is behind all of them), and of each row's tokens over its own,
 // causal.  Both are the kernels of spec_attend, which divide their work evenly over the
 // device whatever the lengths.  The first leaves its results, divided by their sums,
-// and the logarithms of the sums in float32 in the workspace; the second joins them as
-// it writes the results.
+// and the logarithms of the sums in float32 in the workspace, a long item in the parts
+// that its CTAs have, which a launch of its own joins (where one CTA joined an item's
+// parts, 8 items of 16,000 positions took as long as 24).  The second, which may begin
+// while these end, adds them in as it writes the results.
 //
 // Common positions end with a multiple of 128, the larger tile of the kernels, so that
 // neither has a tile of both kinds; the up to 127 that are left go to each row.
+#include <algorithm>
+
 #include "spec_attend.cuh"
 
 namespace specv {
@@ -62,12 +66,54 @@ static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(con
   }
 }
 
-// Workspace, behind that of spec_attend: the groups' rows, tokens and lengths and the rows' first own positions, then
-// the results over the common positions.
-struct SharedSpace {
-  size_t group_row, group_cu, group_len, own_from, lse, out, bytes;
+constexpr int kPartsThreads = 256;
 
-  SharedSpace(size_t base, int N, int B, long long hq, int D) {
+// Joins the parts of the items that several CTAs have, in the order of their positions: D / 4 lanes a query row.  (A's
+// rows are the groups.)
+template <int D>
+static __global__ void __launch_bounds__(kPartsThreads) attend_parts_kernel(const AttendArgs A) {
+  launch_may_follow();
+  launch_before_is_done();
+  constexpr int L = D / 4;
+  const long long all = (long long)A.N * A.hq;
+  const int d = threadIdx.x % L * 4;
+  for (long long at = ((long long)blockIdx.x * kPartsThreads + threadIdx.x) / L; at < all; at += (long long)gridDim.x * (kPartsThreads / L)) {
+    const int token = (int)(at / A.hq), head = (int)(at - (long long)token * A.hq);
+    const int g = paged_row(A.C, token);
+    if (g < 0 || __ldg(A.C.kv_len + g) == 0) continue;
+    const int first = __ldg(A.C.cu + g), kv_head = head / A.group;
+    const long long a = (long long)(token - first) * A.group + (head - kv_head * A.group), qt = a / A.common_rows;
+    const int local = (int)(a - qt * A.common_rows);
+    const int2 ctas = __ldcg(A.common_items + kv_head * A.common_tiles + common_tile(A, g, first) + qt);
+    if (ctas.x < 0) continue;
+    const long long size = (long long)A.common_rows * (D + 1);
+    auto part = [&](int c) { return A.common_parts + (c * 2 + (c == ctas.x)) * size; };
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int c = ctas.x; c <= ctas.y; ++c) top = fmaxf(top, __ldcg(part(c) + A.common_rows * D + local));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 8
+    for (int c = ctas.x; c <= ctas.y; ++c) {
+      const float w = exp2_fast(__ldcg(part(c) + A.common_rows * D + local) - ref);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(part(c) + (long long)local * D + d));
+      sum += w;
+      x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+    }
+    const float by = sum == 0.f ? 1.f : 1.f / sum;
+    __stcg(reinterpret_cast<float4*>(A.common + at * D + d), make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
+    if (d == 0) __stcg(A.common_lse + at, sum == 0.f ? -INFINITY : top + log2f(sum));
+  }
+}
+
+// Workspace, behind that of spec_attend (which serves the rows' own positions): the groups' rows, tokens and lengths, the
+// rows' first own positions, then the results over the common positions.
+struct SharedSpace {
+  size_t group_row, group_cu, group_len, own_from, items, lse, out, parts, bytes;
+
+  SharedSpace(size_t base, int N, int B, int heads, int group, int D) {
+    const size_t hq = (size_t)heads * group;
     auto take = [&](size_t n) {
       const size_t at = base;
       base = (base + n + 255) / 256 * 256;
@@ -78,8 +124,10 @@ struct SharedSpace {
     group_cu = take(((size_t)B + 1) * 4);
     group_len = take((size_t)B * 4);
     own_from = take((size_t)B * 4);
+    items = take(heads * ((size_t)N * group / 16 + B + 1) * sizeof(int2));      // (16: the query rows of the smallest tile)
     lse = take((size_t)N * hq * 4);
     out = take((size_t)N * hq * D * 4);
+    parts = take((size_t)152 * 2 * 256 * (D + 1) * 4);
     bytes = base;
   }
 };
@@ -89,7 +137,7 @@ struct SharedSpace {
 extern "C" size_t spec_attend_shared_workspace_size(int N, int B, int heads, int group, int head_dim) {
   const size_t base = spec_attend_workspace_size(heads, group, head_dim);
   if (base == 0 || N < 0 || B < 0 || (long long)heads * group > 65535) return 0;
-  return specv::SharedSpace(base, N, B, (long long)heads * group, head_dim).bytes;
+  return specv::SharedSpace(base, N, B, heads, group, head_dim).bytes;
 }
 
 extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N, int group, float scale, int max_tokens,
@@ -113,7 +161,7 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   const long long rows = (long long)max_tokens * group;
   if (groups == 0) return attend_launch<kAll>(A, e4m3, rows, st);
   char* const base = static_cast<char*>(workspace);
-  const SharedSpace S(spec_attend_workspace_size(A.C.heads, group, A.C.D), N, A.C.B, A.hq, A.C.D);
+  const SharedSpace S(spec_attend_workspace_size(A.C.heads, group, A.C.D), N, A.C.B, A.C.heads, group, A.C.D);
   int32_t* const group_row = reinterpret_cast<int32_t*>(base + S.group_row);
   int32_t* const group_cu = reinterpret_cast<int32_t*>(base + S.group_cu);
   int32_t* const group_len = reinterpret_cast<int32_t*>(base + S.group_len);
@@ -124,11 +172,19 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   A.own_from = own_from;
   A.common = reinterpret_cast<float*>(base + S.out);
   A.common_lse = reinterpret_cast<float*>(base + S.lse);
+  A.common_parts = reinterpret_cast<float*>(base + S.parts);
+  A.common_items = reinterpret_cast<int2*>(base + S.items);
+  // a group's tokens are not known here: as many as each would have of all
+  const long long common_rows = ((long long)N + groups - 1) / groups * group;
+  A.common_rows = attend_tile_rows(e4m3, common_rows);
+  A.common_tiles = (long long)N * group / A.common_rows + groups + 1;
   AttendArgs common = A;
   common.C.B = groups;
   common.C.cu = group_cu;
   common.C.kv_len = group_len;
-  // a group's tokens are not known here: as many as each would have of all
-  const int each = attend_launch<kCommon>(common, e4m3, ((long long)N + groups - 1) / groups * group, st);
-  return each != SPEC_OK ? each : attend_launch<kOwn>(A, e4m3, rows, st);
+  int did = attend_launch<kCommon>(common, e4m3, common_rows, st);
+  const long long warps = ((long long)N * A.hq * A.C.D + 127) / 128, ctas = std::min((warps + kPartsThreads / 32 - 1) / (kPartsThreads / 32), 152ll * 16);
+  if (did == SPEC_OK)
+    did = launch_early(A.C.D == 128 ? attend_parts_kernel<128> : attend_parts_kernel<64>, (unsigned)ctas, kPartsThreads, 0, st, common);
+  return did != SPEC_OK ? did : attend_launch<kOwn>(A, e4m3, rows, st);
 }
