@@ -26,7 +26,7 @@ struct ConvArgs {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvTile = 32;      // tokens of a tile
-constexpr int kConvAhead = 4;      // tokens loaded before they are used
+constexpr int kConvAhead = 8;      // tokens loaded before they are used
 
 // VEC neighbouring channels of one token, as they are in memory.
 template <bool BF16, int VEC>

@@ -1,11 +1,17 @@
 // spec_scan: h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t, y_t = c_t . h_t, for N
 // states of each channel.
 //
-// A channel's states lie with N / 4 neighbouring lanes, four each, so that a warp
-// reads and writes 512 bytes of states side by side; the sum over the states goes
-// through the lanes.
+// A channel's states lie with neighbouring lanes, four or eight each, so that a warp reads
+// and writes states side by side; the sum over the states goes through the lanes.
 //
-// A few tokens: bound by the states' bytes (one in, one out a token for the commit).
+// A few tokens: one kernel, bound by the instructions of a warp's 16 channels (the
+// states' bytes, one in and one out a token for the commit, would allow half the time:
+// 64x3 tokens of 4096 channels by 16 states 26 us, 3300 GB/s).  Many tokens: tiles of
+// tokens, see below; a long row is split where there are few channels.
+//
+// Measured, 16 states, bf16, gate and softplus: 4x2048 tokens x 4096 channels 215 us (535 M
+// states, 2.5 T states a second), 16x1024x4096 362 us, 1x4096x4096 184 us (four
+// segments), 1x32768x2048 649 us.
 #include <algorithm>
 
 #include "spec_mixer.cuh"
@@ -112,47 +118,65 @@ __device__ __forceinline__ void scan_sum(float* y, int lane) {
 
 // ---------------------------------------------------------------- few tokens
 
-constexpr int kScanStepThreads = 128;
+constexpr int kScanStepThreads = 128, kScanStepCtas = 5;      // an SM: with 4 and 8 the verify step took 5 and 20 % longer
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+
+// Each of a channel's lanes has four states, or twice four, so far apart that the lanes' lie side by side.
+template <int N>
+struct ScanStep {
+  static constexpr int chunks = N == 8 ? 1 : 2, L = N / 4 / chunks;
+};
 
 // Four tokens at a time: each of a channel's lanes fetches one token's inputs (two where there are two lanes), and
 // the lanes hand them to one another.
 template <bool BF16, int N>
-__global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanArgs A, bool wide) {
-  constexpr int L = N / 4, own = L == 2 ? 2 : 1;
-  const int r = blockIdx.y;
+__global__ void __launch_bounds__(kScanStepThreads, kScanStepCtas) scan_step_kernel(const ScanArgs A, bool wide) {
+  constexpr int L = ScanStep<N>::L, CK = ScanStep<N>::chunks, own = L == 2 ? 2 : 1;
   const long long i = (long long)blockIdx.x * kScanStepThreads + threadIdx.x;
   const bool mine = i < (long long)A.D * L;      // (lanes beyond the last channel follow its sums)
-  const int d = mine ? (int)(i / L) : A.D - 1, lane = (int)(i % L), q = lane * 4, j0 = scan_token<L>(lane);
+  const int d = mine ? (int)(i / L) : A.D - 1, lane = (int)(i % L), q = lane * 4, j0 = scan_token<L>(lane), r = blockIdx.y;
   const MixerRow R = mixer_row(A, r, i == 0);
-  const int g = d / A.each;
+  const int g = A.each == A.D ? 0 : d / A.each, at = d * N + q;      // (D N is below 2^31)
   const long long xb = r * A.x_row + d, db = r * A.dt_row + d, zb = r * A.z_row + d;
   const long long bb = r * A.b_row + g * A.b_group + q, cb = r * A.c_row + g * A.c_group + q;
-  const long long out = (long long)r * A.T * A.D + d;
-  const float4 av = __ldg(reinterpret_cast<const float4*>(A.a + (long long)d * N + q));
-  const float2 a[2] = {mul2(make_float2(av.x, av.y), both_of(kLog2e)), mul2(make_float2(av.z, av.w), both_of(kLog2e))};
+  const long long out = (long long)r * A.T * A.D, states = out * N + at;
   const float skip = A.skip ? __ldg(A.skip + d) : 0.f, bias = A.dt_bias ? __ldg(A.dt_bias + d) : 0.f;
-  float2 h[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  if (R.from >= 0) {
-    const float4 s = *reinterpret_cast<const float4*>(A.state + ((long long)R.from * A.D + d) * N + q);
-    h[0] = make_float2(s.x, s.y);
-    h[1] = make_float2(s.z, s.w);
+  float2 a[CK][2], h[CK][2];
+#pragma unroll
+  for (int m = 0; m < CK; ++m) {
+    const float4 av = __ldg(reinterpret_cast<const float4*>(A.a + at + m * 4 * L));
+    a[m][0] = mul2(make_float2(av.x, av.y), both_of(kLog2e));
+    a[m][1] = mul2(make_float2(av.z, av.w), both_of(kLog2e));
+    h[m][0] = h[m][1] = make_float2(0.f, 0.f);
+    if (R.from >= 0) {
+      const float4 s = *reinterpret_cast<const float4*>(A.state + (long long)R.from * A.D * N + at + m * 4 * L);
+      h[m][0] = make_float2(s.x, s.y);
+      h[m][1] = make_float2(s.z, s.w);
+    }
   }
-#pragma unroll 1
-  for (int t0 = 0; t0 < R.len; t0 += 4) {
+  // (a run of tokens has no branch inside, so that their chains of latencies lie side by side)
+  auto run = [&](int t0, auto tokens) {
+    constexpr int left = decltype(tokens)::value;
     float x[own], z[own], delta[2] = {0.f, 0.f}, put[own];
-    ScanFour<BF16> b[4], c[4];
+    ScanFour<BF16> b[left][CK], c[left][CK];
 #pragma unroll
     for (int k = 0; k < own; ++k) {
-      const int t = min(t0 + j0 + k, R.len - 1);
+      const int t = t0 + min(j0 + k, left - 1);
       x[k] = load_one<BF16>(A.x, xb + t * A.x_tok);
       delta[k] = load_one<BF16>(A.dt, db + t * A.dt_tok) + bias;
       z[k] = A.z ? load_one<BF16>(A.z, zb + t * A.z_tok) : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = min(t0 + k, R.len - 1);
-      b[k].load(A.b, bb + t * A.b_tok, wide);
-      c[k].load(A.c, cb + t * A.c_tok, wide);
+    for (int k = 0; k < left; ++k) {
+#pragma unroll
+      for (int m = 0; m < CK; ++m) {
+        b[k][m].load(A.b, bb + (t0 + k) * A.b_tok + m * 4 * L, wide);
+        c[k][m].load(A.c, cb + (t0 + k) * A.c_tok + m * 4 * L, wide);
+      }
     }
 #pragma unroll
     for (int k = 0; k < own; ++k) {
@@ -161,39 +185,53 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanA
     }
     float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (t0 + k >= R.len) break;
+    for (int k = 0; k < left; ++k) {
       // the lane of the channel that has token k: scan_token's inverse
-      const int from = L == 2 ? k >> 1 : (k >> 1) + (k & 1) * 2, at = L == 2 ? k & 1 : 0;
-      const float2 step = both_of(__shfl_sync(0xffffffffu, at ? delta[1] : delta[0], from, L));
-      const float2 in = both_of(__shfl_sync(0xffffffffu, put[own > 1 ? at : 0], from, L));
+      const int from = L == 2 ? k >> 1 : (k >> 1) + (k & 1) * 2, which = L == 2 ? k & 1 : 0;
+      const float2 step = both_of(__shfl_sync(0xffffffffu, which ? delta[1] : delta[0], from, L));
+      const float2 in = both_of(__shfl_sync(0xffffffffu, put[own > 1 ? which : 0], from, L));
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        h[j] = fma2(scan_decay(mul2(step, a[j])), h[j], mul2(in, b[k].get(j)));
-        sum = fma2(c[k].get(j), h[j], sum);
+      for (int m = 0; m < CK; ++m) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          h[m][j] = fma2(scan_decay(mul2(step, a[m][j])), h[m][j], mul2(in, b[k][m].get(j)));
+          sum = fma2(c[k][m].get(j), h[m][j], sum);
+        }
+        if (A.states && mine)
+          __stcs(reinterpret_cast<float4*>(A.states + states + (long long)(t0 + k) * A.D * N + m * 4 * L),
+                 make_float4(h[m][0].x, h[m][0].y, h[m][1].x, h[m][1].y));
       }
       y[k] = sum.x + sum.y;
-      if (A.states && mine)
-        __stcs(reinterpret_cast<float4*>(A.states + (out + (long long)(t0 + k) * A.D) * N + q), make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
     }
     scan_sum<L>(y, lane);
 #pragma unroll
     for (int k = 0; k < own; ++k) {
-      const int t = t0 + j0 + k;
-      if (mine && t < R.len && lane < 4) {
+      if (mine && j0 + k < left && lane < 4) {
         float v = fmaf(skip, x[k], y[k]);
         if (A.z) v *= silu(z[k]);
-        store_one<BF16>(A.y, out + (long long)t * A.D, v);
+        store_one<BF16>(A.y, out + (long long)(t0 + j0 + k) * A.D + d, v);
       }
     }
-  }
+  };
+  int t0 = 0;
+#pragma unroll 1
+  for (; t0 + 4 <= R.len; t0 += 4) run(t0, Count<4>());
+  if (R.len - t0 == 3) run(t0, Count<3>());
+  if (R.len - t0 == 2) run(t0, Count<2>());
+  if (R.len - t0 == 1) run(t0, Count<1>());
   if (!mine) return;
   for (int t = R.len; t < A.T; ++t) {
-    if (lane == 0) store_one<BF16>(A.y, out + (long long)t * A.D, 0.f);
-    if (A.states) __stcs(reinterpret_cast<float4*>(A.states + (out + (long long)t * A.D) * N + q), make_float4(0.f, 0.f, 0.f, 0.f));
+    if (lane == 0) store_one<BF16>(A.y, out + (long long)t * A.D + d, 0.f);
+    if (A.states)
+#pragma unroll
+      for (int m = 0; m < CK; ++m)
+        __stcs(reinterpret_cast<float4*>(A.states + states + (long long)t * A.D * N + m * 4 * L), make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  if (R.to >= 0) *reinterpret_cast<float4*>(A.last + ((long long)R.to * A.D + d) * N + q) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+  if (R.to >= 0)
+#pragma unroll
+    for (int m = 0; m < CK; ++m)
+      *reinterpret_cast<float4*>(A.last + (long long)R.to * A.D * N + at + m * 4 * L) = make_float4(h[m][0].x, h[m][0].y, h[m][1].x, h[m][1].y);
 }
 
 // --------------------------------------------------------------- many tokens
@@ -734,7 +772,7 @@ static int launch_scan(const ScanArgs& A, bool wide, void* workspace, cudaStream
     char* const ws = static_cast<char*>(workspace);
     return four ? launch_tiles<BF16, N, 4>(A, pairs, ws, st) : launch_tiles<BF16, N, 1>(A, pairs, ws, st);
   }
-  const dim3 grid((unsigned)(((long long)A.D * (N / 4) + kScanStepThreads - 1) / kScanStepThreads), A.B);
+  const dim3 grid((unsigned)(((long long)A.D * ScanStep<N>::L + kScanStepThreads - 1) / kScanStepThreads), A.B);
   scan_step_kernel<BF16, N><<<grid, kScanStepThreads, 0, st>>>(A, wide);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
