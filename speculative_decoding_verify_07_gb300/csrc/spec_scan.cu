@@ -242,8 +242,11 @@ __global__ void __launch_bounds__(kScanStepThreads, kScanStepCtas) scan_step_ker
 // lane's part of the sums.  The first then goes through the tile's elements again (the sum,
 // skip, gate, output).
 //
-// Bound by issue slots and the latency of a lane's chain (decay, state), with few warps an
-// SM; the elements' own arithmetic (softplus, gate, a third of all) is off that chain.
+// Bound by issue slots (busy in 54 % of the cycles, 63 % where an SM has work), the multiply-add
+// pipe (57 %) and the walk's loads from shared memory (64 %), which take turns: the walk alone,
+// without the elements, took 160 of 215 us, and with neither loads nor exponentials still 124.
+// Both halves by the same warps 252 us; four channels a lane 300 (half the warps); 16-bit b and c
+// unpacked by the walk 222.
 //
 // Decays are ex2.approx alone here, whose lean to one side (see scan_decay) would add up over
 // the tokens that a state remembers.  So the tile's decays are also multiplied, and at its end
