@@ -137,6 +137,13 @@ __device__ __forceinline__ int attend_sees(const AttendArgs& A, const AttendRow<
   return max(0, min(R.kv - R.n + i + 1, A.C.max_pages * A.C.page_size));
 }
 
+// An item's beginning and end take as long as some tiles, and a row's own positions may be few: they are divided with so
+// many before each item's.  (64x3 tokens of 500 own positions on average take 133 us with 4 to 12 in the few-rows kernel
+// and 153 with none, 64x3 of 2000 196 and 235; 6 chunks of up to 500 220 and 226 with 3 in the other.  Common positions,
+// which are many, gain nothing.)
+template <int M, int PART>
+constexpr int attend_cost() { return PART != kOwn ? 0 : M <= 32 ? 6 : 3; }
+
 // (kOwn: those from the first position on)
 template <int M, int KT, int PART>
 __device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow<PART>& R, int qt) {
@@ -144,7 +151,7 @@ __device__ __forceinline__ int attend_tiles(const AttendArgs& A, const AttendRow
   if (PART == kCommon) return R.kv / KT;
   const int last = min((qt + 1) * M, R.n * A.group) - 1;
   const int tiles = (attend_sees(A, R, attend_token(A, last)) + KT - 1) / KT;
-  return max(1, PART == kOwn ? tiles - R.from / KT : tiles);
+  return max(1, PART == kOwn ? tiles - R.from / KT : tiles) + attend_cost<M, PART>();
 }
 
 template <int M, int PART>
@@ -209,7 +216,8 @@ __device__ __forceinline__ void attend_share(const AttendArgs& A, AttendShare* o
   if (all > 0x7fffffff && A.flags && t == 0 && blockIdx.x == 0) atomicOr(&A.flags[0], (uint32_t)SPEC_F_BAD_IDX);
   const int ctas = min((int)gridDim.x, total), cta = min((int)blockIdx.x, ctas);
   const int tiles_each = ctas ? total / ctas : 0, more = total - tiles_each * ctas;
-  const int slack = min(WHOLE / 2, tiles_each / 32);      // (1/16 more work for a share that takes in both its ends)
+  // (1/16 more work for a share that takes in both its ends; and no share ends before an item's first tile)
+  const int slack = max(min(WHOLE / 2, tiles_each / 32), attend_cost<M, PART>() ? attend_cost<M, PART>() + 1 : 0);
   const int begin = cta * tiles_each + min(cta, more), end = cta < ctas ? begin + tiles_each + (cta < more) : begin;
   if (t == 0) {
     out->each = tiles_each;
@@ -270,6 +278,7 @@ struct AttendWalk {
   AttendRow<PART> R;
   int row, head, qt, tiles;      // the item, and its position tiles
   int a, b;                      // this segment's, by position
+  int from, to;                  // the same from the item's beginning, its cost first
   int at, end;                   // the next tile of all, and the share's end
   int next_a;
 
@@ -293,18 +302,20 @@ struct AttendWalk {
       }
       tiles = attend_tiles<M, KT>(A, R, qt);
     }
-    a = next_a;
-    b = min(tiles, a + (end - at));
-    at += b - a;
-    next_a = b;
-    if (PART == kOwn) a += first(), b += first();
+    from = next_a;
+    to = min(tiles, from + (end - at));
+    at += to - from;
+    next_a = to;
+    constexpr int cost = attend_cost<M, PART>();
+    a = max(from - cost, 0) + first();
+    b = max(to - cost, 0) + first();
     return true;
   }
   // The tile of positions that the item begins with.
   __device__ __forceinline__ int first() const { return PART == kOwn ? R.from / KT : 0; }
-  __device__ __forceinline__ bool whole() const { return a == first() && b == first() + tiles; }
+  __device__ __forceinline__ bool whole() const { return from == 0 && to == tiles; }
   // The first tile of this item among all.
-  __device__ __forceinline__ int item_begin() const { return at - (b - first()); }
+  __device__ __forceinline__ int item_begin() const { return at - to; }
 };
 
 // ---------------------------------------------------------------------- copies

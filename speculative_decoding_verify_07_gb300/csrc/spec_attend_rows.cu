@@ -37,7 +37,7 @@ namespace specv {
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr float kRowsSlack = 8.f;
-constexpr int kOwnWhole = 16;        // a row's own positions: items of so few tiles stay in one CTA (64x3 tokens, 500 on average: 11 us less)
+constexpr int kOwnWhole = 22;        // a row's own positions: items of so few tiles, their cost among them, stay in one CTA
 constexpr int kRowsShift = 32;       // sums of an 8-bit cache are kept 2^-32 times their size: 2^-e is up to 2^126
 static_assert(254 - (int)kAttendTop - kRowsShift >= 1, "so 2^-e of the largest scale is a normal number");
 constexpr unsigned kRowsLow = 64, kRowsHigh = 144;   // the ordinary range: within 2^80 a weight of 2^-46 stays a normal number

@@ -762,13 +762,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             if (PART == kOwn) {
               store_joined(A.out + out_row * D + d, &x[0].x, by * J.own, A.common + out_row * D + d, J.common, join);
-              continue;
-            }
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2)
-              *reinterpret_cast<uint4*>(A.out + out_row * D + d + 4 * i) =
-                  make_uint4(pack_bf16(x[i].x * by, x[i].y * by), pack_bf16(x[i].z * by, x[i].w * by),
-                             pack_bf16(x[i + 1].x * by, x[i + 1].y * by), pack_bf16(x[i + 1].z * by, x[i + 1].w * by));
+              for (int i = 0; i < 8; i += 2)
+                *reinterpret_cast<uint4*>(A.out + out_row * D + d + 4 * i) =
+                    make_uint4(pack_bf16(x[i].x * by, x[i].y * by), pack_bf16(x[i].z * by, x[i].w * by),
+                               pack_bf16(x[i + 1].x * by, x[i + 1].y * by), pack_bf16(x[i + 1].z * by, x[i + 1].w * by));
+            }
           }
           if (PART == kAll) {
             if (d0 == 0 && A.lse) A.lse[out_row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * 0.6931471805599453f;

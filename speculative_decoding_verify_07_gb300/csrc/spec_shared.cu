@@ -13,10 +13,10 @@
 // while these end, adds them in as it writes the results.
 //
 // Measured, 8 heads of 128, group 4, bf16: 64 rows of 3 tokens behind 16,000 common positions
-// and up to 1000 of their own 153 us (spec_attend 514): 72 for the common positions (24 items for
-// 152 CTAs, each at its beginning and end more than half the time), 5 to 10 to join them, 65 for
-// the own ones (a CTA has two items or three, and no way to share the last).  16 groups of 8 rows,
-// 6001 common positions, 8 bits 151 us; 6 chunks of up to 500 tokens behind 12,345 226 us.
+// and up to 1000 of their own 133 us (spec_attend 503): 72 for the common positions (24 items for
+// 152 CTAs, each at its beginning and end more than half the time), 5 to 10 to join them, 45 for
+// the own ones.  16 groups of 8 rows, 6001 common positions, 8 bits 141 us; 6 chunks of up to 500
+// tokens behind 12,345 218 us.
 // Short prompts do not pay: behind 128 positions 64x3 take 54 us, spec_attend 32.
 //
 // Common positions end with a multiple of 128, the larger tile of the kernels, so that

@@ -102,6 +102,20 @@ def test_shared_long(pool):
     check(b, 5, [0, 2], [2640], max_tokens=1)           # (the hint is not a limit)
 
 
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 3, 30])
+def test_long_own_contexts_are_divided(new, pool):
+    """Few rows for the whole device: an item's own positions lie in many shares, each shorter than an item's cost."""
+    for total, heads in (([6000, 5000], 1), ([1700, 2500], 2), ([2048 + 17, 900], 3)):
+        b = Batch([new] * 2, total, page=16, pool=pool, heads=heads, dim=64, seed=17)
+        share(b, [0, 2], [300])
+        first = check(b, 4, [0, 2], [300])
+        b = Batch([new] * 2, total, page=16, pool=pool, heads=heads, dim=64, seed=17)
+        share(b, [0, 2], [300])
+        again = check(b, 4, [0, 2], [300])
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
 @pytest.mark.parametrize("rows,lens", [([0, 5], [300]), ([-1, 2], [300]), ([3, 1], [300]), ([0, 2, 1, 4], [300, 300, 300]),
                                        ([0, 4], [-3]), ([0, 4], [127]), ([2, 2], [300]), ([0], [])])
 def test_groups_that_share_nothing(rows, lens):
