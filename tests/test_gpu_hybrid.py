@@ -323,3 +323,25 @@ def test_states_commit():
             n = int(accept[r])
             cl, rl = layer(l, slice(r, r + 1), n) if n else (conv0[l, slot[r]][None], rec0[l, slot[r], 0][None])
             assert torch.equal(conv[l, slot[r]], cl[0]) and torch.equal(rec[l, slot[r], 0], rl[0])
+
+
+def test_scans_at_once():
+    """Split rows on two streams, a workspace each, and one workspace for calls one after the other: the same bits."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    N, jobs = 16, []
+    for B, T, D in ((1, 3000, 128), (2, 1500, 96)):
+        x, dt, z = (torch.randn((B, T, D), device="cuda").to(torch.bfloat16) for _ in range(3))
+        b, c = (torch.randn((B, T, 1, N), device="cuda").to(torch.bfloat16) for _ in range(2))
+        args = (x, dt, -torch.rand((D, N), device="cuda"), b, c, None, z)
+        jobs.append((args, [t.clone() for t in sv.spec_scan(*args)], sv.new_scan_workspace(B, T, D, N, "cuda"), torch.cuda.Stream()))
+    largest = max((j[2] for j in jobs), key=lambda w: w.numel())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for args, _, ws, stream in jobs:
+            with torch.cuda.stream(stream):
+                got.append(sv.spec_scan(*args, workspace=ws))
+        torch.cuda.synchronize()
+        got += [sv.spec_scan(*args, workspace=largest) for args, _, _, _ in jobs]
+        for g, job in zip(got, jobs + jobs):
+            assert all(torch.equal(a, b) for a, b in zip(g, job[1]))

@@ -207,3 +207,43 @@ def test_shared_is_as_close_to_spec_attend_as_either_to_the_oracle():
     # (row 16's group shares 15 tiles of 128 of its 2000 positions)
     got, l2 = sv.spec_attend_shared(q, dev(np.array([0, 16, 32], np.int32)), dev(np.array([2048, 2000], np.int32)), *b.args(), max_tokens=3)
     assert (got.float() - want.float()).norm() <= 3 * BF16 * want.float().norm() and (l2 - lse).abs().max() <= 2e-5
+
+
+def test_calls_at_once_and_one_after_the_other():
+    """Two streams with a workspace each, and layers that follow one another on one workspace, eagerly and in a graph, with what
+    reads a result right behind the call: the same bits as one call by itself."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    jobs = []
+    for seed, (new, total, rows, lens) in enumerate([([3] * 32, [3000 + 5 * r for r in range(32)], [0, 32], [2944]),
+                                                     ([1] * 6, [900 + 40 * r for r in range(6)], [0, 3, 6], [768, 640])]):
+        b = Batch(new, total, page=16, heads=4, dim=128, seed=30 + seed)
+        share(b, rows, lens)
+        q = torch.randn((b.N, 16, 128), device="cuda").to(torch.bfloat16)
+        args = (q, dev(np.array(rows, np.int32)), dev(np.array(lens, np.int32)), *b.args())
+        want = [t.clone() for t in sv.spec_attend_shared(*args, max_tokens=max(new))]
+        jobs.append((args, max(new), want, sv.new_attend_shared_workspace(b.N, len(new), 4, 4, 128, "cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for args, most, _, ws, stream in jobs:
+            with torch.cuda.stream(stream):
+                out, lse = sv.spec_attend_shared(*args, max_tokens=most, workspace=ws)
+                got.append((out + 0, lse + 0))
+        torch.cuda.synchronize()
+        for (a, b), job in zip(got, jobs):
+            assert torch.equal(a, job[2][0]) and torch.equal(b, job[2][1])
+    most_tokens, most_rows = max(j[0][0].shape[0] for j in jobs), max(len(j[0][4]) for j in jobs)
+    ws = sv.new_attend_shared_workspace(most_tokens, most_rows, 4, 4, 128, "cuda")
+    outs = [[torch.empty_like(t) for t in j[2]] for j in jobs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for (args, most, _, _, _), (out, lse) in zip(jobs + jobs, outs + outs):
+            sv.spec_attend_shared(*args, max_tokens=most, workspace=ws, out=out, lse=lse)
+        copies = [[t + 0 for t in o] for o in outs]
+    for _ in range(5):
+        for o in outs + copies:
+            for t in o:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, w) for o, j in zip(copies, jobs) for t, w in zip(o, j[2]))
