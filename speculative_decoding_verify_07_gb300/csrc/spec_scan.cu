@@ -734,6 +734,7 @@ static ScanSplit scan_split(int B, int T, int D, int each, int N) {
 
 // (the most parts that a call of these sizes may have, whatever its groups: one group has the fewest CTAs)
 static size_t scan_split_bytes(int B, int T, int D, int N) {
+  if (B == 0) return 0;
   const ScanSplit W = scan_split(B, std::max(T, 1), D, D, N);
   const size_t n = W.segments > 1 ? (size_t)W.segments * W.fine : 0;
   return (n * B * D * 4 + 255) / 256 * 256 + n * B * D * N * 4;
