@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "spec_mixer.cuh"
+#include "spec_scan_split.h"
 #include "spec_tma.cuh"
 
 namespace specv {
@@ -252,11 +253,7 @@ __global__ void __launch_bounds__(kScanStepThreads, kScanStepCtas) scan_step_ker
 // the tokens that a state remembers.  So the tile's decays are also multiplied, and at its end
 // the state that entered gets the difference to the exact decay of the tile's sum of delta.
 
-constexpr int kScanThreads = 128;      // of each half
-constexpr int kScanLane = 2;           // channels of a lane
-constexpr int kScanTile = 16;          // tokens of a tile
 constexpr int kScanGroup = 8;          // tokens that a lane takes together
-constexpr int kScanCtas = 2;           // an SM
 
 template <bool BF16, int N, int VEC>
 struct ScanShape {
@@ -465,17 +462,6 @@ struct ScanStates {
     for (int n = 0; n < 4; ++n) v[n] = mul2(v[n], both_of(by));
   }
 };
-
-// A row's tokens where they are split into segments, and the workspace of such a call: each part's sum of delta by (row,
-// part, channel), then by (row, part, channel, state) the state behind the part if it began with zeros, which
-// scan_join_kernel turns into the state that enters it.  A segment has `fine` parts: scan_segment_kernel has fewer
-// registers and takes more CTAs an SM.
-struct ScanSplit {
-  int segments, span, fine;            // span: tokens of a segment
-  float* sums;
-  float* states;
-};
-constexpr int kScanFine = 4, kScanLeast = 128;      // at most; no part is of fewer tokens
 
 template <bool BF16, int N, int VEC, bool GATE>
 __global__ void __launch_bounds__(2 * kScanThreads, kScanCtas) scan_tile_kernel(const ScanArgs A, const ScanSplit W, bool pairs) {
@@ -712,41 +698,13 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
 
 constexpr int kScanStepTokens = 16;    // up to so many are walked by scan_step_kernel
 
-static int scan_blocks(int D, int each, int N) {
-  const int ch = kScanThreads / (N / 4) * kScanLane;
-  return (each + ch - 1) / ch * (D / each);
-}
-
-// A row's segments: one where there are CTAs for most SMs, otherwise as many as fill all of them once.  The first pass
-// makes a split cost half as much again: 64 CTAs of 4096 tokens take 184 us in four segments, 247 in one, and a row of 512
-// tokens 37 and 34; 256 CTAs of 2048 tokens took 220 us whole and 300 and more in two.
-static ScanSplit scan_split(int B, int T, int D, int each, int N) {
-  const long long ctas = (long long)scan_blocks(D, each, N) * B;
-  const long long want = ctas >= 100 ? 1 : std::max(1ll, 152 * kScanCtas / ctas);
-  ScanSplit W = {};
-  W.segments = (int)std::max(1ll, std::min(want, (long long)T / kScanLeast));
-  W.fine = W.segments > 1 ? std::max(1, std::min(kScanFine, T / W.segments / kScanLeast)) : 1;
-  const int unit = kScanTile * W.fine;
-  W.span = (int)(((long long)T + (long long)W.segments * unit - 1) / ((long long)W.segments * unit) * unit);
-  W.segments = (int)(((long long)T + W.span - 1) / W.span);
-  return W;
-}
-
-// (the most parts that a call of these sizes may have, whatever its groups: one group has the fewest CTAs)
-static size_t scan_split_bytes(int B, int T, int D, int N) {
-  if (B == 0) return 0;
-  const ScanSplit W = scan_split(B, std::max(T, 1), D, D, N);
-  const size_t n = W.segments > 1 ? (size_t)W.segments * W.fine : 0;
-  return (n * B * D * 4 + 255) / 256 * 256 + n * B * D * N * 4;
-}
-
 template <bool BF16, int N, int VEC>
 static int launch_tiles(const ScanArgs& A, bool pairs, char* workspace, cudaStream_t st) {
   using S = ScanShape<BF16, N, VEC>;
   const int blocks = scan_blocks(A.D, A.each, N);
   ScanSplit W = scan_split(A.B, A.T, A.D, A.each, N);
   W.sums = reinterpret_cast<float*>(workspace);
-  W.states = reinterpret_cast<float*>(workspace + ((size_t)W.segments * W.fine * A.B * A.D * 4 + 255) / 256 * 256);
+  W.states = reinterpret_cast<float*>(workspace + scan_states_at(scan_parts(W, A.B), A.D));
   constexpr int smem = sizeof(ScanShared<N, S::CH, true>), less = sizeof(ScanShared<N, S::CH, false>);
   const dim3 grid((unsigned)blocks * W.segments, A.B);
   if (W.segments > 1) {
@@ -801,7 +759,7 @@ static bool scan_dims(int B, int T, int D, int N) {
 
 extern "C" size_t spec_scan_workspace_size(int B, int T, int D, int N) {
   if (!specv::scan_dims(B, T, D, N)) return 0;
-  return std::max<size_t>(256, specv::scan_split_bytes(B, T, D, N));
+  return std::max<size_t>(256, specv::scan_bytes(specv::scan_parts_most(B, T, D, N), D, N));
 }
 
 extern "C" int spec_scan(const spec_scan_t* s, void* workspace, size_t workspace_bytes, void* cuda_stream) {

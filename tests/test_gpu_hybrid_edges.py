@@ -2,16 +2,12 @@
 
 Tolerances count roundings: half a step of bf16 is 2^-8 relative, of float32 2^-24.
 """
-import numpy as np
 import pytest
 import torch
 
-from oracle import hybrid as oh
-from tests.test_gpu_hybrid import F32, half, host, near
+from tests.test_gpu_hybrid import run_scan
 
 pytestmark = pytest.mark.gpu
-
-DT = [torch.bfloat16, torch.float32]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -28,3 +24,16 @@ def test_an_empty_batch(T):
     assert y.shape == (0, T, 24) and last.shape == (0, 24, 16)
     y, last = sv.spec_conv(x, torch.ones((4, 24), device="cuda"))
     assert y.shape == (0, T, 24) and last.shape == (0, 3, 24)
+
+
+# ------------------------------------------------------------------- the scan
+
+@pytest.mark.parametrize("B,T,D,N,groups", [(8, 2048, 512, 8, 8), (9, 8192, 64, 16, 2), (5, 1279, 384, 32, 8), (7, 2934, 312, 16, 2),
+                                            (2, 1551, 1338, 16, 2), (1, 2048, 1728, 16, 36)])
+def test_scan_stays_within_its_workspace(B, T, D, N, groups):
+    """Several groups that divide a row otherwise than one: what lies behind a workspace of the size asked for is untouched."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    size = sv.LIB.spec_scan_workspace_size(B, T, D, N)
+    whole = torch.full((size + (8 << 20),), 0xa5, dtype=torch.uint8, device="cuda")
+    run_scan(B, T, D, N, torch.bfloat16, groups=groups, seed=B + T, workspace=whole[:size])
+    assert (whole[size:] == 0xa5).all()

@@ -1,5 +1,7 @@
 """The workspace of spec_scan, which needs no GPU: its size for every legal batch."""
+import ctypes
 import os
+import random
 import subprocess
 import sys
 
@@ -25,3 +27,56 @@ def test_an_empty_batch_has_a_workspace(sv):
                           "        assert sv.LIB.spec_scan_workspace_size(0, T, 64, N) >= 256\n"
                           "assert sv.new_scan_workspace(0, 8192, 64, 16, 'cpu').numel() >= 256\n"], cwd=ROOT)
     assert run.returncode == 0
+
+
+# Through the source's own arithmetic: the most bytes that any number of groups takes of a workspace, and how many parts.
+PROBE = """
+#include "spec_scan_split.h"
+using namespace specv;
+extern "C" size_t used(int B, int T, int D, int N, int groups) {
+  const ScanSplit W = scan_split(B, T, D, D / groups, N);
+  return scan_bytes(scan_parts(W, B), D, N);
+}
+extern "C" size_t most_used(int B, int T, int D, int N) {
+  size_t most = 0;
+  for (int g = 1; g <= D; ++g)
+    if (D % g == 0) most = std::max(most, used(B, T, D, N, g));
+  return most;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def split(tmp_path_factory):
+    from speculative_decoding_verify_07_gb300 import build
+    path = tmp_path_factory.mktemp("scan")
+    (path / "probe.cpp").write_text(PROBE)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-I", build.CSRC, "-o", str(path / "probe.so"), str(path / "probe.cpp")],
+                   check=True)
+    lib = ctypes.CDLL(str(path / "probe.so"))
+    lib.used.restype = lib.most_used.restype = ctypes.c_size_t
+    return lib
+
+
+# (B, T, D, N, groups): fewer CTAs and more parts with several groups than with one
+GROUPED = [(8, 2048, 512, 8, 8), (9, 8192, 64, 16, 2), (17, 4096, 64, 16, 2), (5, 1279, 384, 32, 8), (7, 2934, 312, 16, 2),
+           (2, 1551, 1338, 16, 2), (8, 1536, 576, 8, 2), (1, 2048, 1728, 16, 36)]
+
+
+@pytest.mark.parametrize("B,T,D,N,groups", GROUPED)
+def test_groups_that_divide_otherwise_than_one(sv, split, B, T, D, N, groups):
+    assert split.used(B, T, D, N, groups) > split.used(B, T, D, N, 1)
+    assert split.used(B, T, D, N, groups) <= sv.LIB.spec_scan_workspace_size(B, T, D, N)
+
+
+def test_no_call_takes_more_than_the_workspace(sv, split):
+    rng = random.Random(1)
+    log = lambda lo, hi: int(lo * (hi / lo) ** rng.random() + 0.5)
+    split_calls = 0
+    for i in range(20000):
+        B, T, N = log(1, 400), log(1, 0x7fffff00) if i % 4 == 0 else log(1, 40000), rng.choice([8, 16, 32, 64, 128])
+        D = rng.randrange(1, 65) * rng.choice([1, 2, 6, 8, 16, 48, 64]) if i % 2 else log(1, 16384)
+        most = split.most_used(B, T, D, N)
+        split_calls += most > 0
+        assert most <= sv.LIB.spec_scan_workspace_size(B, T, D, N), (B, T, D, N)
+    assert split_calls > 2000
