@@ -135,9 +135,9 @@ typedef struct {
   int32_t softplus;
 } spec_scan_t;
 
-/* Bytes of workspace spec_scan needs for B rows of T tokens over D channels of N
- * states (256 at least; 0 when a size is out of range).  Its contents need not be
- * kept or cleared; calls that may overlap take one each. */
+/* Bytes of workspace spec_scan needs for up to B rows of up to T tokens over D
+ * channels of N states (256 at least; 0 when a size is out of range).  Its contents
+ * need not be kept or cleared; calls that may overlap take one each. */
 size_t spec_scan_workspace_size(int B, int T, int D, int N);
 
 /* spec_scan - the selective scan, for channel d and state n:

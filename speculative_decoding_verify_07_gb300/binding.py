@@ -889,7 +889,7 @@ def spec_conv(x, weight, bias=None, state=None, slot=None, lens=None, *, silu=Tr
 
 
 def new_scan_workspace(B: int, T: int, D: int, N: int, device) -> torch.Tensor:
-    """A workspace for spec_scan: calls of these sizes, one at a time."""
+    """A workspace for spec_scan: calls of up to B rows of up to T tokens over D channels of N states, one at a time."""
     n = int(LIB.spec_scan_workspace_size(int(B), int(T), int(D), int(N)))
     if n == 0:
         raise ValueError(f"spec_scan takes no {B} rows of {T} tokens over {D} channels of {N} states")

@@ -48,12 +48,13 @@ inline ScanSplit scan_split(int B, int T, int D, int each, int N) {
 // Parts of all rows that a call keeps.
 inline long long scan_parts(const ScanSplit& W, int B) { return W.segments > 1 ? (long long)W.segments * W.fine * B : 0; }
 
-// No division has more, whatever its groups: one group has the fewest CTAs and so may have the most segments, but fewer
-// segments may have more parts each.  A segment has at most kScanFine parts, and none is of fewer than kScanLeast tokens
-// before segments are rounded up to whole tiles, which makes fewer of them.
+// No division of up to B rows of up to T tokens has more, whatever its groups: one group has the fewest CTAs and so may have
+// the most segments, but fewer segments may have more parts each, and fewer rows more segments.  Rows that are split have
+// at most 152 kScanCtas segments for the CTAs of one, a segment at most kScanFine parts, and none of these is of fewer than
+// kScanLeast tokens before segments are rounded up to whole tiles, which makes fewer of them.
 inline long long scan_parts_most(int B, int T, int D, int N) {
-  const long long want = B ? scan_want((long long)scan_blocks(D, D, N) * B) : 1;
-  return want > 1 ? std::min((long long)T / kScanLeast, want * kScanFine) * B : 0;
+  const int blocks = scan_blocks(D, D, N);
+  return scan_want(blocks) > 1 ? std::min((long long)T / kScanLeast * B, 152ll * kScanCtas * kScanFine / blocks) : 0;
 }
 
 // Where the states lie in the workspace, and its bytes for so many parts.

@@ -37,3 +37,10 @@ def test_scan_stays_within_its_workspace(B, T, D, N, groups):
     whole = torch.full((size + (8 << 20),), 0xa5, dtype=torch.uint8, device="cuda")
     run_scan(B, T, D, N, torch.bfloat16, groups=groups, seed=B + T, workspace=whole[:size])
     assert (whole[size:] == 0xa5).all()
+
+
+def test_scan_workspace_serves_smaller_batches():
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    ws = sv.new_scan_workspace(8, 3000, 2048, 16, "cuda")
+    for B, T in ((8, 50), (1, 3000), (3, 1000)):
+        run_scan(B, T, 2048, 16, torch.bfloat16, seed=T, workspace=ws)
