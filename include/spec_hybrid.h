@@ -93,7 +93,8 @@ int spec_conv(const spec_conv_t* conv, void* cuda_stream);
  *   states   [B, T, D, N] float32 or NULL: the state behind each token, one layer
  *            of spec_commit's verify_rec with H = 1, Dk = D, Dv = N.
  *   last     [last_slots, D, N] float32 or NULL, last_slot: as in spec_conv_t.
- *   softplus nonzero: delta = ln(1 + exp(dt + dt_bias)), otherwise dt + dt_bias.
+ *   softplus nonzero: delta = ln(1 + exp(dt + dt_bias)), and 0 where that is below
+ *            2^-126 (dt + dt_bias < -87.3, -inf too); otherwise dt + dt_bias.
  * Outputs overlap no input, but for `last`. */
 typedef struct {
   const void* x;

@@ -33,13 +33,14 @@ struct ScanArgs {
   bool softplus;
 };
 
-// ln(1 + exp(v)) within 12 half steps (2^-24) of itself: max(v, 0) + ln(1 + e), e = exp(-|v|), with the polynomial
-// of degree 8 that is nearest to ln(1 + e) / e over [0, 1] (by Remez's method; 1.3e-7 of it off as evaluated here).
+// ln(1 + exp(v)) within 12 half steps (2^-24) of itself where exp(v) is a normal number, and 0 below (v < -87.3): max(v, 0)
+// + ln(1 + e), e = exp(-|v|), with the polynomial of degree 8 that is nearest to ln(1 + e) / e over [0, 1] (by Remez's
+// method; 1.3e-7 of it off as evaluated here).
 __device__ __forceinline__ float softplus(float v) {
   float pos;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(pos) : "f"(v));
-  // exp(-m) with the roundings of log2(e) and of the product made up for
-  const float m = fminf(fabsf(v), 87.f), p = m * -kLog2e, low = fmaf(m, -1.92596299e-8f, fmaf(m, -kLog2e, -p));
+  // exp(-m) with the roundings of log2(e) and of the product made up for (of 88 it is below 2^-126 and flushed to zero)
+  const float m = fminf(fabsf(v), 88.f), p = m * -kLog2e, low = fmaf(m, -1.92596299e-8f, fmaf(m, -kLog2e, -p));
   const float e0 = exp2_fast(p), e = fmaf(e0, low * 0.6931471805599453f, e0);
   float t = 0x1.56ee0ap-8f;
   t = fmaf(t, e, -0x1.e369f2p-6f);

@@ -2,10 +2,11 @@
 
 Tolerances count roundings: half a step of bf16 is 2^-8 relative, of float32 2^-24.
 """
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_hybrid import run_scan
+from tests.test_gpu_hybrid import F32, host, near, run_scan
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,25 @@ def test_scan_workspace_serves_smaller_batches():
     ws = sv.new_scan_workspace(8, 3000, 2048, 16, "cuda")
     for B, T in ((8, 50), (1, 3000), (3, 1000)):
         run_scan(B, T, 2048, 16, torch.bfloat16, seed=T, workspace=ws)
+
+
+@pytest.mark.parametrize("T", [1, 17])
+def test_scan_steps_far_below_zero(T):
+    """softplus on both sides of where exp(v) leaves the normal numbers: as exact as elsewhere above, zero below, and a token
+    of such a step leaves the state to the bit."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    above, below = np.linspace(-87.33, -80.0, 500), np.array([-87.34, -87.5, -88.0, -88.8, -95.0, -104.0, -1e4, -3e38, -np.inf])
+    v = torch.from_numpy(np.concatenate([above, below]).astype(np.float32))
+    D, N = v.numel(), 8
+    x, b = torch.ones((1, T, D), device="cuda"), torch.ones((1, T, 1, N), device="cuda")
+    a = torch.full((D, N), -1.0, device="cuda")
+    dt = torch.full((1, T, D), -float("inf"))
+    dt[0, T // 2] = v
+    _, last = sv.spec_scan(x, dt.cuda(), a, b, b)
+    want = np.exp(v.double().numpy())[:500]          # (ln(1 + e) is e there)
+    near(host(last)[0, :500, 0], want, 13 * F32 * want - 1e-37, "softplus")
+    assert not last[0, 500:].any()
+    state = torch.randn((1, D, N), device="cuda")
+    dt[0, T // 2] = -float("inf")
+    _, last = sv.spec_scan(x, dt.cuda(), a, b, b, None, None, None, state)
+    assert torch.equal(last, state)
