@@ -87,6 +87,7 @@ int spec_conv(const spec_conv_t* conv, void* cuda_stream);
  *            group.  Channel d reads group d / (D / groups).
  *   a        [D, N] float32, at most 0: decays are exp(delta a).  With a above zero or
  *            delta below it, products of decays may overflow before the state does.
+ *            -inf forgets a finite state (but for a step of 0).
  *   skip, dt_bias  [D] float32 or NULL (zeros).
  *   state    [slots, D, N] float32 or NULL, slot, lens, flags: as in spec_conv_t.
  *   y        [B, T, D] of dtype, dense.

@@ -54,6 +54,14 @@ __device__ __forceinline__ float softplus(float v) {
   return fmaf(t, e, pos);
 }
 
+// a in powers of two.  What is below every number is the lowest, so that a step of zero, of a tile's last tokens or of a part
+// without any, leaves the state of a = -inf too.
+__device__ __forceinline__ float scan_rate(float a) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0fFF7FFFFF;" : "=f"(r) : "f"(a * kLog2e));
+  return r;
+}
+
 // exp(g) of two states, y = g log2(e).  An error of the decay adds up over the tokens that
 // the state remembers, 1 / (1 - exp(g)) of them, and that of ex2.approx leans to one side
 // (by 1e-8 to 3e-8 in the mean below |g| = 1/2, measured), so below |g| = 1/32 the series to
@@ -151,8 +159,8 @@ __global__ void __launch_bounds__(kScanStepThreads, kScanStepCtas) scan_step_ker
 #pragma unroll
   for (int m = 0; m < CK; ++m) {
     const float4 av = __ldg(reinterpret_cast<const float4*>(A.a + at + m * 4 * L));
-    a[m][0] = mul2(make_float2(av.x, av.y), both_of(kLog2e));
-    a[m][1] = mul2(make_float2(av.z, av.w), both_of(kLog2e));
+    a[m][0] = make_float2(scan_rate(av.x), scan_rate(av.y));
+    a[m][1] = make_float2(scan_rate(av.z), scan_rate(av.w));
     h[m][0] = h[m][1] = make_float2(0.f, 0.f);
     if (R.from >= 0) {
       const float4 s = *reinterpret_cast<const float4*>(A.state + (long long)R.from * A.D * N + at + m * 4 * L);
@@ -458,9 +466,9 @@ struct ScanStates {
     *reinterpret_cast<float4*>(p + d * N + q) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
     if (both) *reinterpret_cast<float4*>(p + (d + 1) * N + q) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
   }
-  __device__ __forceinline__ void times(float by) {
+  __device__ __forceinline__ void rates() {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) v[n] = mul2(v[n], both_of(by));
+    for (int n = 0; n < 4; ++n) v[n] = make_float2(scan_rate(v[n].x), scan_rate(v[n].y));
   }
 };
 
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, kScanCtas) scan_tile_kernel(
     const bool both = ch + 1 < P.left;      // (lanes without channels follow the last one)
     ScanStates a, h;
     a.load(A.a, d, N, q, both);
-    a.times(kLog2e);
+    a.rates();
     h.fill(0.f);
     if (W.segments > 1) h.load(W.states, ((long long)P.r * W.segments + P.seg) * W.fine * A.D + d, N, q, both);
     else if (R.from >= 0) h.load(A.state, (long long)R.from * A.D + d, N, q, both);
@@ -638,7 +646,7 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
     const bool both = ch + 1 < P.left;
     ScanStates a, h;
     a.load(A.a, d, N, q, both);
-    a.times(kLog2e);
+    a.rates();
     h.fill(0.f);
     float2 behind = make_float2(0.f, 0.f);           // the delta of the tiles behind this one
     __syncthreads();
@@ -682,7 +690,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
   const int d = (int)(i / L), q = (int)(i % L) * 4, r = blockIdx.y;
   const MixerRow R = mixer_row(A, r, false);
   const float4 av = *reinterpret_cast<const float4*>(A.a + (long long)d * N + q);
-  const float2 a[2] = {mul2(make_float2(av.x, av.y), both_of(kLog2e)), mul2(make_float2(av.z, av.w), both_of(kLog2e))};
+  const float2 a[2] = {make_float2(scan_rate(av.x), scan_rate(av.y)), make_float2(scan_rate(av.z), scan_rate(av.w))};
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (R.from >= 0) h = *reinterpret_cast<const float4*>(A.state + ((long long)R.from * A.D + d) * N + q);
 #pragma unroll 8

@@ -67,3 +67,25 @@ def test_scan_steps_far_below_zero(T):
     dt[0, T // 2] = -float("inf")
     _, last = sv.spec_scan(x, dt.cuda(), a, b, b, None, None, None, state)
     assert torch.equal(last, state)
+
+
+@pytest.mark.parametrize("T", [3, 16, 33, 1000])
+def test_scan_states_that_are_forgotten_at_once(T):
+    """a of -inf and of the lowest numbers: a state is what the last token puts in, whatever the row's length, and a row
+    without tokens keeps what it had."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    D, N, lens = 24, 8, [T, T // 2 + 1, 1, 0]
+    x, b, c = (torch.randn(s, device="cuda") for s in ((4, T, D), (4, T, 1, N), (4, T, 1, N)))
+    dt = torch.rand((4, T, D), device="cuda") + 0.01
+    state = torch.randn((4, D, N), device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    a = -torch.rand((D, N), device="cuda")
+    got = []
+    for low in (-2e38, -3.4e38, -float("inf")):
+        a[1::2, 3] = low
+        got.append(sv.spec_scan(x, dt, a, b, c, None, None, None, state, None, n, softplus=False))
+    for y, last in got:
+        assert torch.isfinite(y).all() and torch.equal(y, got[0][0]) and torch.equal(last, got[0][1])
+        for r, m in enumerate(lens):
+            want = host(dt[r, m - 1, 1::2]) * host(x[r, m - 1, 1::2]) * host(b[r, m - 1, 0, 3]) if m else host(state[r, 1::2, 3])
+            near(host(last[r, 1::2, 3]), want, 2.1 * F32 * np.abs(want), "last")
