@@ -147,7 +147,8 @@ size_t spec_scan_workspace_size(int B, int T, int D, int N);
  *   y_t[d] = (sum_n c_t[n] h_t[d, n] + skip[d] x_t[d]) * (z_t[d] / (1 + exp(-z_t[d]))),
  * the last factor only with z.  A token of delta 0 leaves the state.  N is 8, 16, 32,
  * 64 or 128; B at most 65535, T SPEC_MAX_LENGTH, D 2^24 and a multiple of
- * groups.  States and sums are float32.
+ * groups.  States and sums are float32.  A state that has become infinite stays so
+ * while the decays of single tokens are 2^-126 and more (below, it may be NaN).
  * state, states, last and a are aligned to 16 bytes, the others to their elements.
  * Errors: SPEC_E_NULL, SPEC_E_DIM, SPEC_E_DTYPE, SPEC_E_ALIGN, SPEC_E_WORKSPACE,
  * SPEC_E_ARCH, SPEC_E_CUDA. */

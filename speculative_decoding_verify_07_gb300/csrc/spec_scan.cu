@@ -681,6 +681,12 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
   }
 }
 
+// exp2(y) h + put for a part's y, k = exp2(y): an infinite h stays what it is, as it does token by token, where no decay is
+// rounded to zero though all of them together are.
+__device__ __forceinline__ float scan_enter(float k, float y, float h, float put) {
+  return fmaf(k == 0.f && y > -INFINITY && fabsf(h) == INFINITY ? 1.f : k, h, put);
+}
+
 // Walks the parts of four states: what is behind one enters the next.
 template <int N>
 __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs A, const ScanSplit W) {
@@ -700,8 +706,9 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs 
     const float4 put = *p;
     const float sum = W.sums[at];
     *p = h;
-    const float2 k0 = scan_decay(mul2(both_of(sum), a[0])), k1 = scan_decay(mul2(both_of(sum), a[1]));
-    h = make_float4(fmaf(k0.x, h.x, put.x), fmaf(k0.y, h.y, put.y), fmaf(k1.x, h.z, put.z), fmaf(k1.y, h.w, put.w));
+    const float2 y0 = mul2(both_of(sum), a[0]), y1 = mul2(both_of(sum), a[1]), k0 = scan_decay(y0), k1 = scan_decay(y1);
+    h = make_float4(scan_enter(k0.x, y0.x, h.x, put.x), scan_enter(k0.y, y0.y, h.y, put.y), scan_enter(k1.x, y1.x, h.z, put.z),
+                    scan_enter(k1.y, y1.y, h.w, put.w));
   }
 }
 

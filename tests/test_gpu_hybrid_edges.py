@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import hybrid as oh
 from tests.test_gpu_hybrid import F32, host, near, run_scan
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,35 @@ def test_scan_states_that_are_forgotten_at_once(T):
         for r, m in enumerate(lens):
             want = host(dt[r, m - 1, 1::2]) * host(x[r, m - 1, 1::2]) * host(b[r, m - 1, 0, 3]) if m else host(state[r, 1::2, 3])
             near(host(last[r, 1::2, 3]), want, 2.1 * F32 * np.abs(want), "last")
+
+
+def infinite_scan(T, edit):
+    """A scan of fast states (decays of a token from exp(-0.1) to exp(-16), none of more than a few tokens above 2^-126) with
+    something infinite put in by `edit`, against the oracle: the same infinities and NaN, and all else as ever."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    rng = np.random.default_rng(T)
+    B, D, N = 2, 24, 16
+    x, b, c = (rng.standard_normal(s).astype(np.float32) for s in ((B, T, D), (B, T, 1, N), (B, T, 1, N)))
+    dt = rng.uniform(0.1, 1.0, (B, T, D)).astype(np.float32)
+    a = np.tile(-np.arange(1.0, N + 1), (D, 1)).astype(np.float32)
+    state = rng.standard_normal((B, D, N)).astype(np.float32)
+    edit(x, b, state)
+    move = lambda v: torch.from_numpy(v).cuda()
+    y, last = sv.spec_scan(move(x), move(dt), move(a), move(b), move(c), None, None, None, move(state), softplus=False)
+    with np.errstate(all="ignore"):
+        wy, wl, _, (ey, el, _) = oh.scan(x, dt, a, b, c, None, None, None, state, [T] * B, False)
+    for got, want, err in ((host(y), wy, F32 * ey + F32 * np.abs(wy)), (host(last), wl, F32 * el)):
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+        there = np.isfinite(want)
+        near(got[there], want[there], err[there], "finite")
+    return wl
+
+
+@pytest.mark.parametrize("T", [3, 40, 300, 1500])
+def test_scan_infinite_states_stay(T):
+    def edit(x, b, state):
+        state[0, 3] = np.inf
+        state[0, 4, ::2] = -np.inf
+        state[1, 23, 15] = np.inf
+    wl = infinite_scan(T, edit)
+    assert np.isinf(wl[0, 3]).all() and np.isinf(wl[1, 23, 15])
