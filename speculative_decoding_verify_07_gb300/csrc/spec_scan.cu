@@ -611,6 +611,12 @@ __global__ void __launch_bounds__(2 * kScanThreads, kScanCtas) scan_tile_kernel(
   }
 }
 
+// k h + put, k = exp2(y) of many tokens: an infinite h stays what it is, as it does token by token, where no decay is rounded
+// to zero though all of them together are.
+__device__ __forceinline__ float scan_enter(float k, float y, float h, float put) {
+  return fmaf(k == 0.f && y > -INFINITY && fabsf(h) == INFINITY ? 1.f : k, h, put);
+}
+
 // The state behind a segment that begins with zeros, from its last token to the first:
 // sum_t exp(a (delta of the tokens after t)) delta_t x_t b_t.  Each weight is taken by
 // itself, so nothing adds up.
@@ -654,6 +660,7 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
     for (int k = 0; k < tiles; ++k) {
       const typename Shared::Tile& tile = sm.tile[k & 1];
       scan_wait<kScanMade>(k & 1);
+      const ScanStates was = h;
       float2 here = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int t = kScanTile - 1; t >= 0; --t) {
@@ -667,6 +674,24 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
         }
         here = add2(here, make_float2(s.x, s.y));
       }
+      // (of what is not finite the tile is taken again)
+      const float2 some = add2(add2(h.v[0], h.v[1]), add2(h.v[2], h.v[3]));
+      if (__builtin_expect(!(fabsf(some.x) + fabsf(some.y) < INFINITY), 0)) {
+        h = was;
+        here = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int t = kScanTile - 1; t >= 0; --t) {
+          const float4 b = *reinterpret_cast<const float4*>(&tile.b[t][q]), s = tile.step[t][ch / 2];
+          const float bb[4] = {b.x, b.y, b.z, b.w};
+          const float2 far = add2(behind, here);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float2 e = mul2(far, a.v[n]), put = mul2(make_float2(s.z, s.w), both_of(bb[n]));
+            h.v[n] = make_float2(scan_enter(exp2_fast(e.x), e.x, put.x, h.v[n].x), scan_enter(exp2_fast(e.y), e.y, put.y, h.v[n].y));
+          }
+          here = add2(here, make_float2(s.x, s.y));
+        }
+      }
       scan_tell<kScanWalked>(k & 1);
       behind = add2(behind, here);
     }
@@ -679,12 +704,6 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
       }
     }
   }
-}
-
-// exp2(y) h + put for a part's y, k = exp2(y): an infinite h stays what it is, as it does token by token, where no decay is
-// rounded to zero though all of them together are.
-__device__ __forceinline__ float scan_enter(float k, float y, float h, float put) {
-  return fmaf(k == 0.f && y > -INFINITY && fabsf(h) == INFINITY ? 1.f : k, h, put);
 }
 
 // Walks the parts of four states: what is behind one enters the next.

@@ -122,3 +122,32 @@ def test_scan_infinite_states_stay(T):
         state[1, 23, 15] = np.inf
     wl = infinite_scan(T, edit)
     assert np.isinf(wl[0, 3]).all() and np.isinf(wl[1, 23, 15])
+
+
+@pytest.mark.parametrize("T", [3, 40, 300, 1500])
+def test_scan_infinite_inputs_stay(T):
+    """Infinities in the first, a middle and the last token; opposite ones cancel to NaN, also against an infinite state."""
+    def edit(x, b, state):
+        x[0, 0, 3] = np.inf
+        x[0, T // 2, 5] = -np.inf
+        x[0, T - 1, 6] = np.inf
+        x[0, 1, 7], x[0, T - 2, 7] = np.inf, -np.inf
+        b[1, T // 2, 0, 2] = -np.inf
+        state[0, 9], x[0, T // 2, 9] = np.inf, -np.inf
+    wl = infinite_scan(T, edit)
+    assert np.isinf(wl[0, 3]).all() and np.isinf(wl[1, :, 2]).all() and not np.isfinite(wl[0, 9]).any()
+
+
+def test_scan_infinite_inputs_leave_the_others_alone():
+    """The same bits in all channels and rows that nothing infinite enters."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, T, D, N = 2, 2000, 24, 16
+    x, dt, b = (torch.randn(s, device="cuda") for s in ((B, T, D), (B, T, D), (B, T, 1, N)))
+    a = -torch.rand((D, N), device="cuda")
+    want = [t.clone() for t in sv.spec_scan(x, dt, a, b, b)]
+    x[0, 700, 5] = float("inf")
+    got = sv.spec_scan(x, dt, a, b, b)
+    others = torch.tensor([d for d in range(D) if d != 5], device="cuda")
+    for g, w, channels in zip(got, want, (1, 0)):
+        assert torch.equal(g[1], w[1]) and torch.equal(g[0].index_select(channels, others), w[0].index_select(channels, others))
+    assert torch.isinf(got[1][0, 5]).all()
