@@ -352,9 +352,10 @@ inline int launch_early(Kernel kernel, unsigned ctas, int threads, int smem, cud
   return cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
-// Whether items of up to `rows` query rows go to the many-rows kernel, and the query rows of a tile.
+// Whether items of up to `rows` query rows go to the many-rows kernel, and the query rows and the positions of a tile.
 bool attend_is_wide(bool e4m3, long long rows);
 int attend_tile_rows(bool e4m3, long long rows);
+int attend_tile_positions(bool e4m3, long long rows);
 
 // Either of them, for items of up to `rows` query rows.
 template <int PART>

@@ -30,10 +30,14 @@ namespace specv {
 constexpr int kGroupThreads = 1024;
 
 // Finds what each group has in common: shared_len, but nothing behind the first new token of any of its rows or
-// beyond the page table, in whole tiles, and nothing for a single row.  A warp a group.
+// beyond the page table, in whole tiles, and nothing for a single row.  A warp a group.  Where that would be more tiles, of
+// tile_rows query rows by tile_positions, than the attention over it takes, nothing is in common: the rows' own attention, of
+// no fewer, then answers for the call, or refuses it.
 static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(const PagedCache C, int N, const int32_t* shared_rows, const int32_t* shared_len,
-                                                                      int groups, int32_t* group_row, int32_t* group_cu, int32_t* group_len,
-                                                                      int32_t* own_from) {
+                                                                      int groups, int group, int tile_rows, int tile_positions, int32_t* group_row,
+                                                                      int32_t* group_cu, int32_t* group_len, int32_t* own_from) {
+  __shared__ unsigned long long tiles;       // of a head
+  if (threadIdx.x == 0) tiles = 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   bool ok = true;
   for (int g = threadIdx.x; g < groups; g += kGroupThreads) {
@@ -62,6 +66,7 @@ static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(con
     if (busy > 1) len = max(0, min(min(least, __ldg(shared_len + g)), C.max_pages * C.page_size)) / kCommonTile * kCommonTile;
     for (int r = a + lane; r < b; r += 32) own_from[r] = __ldg(C.cu + r + 1) > __ldg(C.cu + r) ? len : 0;
     if (lane == 0) {
+      if (len > 0) atomicAdd(&tiles, (unsigned long long)(((long long)(t1 - t0) * group + tile_rows - 1) / tile_rows * (len / tile_positions)));
       group_len[g] = len;
       group_row[g] = a;
       group_cu[g] = t0;
@@ -71,6 +76,10 @@ static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(con
       }
     }
   }
+  __syncthreads();
+  if (tiles * C.heads <= 0x7fffffffull) return;
+  for (int g = threadIdx.x; g < groups; g += kGroupThreads) group_len[g] = 0;
+  for (int r = threadIdx.x; r < C.B; r += kGroupThreads) own_from[r] = 0;
 }
 
 constexpr int kPartsThreads = 256;
@@ -173,8 +182,6 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   int32_t* const group_cu = reinterpret_cast<int32_t*>(base + S.group_cu);
   int32_t* const group_len = reinterpret_cast<int32_t*>(base + S.group_len);
   int32_t* const own_from = reinterpret_cast<int32_t*>(base + S.own_from);
-  attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group_row, group_cu, group_len, own_from);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_E_CUDA;
   A.group_row = group_row;
   A.own_from = own_from;
   A.common = reinterpret_cast<float*>(base + S.out);
@@ -184,6 +191,9 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   // a group's tokens are not known here: as many as each would have of all
   const long long common_rows = ((long long)N + groups - 1) / groups * group;
   A.common_rows = attend_tile_rows(e4m3, common_rows);
+  attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group, A.common_rows,
+                                                    attend_tile_positions(e4m3, common_rows), group_row, group_cu, group_len, own_from);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_E_CUDA;
   A.common_tiles = (long long)N * group / A.common_rows + groups + 1;
   AttendArgs common = A;
   common.C.B = groups;

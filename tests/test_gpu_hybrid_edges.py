@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import forward as of
 from oracle import hybrid as oh
 from tests.test_gpu_hybrid import F32, host, near, run_scan
 
@@ -151,3 +152,32 @@ def test_scan_infinite_inputs_leave_the_others_alone():
     for g, w, channels in zip(got, want, (1, 0)):
         assert torch.equal(g[1], w[1]) and torch.equal(g[0].index_select(channels, others), w[0].index_select(channels, others))
     assert torch.isinf(got[1][0, 5]).all()
+
+
+# -------------------------------------------------------- the shared attention
+
+@pytest.mark.parametrize("group", [1, 40])
+def test_more_common_tiles_than_a_call_takes(group):
+    """2^31 tiles and more (two rows that see one page again and again): as spec_attend, nothing is written and row 0 flagged;
+    the workspace serves on."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    heads, page, most, dim = 140, 4096, 524287, 64
+    kv = torch.randn((1, heads, page, dim), device="cuda").to(torch.bfloat16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table = torch.zeros((2, most), dtype=torch.int32, device="cuda")
+    q = torch.randn((2, heads * group, dim), device="cuda").to(torch.bfloat16)
+    ws = sv.new_attend_shared_workspace(2, 2, heads, group, dim, "cuda")
+
+    def call(kv_len):
+        out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        flags = i32(0, 0)
+        sv.spec_attend_shared(q, i32(0, 2), i32(0x7fffffff), i32(0, 1, 2), i32(*kv_len), table, kv, kv, max_tokens=1, out=out, lse=lse,
+                              flags=flags, workspace=ws)
+        return out, lse, flags.tolist()
+
+    want = call((700, 650))
+    assert want[2] == [0, 0] and torch.isfinite(want[1]).all() and (want[0] != 7).all()
+    out, lse, flags = call((most * page, most * page))
+    assert flags == [of.F_BAD_IDX, 0] and (out == 7).all() and (lse == 7).all()
+    again = call((700, 650))
+    assert again[2] == [0, 0] and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
