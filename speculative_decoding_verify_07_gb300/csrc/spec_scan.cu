@@ -611,12 +611,6 @@ __global__ void __launch_bounds__(2 * kScanThreads, kScanCtas) scan_tile_kernel(
   }
 }
 
-// k h + put, k = exp2(y) of many tokens: an infinite h stays what it is, as it does token by token, where no decay is rounded
-// to zero though all of them together are.
-__device__ __forceinline__ float scan_enter(float k, float y, float h, float put) {
-  return fmaf(k == 0.f && y > -INFINITY && fabsf(h) == INFINITY ? 1.f : k, h, put);
-}
-
 // The state behind a segment that begins with zeros, from its last token to the first:
 // sum_t exp(a (delta of the tokens after t)) delta_t x_t b_t.  Each weight is taken by
 // itself, so nothing adds up.
@@ -660,7 +654,6 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
     for (int k = 0; k < tiles; ++k) {
       const typename Shared::Tile& tile = sm.tile[k & 1];
       scan_wait<kScanMade>(k & 1);
-      const ScanStates was = h;
       float2 here = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int t = kScanTile - 1; t >= 0; --t) {
@@ -673,24 +666,6 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
           h.v[n] = fma2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), mul2(put, both_of(bb[n])), h.v[n]);
         }
         here = add2(here, make_float2(s.x, s.y));
-      }
-      // (of what is not finite the tile is taken again)
-      const float2 some = add2(add2(h.v[0], h.v[1]), add2(h.v[2], h.v[3]));
-      if (__builtin_expect(!(fabsf(some.x) + fabsf(some.y) < INFINITY), 0)) {
-        h = was;
-        here = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int t = kScanTile - 1; t >= 0; --t) {
-          const float4 b = *reinterpret_cast<const float4*>(&tile.b[t][q]), s = tile.step[t][ch / 2];
-          const float bb[4] = {b.x, b.y, b.z, b.w};
-          const float2 far = add2(behind, here);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float2 e = mul2(far, a.v[n]), put = mul2(make_float2(s.z, s.w), both_of(bb[n]));
-            h.v[n] = make_float2(scan_enter(exp2_fast(e.x), e.x, put.x, h.v[n].x), scan_enter(exp2_fast(e.y), e.y, put.y, h.v[n].y));
-          }
-          here = add2(here, make_float2(s.x, s.y));
-        }
       }
       scan_tell<kScanWalked>(k & 1);
       behind = add2(behind, here);
@@ -706,28 +681,78 @@ __global__ void __launch_bounds__(2 * kScanThreads) scan_segment_kernel(const Sc
   }
 }
 
-// Walks the parts of four states: what is behind one enters the next.
-template <int N>
+// k h + put, k = exp2(y) of many tokens: an infinite h stays what it is, as it does token by token, where no decay is rounded
+// to zero though all of them together are.
+__device__ __forceinline__ float scan_enter(float k, float y, float h, float put) {
+  return fmaf(k == 0.f && y > -INFINITY && fabsf(h) == INFINITY ? 1.f : k, h, put);
+}
+
+// What scan_segment_kernel left of a part's four states, anew, for a part where that is not finite: an infinite term stays in
+// the sum although its weight is rounded to zero.  (From memory and by the join: a look at each tile in the first pass cost it
+// a CTA an SM, 1x32768x2048 658 us.)
+template <bool BF16>
+__device__ __noinline__ float4 scan_again(const ScanArgs& A, int r, int d, long long b, float4 a, int first, int end) {
+  const float bias = A.dt_bias ? __ldg(A.dt_bias + d) : 0.f;
+  float behind = 0.f, here = 0.f;
+  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int t = end - 1; t >= first; --t) {
+    float delta = load_one<BF16>(A.dt, r * A.dt_row + t * A.dt_tok + d) + bias;
+    if (A.softplus) delta = softplus(delta);
+    const float far = behind + here, in = delta * load_one<BF16>(A.x, r * A.x_row + t * A.x_tok + d);
+    auto add = [&](float& to, float rate, int n) {
+      const float e = far * rate;
+      to = scan_enter(exp2_fast(e), e, in * load_one<BF16>(A.b, b + t * A.b_tok + n), to);
+    };
+    add(h.x, a.x, 0), add(h.y, a.y, 1), add(h.z, a.z, 2), add(h.w, a.w, 3);
+    here += delta;
+    // (summed up tile by tile, as there)
+    if ((t - first) % kScanTile == 0) behind += here, here = 0.f;
+    if (h.x != h.x && h.y != h.y && h.z != h.z && h.w != h.w) break;
+  }
+  return h;
+}
+
+// Walks the parts of four states, eight parts' loads at a time: what is behind one enters the next.  (1x32768x2048 631 us in
+// all, 646 with a part's loads behind the last one's store.)
+template <bool BF16, int N>
 __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const ScanArgs A, const ScanSplit W) {
-  constexpr int L = N / 4;
+  constexpr int L = N / 4, ahead = 8;
   const long long i = (long long)blockIdx.x * kScanThreads + threadIdx.x;
   if (i >= (long long)A.D * L) return;
-  const int d = (int)(i / L), q = (int)(i % L) * 4, r = blockIdx.y;
+  const int d = (int)(i / L), q = (int)(i % L) * 4, r = blockIdx.y, parts = W.segments * W.fine, span = W.span / W.fine;
   const MixerRow R = mixer_row(A, r, false);
   const float4 av = *reinterpret_cast<const float4*>(A.a + (long long)d * N + q);
-  const float2 a[2] = {make_float2(scan_rate(av.x), scan_rate(av.y)), make_float2(scan_rate(av.z), scan_rate(av.w))};
+  const float4 a = make_float4(scan_rate(av.x), scan_rate(av.y), scan_rate(av.z), scan_rate(av.w));
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (R.from >= 0) h = *reinterpret_cast<const float4*>(A.state + ((long long)R.from * A.D + d) * N + q);
-#pragma unroll 8
-  for (int s = 0; s < W.segments * W.fine; ++s) {
-    const long long at = ((long long)r * W.segments * W.fine + s) * A.D + d;
-    float4* const p = reinterpret_cast<float4*>(W.states + at * N + q);
-    const float4 put = *p;
-    const float sum = W.sums[at];
-    *p = h;
-    const float2 y0 = mul2(both_of(sum), a[0]), y1 = mul2(both_of(sum), a[1]), k0 = scan_decay(y0), k1 = scan_decay(y1);
-    h = make_float4(scan_enter(k0.x, y0.x, h.x, put.x), scan_enter(k0.y, y0.y, h.y, put.y), scan_enter(k1.x, y1.x, h.z, put.z),
-                    scan_enter(k1.y, y1.y, h.w, put.w));
+  auto finite = [](float4 v) { return fabsf((v.x + v.y) + (v.z + v.w)) < INFINITY; };
+#pragma unroll 1
+  for (int s0 = 0; s0 < parts; s0 += ahead) {
+    float4 put[ahead];
+    float sum[ahead];
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < ahead; ++j) {
+      const long long at = ((long long)r * parts + min(s0 + j, parts - 1)) * A.D + d;
+      put[j] = *reinterpret_cast<const float4*>(W.states + at * N + q);
+      sum[j] = W.sums[at];
+    }
+#pragma unroll
+    for (int j = 0; j < ahead; ++j) odd = odd || !finite(put[j]);
+#pragma unroll
+    for (int j = 0; j < ahead; ++j) {
+      if (s0 + j >= parts) break;
+      if (odd && !finite(put[j])) {
+        const int first = (s0 + j) * span, end = min((int)min((long long)first + span, (long long)A.T), R.len);
+        put[j] = scan_again<BF16>(A, r, d, r * A.b_row + d / A.each * A.b_group + q, a, first, end);
+      }
+      *reinterpret_cast<float4*>(W.states + (((long long)r * parts + s0 + j) * A.D + d) * N + q) = h;
+      const float2 y0 = mul2(both_of(sum[j]), make_float2(a.x, a.y)), y1 = mul2(both_of(sum[j]), make_float2(a.z, a.w));
+      const float2 k0 = scan_decay(y0), k1 = scan_decay(y1);
+      h = make_float4(scan_enter(k0.x, y0.x, h.x, put[j].x), scan_enter(k0.y, y0.y, h.y, put[j].y),
+                      scan_enter(k1.x, y1.x, h.z, put[j].z), scan_enter(k1.y, y1.y, h.w, put[j].w));
+    }
   }
 }
 
@@ -747,7 +772,7 @@ static int launch_tiles(const ScanArgs& A, bool pairs, char* workspace, cudaStre
     if (!allow_shared(reinterpret_cast<const void*>(scan_segment_kernel<BF16, N, VEC>), less, &allowed)) return SPEC_E_CUDA;
     scan_segment_kernel<BF16, N, VEC><<<dim3(grid.x * W.fine, A.B), 2 * kScanThreads, less, st>>>(A, W, pairs);
     const dim3 joins((unsigned)(((long long)A.D * S::L + kScanThreads - 1) / kScanThreads), A.B);
-    scan_join_kernel<N><<<joins, kScanThreads, 0, st>>>(A, W);
+    scan_join_kernel<BF16, N><<<joins, kScanThreads, 0, st>>>(A, W);
   }
   static std::atomic<unsigned long long> allowed[2];
   const auto gated = scan_tile_kernel<BF16, N, VEC, true>, plain = scan_tile_kernel<BF16, N, VEC, false>;

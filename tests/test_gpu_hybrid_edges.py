@@ -8,7 +8,7 @@ import torch
 
 from oracle import forward as of
 from oracle import hybrid as oh
-from tests.test_gpu_hybrid import F32, host, near, run_scan
+from tests.test_gpu_hybrid import DT, F32, half, host, near, run_scan
 
 pytestmark = pytest.mark.gpu
 
@@ -152,6 +152,28 @@ def test_scan_infinite_inputs_leave_the_others_alone():
     for g, w, channels in zip(got, want, (1, 0)):
         assert torch.equal(g[1], w[1]) and torch.equal(g[0].index_select(channels, others), w[0].index_select(channels, others))
     assert torch.isinf(got[1][0, 5]).all()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D", [24, 26])
+def test_scan_infinite_inputs_of_groups_and_ragged_rows(D, dtype):
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, T, N, lens = 3, 1300, 8, [1300, 901, 130]
+    gen = torch.Generator().manual_seed(D)
+    x, dt = (torch.randn((B, T, D), generator=gen).to(dtype) for _ in range(2))
+    b, c = (torch.randn((B, T, 2, N), generator=gen).to(dtype) for _ in range(2))
+    a, skip, bias = -torch.arange(1.0, N + 1).repeat(D, 1), torch.randn(D, generator=gen), torch.ones(D)
+    x[0, 100, 3], x[0, 700, D - 1], x[1, 880, 5], x[2, 0, 7] = float("inf"), -float("inf"), float("inf"), float("inf")
+    b[1, 300, 1, 4] = float("inf")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    y, last = sv.spec_scan(*(v.cuda() for v in (x, dt, a, b, c, skip)), None, bias.cuda(), lens=n)
+    with np.errstate(all="ignore"):
+        wy, wl, _, (ey, el, _) = oh.scan(*(host(v) for v in (x, dt, a, b, c, skip)), None, host(bias), np.zeros((B, D, N)), lens, True)
+    for got, want, err in ((host(y), wy, half(dtype) * np.abs(wy) + F32 * ey), (host(last), wl, F32 * el)):
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+        there = np.isfinite(want)
+        near(got[there], want[there], err[there], "finite")
+    assert np.isinf(wl[0, 3]).all() and np.isinf(wl[1, D // 2:, 4]).all() and np.isfinite(wl[1, :5]).all()
 
 
 # -------------------------------------------------------- the shared attention
