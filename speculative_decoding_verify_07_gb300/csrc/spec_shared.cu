@@ -31,8 +31,8 @@ constexpr int kGroupThreads = 1024;
 
 // Finds what each group has in common: shared_len, but nothing behind the first new token of any of its rows or
 // beyond the page table, in whole tiles, and nothing for a single row.  A warp a group.  Where that would be more tiles, of
-// tile_rows query rows by tile_positions, than the attention over it takes, nothing is in common: the rows' own attention, of
-// no fewer, then answers for the call, or refuses it.
+// 2^tile_rows query rows by 2^tile_positions, than the attention over it takes, nothing is in common: the rows' own attention,
+// of no fewer, then answers for the call, or refuses it.
 static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(const PagedCache C, int N, const int32_t* shared_rows, const int32_t* shared_len,
                                                                       int groups, int group, int tile_rows, int tile_positions, int32_t* group_row,
                                                                       int32_t* group_cu, int32_t* group_len, int32_t* own_from) {
@@ -66,7 +66,7 @@ static __global__ void __launch_bounds__(kGroupThreads) attend_groups_kernel(con
     if (busy > 1) len = max(0, min(min(least, __ldg(shared_len + g)), C.max_pages * C.page_size)) / kCommonTile * kCommonTile;
     for (int r = a + lane; r < b; r += 32) own_from[r] = __ldg(C.cu + r + 1) > __ldg(C.cu + r) ? len : 0;
     if (lane == 0) {
-      if (len > 0) atomicAdd(&tiles, (unsigned long long)(((long long)(t1 - t0) * group + tile_rows - 1) / tile_rows * (len / tile_positions)));
+      if (len > 0) atomicAdd(&tiles, (unsigned long long)((((long long)(t1 - t0) * group - 1) >> tile_rows) + 1) * (len >> tile_positions));
       group_len[g] = len;
       group_row[g] = a;
       group_cu[g] = t0;
@@ -121,6 +121,12 @@ static __global__ void __launch_bounds__(kPartsThreads) attend_parts_kernel(cons
     __stcg(reinterpret_cast<float4*>(A.common + at * D + d), make_float4(x.x * by, x.y * by, x.z * by, x.w * by));
     if (d == 0) __stcg(A.common_lse + at, sum == 0.f ? -INFINITY : top + log2f(sum));
   }
+}
+
+static int log2_of(int power) {
+  int n = 0;
+  while (power >> (n + 1)) ++n;
+  return n;
 }
 
 // Workspace, behind that of spec_attend (which serves the rows' own positions): the groups' rows, tokens and lengths, the
@@ -191,8 +197,9 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   // a group's tokens are not known here: as many as each would have of all
   const long long common_rows = ((long long)N + groups - 1) / groups * group;
   A.common_rows = attend_tile_rows(e4m3, common_rows);
-  attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group, A.common_rows,
-                                                    attend_tile_positions(e4m3, common_rows), group_row, group_cu, group_len, own_from);
+  attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group,
+                                                    log2_of(A.common_rows), log2_of(attend_tile_positions(e4m3, common_rows)), group_row,
+                                                    group_cu, group_len, own_from);
   if (cudaGetLastError() != cudaSuccess) return SPEC_E_CUDA;
   A.common_tiles = (long long)N * group / A.common_rows + groups + 1;
   AttendArgs common = A;
