@@ -8,7 +8,9 @@ import torch
 
 from oracle import forward as of
 from oracle import hybrid as oh
+from tests.test_gpu_forward import Batch
 from tests.test_gpu_hybrid import DT, F32, half, host, near, run_scan
+from tests.test_gpu_shared import check, share
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +205,62 @@ def test_more_common_tiles_than_a_call_takes(group):
     assert flags == [of.F_BAD_IDX, 0] and (out == 7).all() and (lse == 7).all()
     again = call((700, 650))
     assert again[2] == [0, 0] and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("most", [3, 4096])
+def test_more_groups_and_rows_than_a_cta_has_warps_and_threads(most, pool):
+    """1040 rows in 90 groups of uneven sizes, some empty, some of one row, rows of no group before and behind them."""
+    rng = np.random.default_rng(7)
+    new = rng.integers(0, 3, 1040)
+    new[[10, 600, 1039]] = 4, 3, 2
+    rows = np.sort(rng.integers(7, 1030, 91))
+    rows[20] = rows[21] = rows[19]
+    lens = rng.integers(0, 420, 90).tolist()
+    total = new + rng.integers(100, 240, 1040)
+    b = Batch(new.tolist(), total.tolist(), page=32, heads=1, dim=64, pool=pool, seed=21)
+    share(b, rows.tolist(), lens)
+    check(b, 2, rows.tolist(), lens, max_tokens=most)
+
+
+# ------------------------------------------------------------------ the ranges
+
+def test_the_longest_rows():
+    """SPEC_MAX_LENGTH tokens of one value each (strides of zero), which both operators soon answer alike: offsets, tiles and
+    segments count in 64 bits where 32 do not hold them."""
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    T, N, n = 0x7fffff00, 8, 0x7fffff00 - 1000
+    one = torch.ones((1, 1, 1), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5], [0.25], [2.0]], device="cuda")
+    y, last = sv.spec_conv(one.expand(1, T, 1), w, lens=lens, silu=False)
+    assert y[0, :2, 0].tolist() == [2.0, 2.25] and (y[0, 2:n:1000003] == 2.75).all() and (y[0, n - 3:n] == 2.75).all()
+    assert not y[0, n:].any() and (last == 1).all()
+    del y
+    b = torch.ones((1, 1, 1, N), dtype=torch.bfloat16, device="cuda").expand(1, T, 1, N)
+    a = -torch.arange(1, N + 1, device="cuda").float().view(1, N)
+    y, last = sv.spec_scan(one.expand(1, T, 1), (0.5 * one).expand(1, T, 1), a, b, b, lens=lens, softplus=False)
+    # h = 1/2 (1 + e + e^2 + ...) with e = exp(a / 2), 1 / (1 - e) tokens remembered, each with less than 30 roundings as the
+    # oracle counts them
+    e = np.exp(-0.5 * np.arange(1, N + 1))
+    want = 0.5 / (1 - e)
+    near(host(last)[0, 0], want, 30 * F32 * want / (1 - e), "last")
+    some = host(torch.cat([y[0, 100:n:1000003, 0], y[0, n - 100:n, 0]]))
+    near(some, np.full_like(some, want.sum()), half(torch.bfloat16) * want.sum() + 300 * F32, "y")
+    assert not y[0, n:].any()
+
+
+def test_the_most_rows():
+    from speculative_decoding_verify_07_gb300 import binding as sv
+    B, C, N = 65535, 9, 8
+    x, dt, b = (torch.randn(s, device="cuda") for s in ((B, 1, C), (B, 1, C), (B, 1, 1, N)))
+    w, a = torch.randn((3, C), device="cuda"), -torch.rand((C, N), device="cuda")
+    y, last = sv.spec_conv(x, w, silu=False)
+    assert torch.equal(y[:, 0], x[:, 0] * w[2]) and torch.equal(last[:, 1], x[:, 0]) and not last[:, 0].any()
+    y, last = sv.spec_scan(x, dt, a, b, b, softplus=False)
+    want = (dt[:, 0] * x[:, 0])[..., None] * b[:, 0]
+    assert torch.equal(last, want)
+    full = (want.double() * b[:, 0].double()).sum(-1)
+    near(host(y)[:, 0], host(full), 2 * N * F32 * host((want * b[:, 0]).abs().sum(-1)), "y")
+    with pytest.raises(sv.SpecError):
+        sv.spec_conv(torch.zeros((B + 1, 1, 1), device="cuda"), torch.ones((2, 1), device="cuda"))
