@@ -961,7 +961,8 @@ def spec_attend_shared(q, shared_rows, shared_len, cu_tokens, kv_len, page_table
 
     shared_rows [groups + 1] int32: group g are rows shared_rows[g] .. shared_rows[g + 1] - 1; shared_len [groups] int32: the
     positions that they share, read through the page table of the group's first row.  All else as for spec_attend, but
-    for the workspace, which new_attend_shared_workspace makes.
+    for the workspace, which new_attend_shared_workspace makes.  It pays for many rows of few tokens behind a long prompt (64
+    rows behind 1000 positions, 8 behind 12,000; see the header); otherwise spec_attend is the faster.
     """
     view, B, heads, head_dim = _cache_view(cu_tokens, kv_len, page_table, k_pages, v_pages, k_exp, v_exp, flags)
     dev = k_pages.device

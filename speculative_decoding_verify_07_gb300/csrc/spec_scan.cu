@@ -9,9 +9,9 @@
 // 64x3 tokens of 4096 channels by 16 states 26 us, 3300 GB/s).  Many tokens: tiles of
 // tokens, see below; a long row is split where there are few channels.
 //
-// Measured, 16 states, bf16, gate and softplus: 4x2048 tokens x 4096 channels 215 us (537 M
-// states, 2.5 T states a second), 16x1024x4096 362 us, 1x4096x4096 184 us (four
-// segments), 1x32768x2048 649 us.
+// Measured, 16 states, bf16, gate and softplus: 4x2048 tokens x 4096 channels 213 us (537 M
+// states, 2.5 T states a second), 16x1024x4096 360 us, 1x4096x4096 181 us (four
+// segments), 1x32768x2048 631 us.
 #include <algorithm>
 
 #include "spec_mixer.cuh"

@@ -30,7 +30,7 @@ inline int scan_blocks(int D, int each, int N) {
 }
 
 // Segments a row at most: one where there are CTAs for most SMs, otherwise as many as fill all of them once.  The first pass
-// makes a split cost half as much again: 64 CTAs of 4096 tokens take 184 us in four segments, 247 in one, and a row of 512
+// makes a split cost half as much again: 64 CTAs of 4096 tokens take 181 us in four segments, 247 in one, and a row of 512
 // tokens 37 and 34; 256 CTAs of 2048 tokens took 220 us whole and 300 and more in two.
 inline long long scan_want(long long ctas) { return ctas >= 100 ? 1 : std::max(1ll, 152 * kScanCtas / ctas); }
 

@@ -17,7 +17,13 @@
 // 152 CTAs, each at its beginning and end more than half the time), 5 to 10 to join them, 45 for
 // the own ones.  16 groups of 8 rows, 6001 common positions, 8 bits 141 us; 6 chunks of up to 500
 // tokens behind 12,345 218 us.
-// Short prompts do not pay: behind 128 positions 64x3 take 54 us, spec_attend 32.
+// What is saved is reads, so it pays where the rows behind the first of their groups would
+// read some 65,000 common positions or more together, of 8 heads of 128.  In a graph, beside
+// spec_attend on the same rows: 64x3 behind 512, 1024 and 2048 positions 53, 53 and 64 us and
+// 41, 54 and 83; 8x3 behind 8192 and 16,384 53 and 62 us and 47 and 78; 16 groups of 8, 8 bits,
+// behind 512 and 1024 60 and 72 us and 60 and 80; two rows behind 32,768 (heads of 64) still 43
+// and 36.  Chunks of prompts are bound by their products, which are the same: 4 of up to
+// 500 tokens behind 16,384 185 us and 144.
 //
 // Common positions end with a multiple of 128, the larger tile of the kernels, so that
 // neither has a tile of both kinds; the up to 127 that are left go to each row.
