@@ -83,8 +83,6 @@ int attend_tile_rows(bool e4m3, long long rows) {
   return attend_is_wide(e4m3, rows) ? (rows <= 128 ? 128 : 256) : (rows <= 16 ? 16 : 32);
 }
 
-int attend_tile_positions(bool e4m3, long long rows) { return attend_is_wide(e4m3, rows) || e4m3 ? 128 : 64; }
-
 template <int PART>
 int attend_launch(AttendArgs& A, bool e4m3, long long rows, cudaStream_t st) {
   const bool wide = attend_is_wide(e4m3, rows);

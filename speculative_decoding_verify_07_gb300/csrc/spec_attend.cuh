@@ -352,10 +352,10 @@ inline int launch_early(Kernel kernel, unsigned ctas, int threads, int smem, cud
   return cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
 }
 
-// Whether items of up to `rows` query rows go to the many-rows kernel, and the query rows and the positions of a tile.
+// Whether items of up to `rows` query rows go to the many-rows kernel, and the query rows and the positions of a kernel's tile.
 bool attend_is_wide(bool e4m3, long long rows);
 int attend_tile_rows(bool e4m3, long long rows);
-int attend_tile_positions(bool e4m3, long long rows);
+constexpr int attend_tile_positions(bool wide, bool e4m3) { return wide || e4m3 ? 128 : 64; }
 
 // Either of them, for items of up to `rows` query rows.
 template <int PART>

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsShape<D, E4M3, MT>::ctas))
     attend_rows_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = RowsShape<D, E4M3, MT>;
   constexpr int M = S::M, KT = S::KT, NK = S::NK, NS = NK / 16;
+  static_assert(KT == attend_tile_positions(false, E4M3), "as the tiles are counted");
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) unsigned long long full[kRowsWarps][S::stages];
   // bits: positions of the stage that are there; whether values are NaN (1), scales above (2) or below (4) the ordinary

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     attend_wide_kernel(const AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = WideShape<D, E4M3, SPLIT>;
   constexpr int M = S::M, KT = kWideKT, KST = S::k_stages, VST = S::v_stages, QT = S::QT;
+  static_assert(KT == attend_tile_positions(true, E4M3), "as the tiles are counted");
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) WideBars bar;
   __shared__ unsigned there[8][4], v_there[8][4];      // which positions of the tile are there, for the last eight tiles

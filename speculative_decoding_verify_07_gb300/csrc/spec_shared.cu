@@ -204,7 +204,8 @@ extern "C" int spec_attend_shared(const uint16_t* q, int64_t token_stride, int N
   const long long common_rows = ((long long)N + groups - 1) / groups * group;
   A.common_rows = attend_tile_rows(e4m3, common_rows);
   attend_groups_kernel<<<1, kGroupThreads, 0, st>>>(A.C, N, shared_rows, shared_len, groups, group,
-                                                    log2_of(A.common_rows), log2_of(attend_tile_positions(e4m3, common_rows)), group_row,
+                                                    log2_of(A.common_rows),
+                                                    log2_of(attend_tile_positions(attend_is_wide(e4m3, common_rows), e4m3)), group_row,
                                                     group_cu, group_len, own_from);
   if (cudaGetLastError() != cudaSuccess) return SPEC_E_CUDA;
   A.common_tiles = (long long)N * group / A.common_rows + groups + 1;
